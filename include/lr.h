@@ -57,7 +57,8 @@ typedef enum {
   LR_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed */
   LR_ERR_TIMEOUT = 4,      /* device: a bounded wait ran out */
   LR_ERR_REMAP_RANGE = 5,  /* device: a remap entry outside the pool */
-  LR_ERR_STATE = 6         /* wrong object state (e.g. replaying a destroyed graph) */
+  LR_ERR_STATE = 6,        /* wrong object state (e.g. replaying a destroyed graph) */
+  LR_ERR_INDEX_RANGE = 7   /* device: a position, length or row offset outside its range */
 } lr_status;
 
 typedef enum { LR_BF16 = 0, LR_F32 = 1 } lr_dtype;
@@ -335,6 +336,152 @@ lr_status lr_linear_forward_rank_sharded(const void* x, int64_t ldx, void* y, in
  * multiple of 64, or n_shards outside [1, min(r, d_out)/64]. */
 lr_status lr_rank_shard_comm_bytes(int64_t M, int32_t d_out, int32_t r, int32_t n_shards,
                                    int32_t elem_bytes, int64_t* rank_space, int64_t* full_space);
+
+/* ---------------------------------------------------------------------------
+ * Attention over a context, for decoding with a full (reconstructed or
+ * ordinary) KV cache: the pages' block with a real attention core instead of
+ * the one-token context of lr_block_forward.  The cache is paged as the latent
+ * pool is: page b holds rows b * block_rows .. b * block_rows + block_rows - 1
+ * of the K and of the V pool, and a row holds one token's n_kv_heads heads of
+ * head_dim elements.  lr_kv_reconstruct_paged's output, with one page a list
+ * entry, is such a pool.
+ *   k, v: device bf16 [pool_blocks * block_rows][ld], 16-byte aligned, ld a
+ *   multiple of 8 and >= n_kv_heads * head_dim (both may point into one pool
+ *   of [K | V] rows).  pool_blocks * block_rows is at most 2^31 - 1; element
+ *   offsets are 64-bit. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t ld;
+  int64_t pool_blocks;
+  int32_t block_rows;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+} lr_kv_cache;
+
+/* How the heads of queries and keys are prepared, for a head x of head_dim
+ * elements at position p:
+ *   norm != 0:  x <- x * gain / sqrt(mean(x^2) + eps);  gain: device bf16
+ *               [head_dim], NULL for unit gain; q and k have their own.
+ *   rot_dim > 0: the pairs (a, b) of the first rot_dim elements turn by the
+ *               angles of p, (a, b) <- (a c - b s, b c + a s); pair i is
+ *               (x[i], x[i + rot_dim/2]) for LR_ROT_HALF and
+ *               (x[2i], x[2i+1]) for LR_ROT_PAIR; the other elements pass.
+ *   cos_sin: device fp32 [max_pos][rot_dim], 16-byte aligned: the rot_dim/2
+ *   cosines of a position, then the sines (lr_rope_table).
+ * The arithmetic is fp32; a result is rounded once, to bf16.
+ * head_dim: a multiple of 64, at most 256; rot_dim: a multiple of 16, at most
+ * head_dim (LR_ERR_UNSUPPORTED otherwise). */
+enum { LR_ROT_HALF = 0, LR_ROT_PAIR = 1 };
+typedef struct {
+  int32_t head_dim;
+  int32_t norm;
+  float eps;
+  const void* q_gain;
+  const void* k_gain;
+  int32_t rot_dim;
+  int32_t rot_style;
+  const float* cos_sin;
+  int64_t max_pos;
+} lr_head_map;
+
+/* lr_rope_table (host only): out[p][i] = cos(p f_i), out[p][rot_dim/2 + i] =
+ * sin(p f_i) with f_i = theta^(-2i/rot_dim), for p < max_pos; the angle and
+ * its functions are computed in 64 bits and rounded once to fp32.  out: host
+ * fp32 [max_pos][rot_dim].  rot_dim positive and even, theta > 0. */
+lr_status lr_rope_table(int64_t max_pos, int32_t rot_dim, double theta, float* out);
+
+/* lr_qk_norm_rope: norm and rotation of the heads of M rows of queries and
+ * keys in one pass (one launch).
+ *   q: device [M][ldq] of in_dtype (LR_BF16 or LR_F32), head h in columns
+ *   h * head_dim ..; k likewise with n_kv_heads heads; n_heads or n_kv_heads
+ *   may be 0 (its pointers are not read).  q_out, k_out: device bf16 [M][ldqo]
+ *   and [M][ldko].  A bf16 q_out may be q itself, with the same leading
+ *   dimension (k_out and k likewise); any other overlap is not allowed.
+ *   pos: device int32 [M], the rows' positions (not read when rot_dim is 0).
+ *   n_active: device int32 or NULL; rows m >= *n_active are neither read nor
+ *   written, so a captured call serves every batch up to M.
+ *   Pointers 16-byte aligned, leading dimensions multiples of 8 and at least
+ *   heads * head_dim.  A position outside [0, max_pos) gives a zero row and
+ *   LR_ERR_INDEX_RANGE in dev_status.  M = 0 is a no-op. */
+lr_status lr_qk_norm_rope(const void* q, int64_t ldq, int32_t n_heads, const void* k, int64_t ldk,
+                          int32_t n_kv_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
+                          const int32_t* n_active, const lr_head_map* hm, void* q_out, int64_t ldqo,
+                          void* k_out, int64_t ldko, int32_t* dev_status, lr_stream s);
+
+/* lr_kv_append: the new tokens' keys, normed and rotated as above, and their
+ * values, written to their rows of the paged cache:
+ *   cache.k[rows[m]] = heads(k[m]), cache.v[rows[m]] = bf16(v[m])  for m < M.
+ * With n_heads > 0 the tokens' queries are prepared in the same launch
+ * (q -> q_out, as lr_qk_norm_rope).  rows: device int32 [M] (remap_build with
+ * tail_rows = the new tokens of a sequence gives them); rows must be distinct.
+ * A row outside the pool is skipped and reported as LR_ERR_REMAP_RANGE; a
+ * position outside [0, max_pos) writes neither key nor value, gives a zero
+ * query row and reports LR_ERR_INDEX_RANGE.  Other pool rows are not touched.
+ * hm->head_dim must equal cache->head_dim; the other arguments and checks are
+ * those of lr_qk_norm_rope. */
+lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq,
+                       int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
+                       const int32_t* rows, const int32_t* n_active, const lr_head_map* hm,
+                       const lr_kv_cache* cache, void* q_out, int64_t ldqo, int32_t* dev_status, lr_stream s);
+
+/* lr_prefix_attention: attention of a batch whose sequences share a prefix.
+ * Sequence b has the shared tokens 0 .. *prefix_len - 1, kept once in the
+ * pages prefix_blocks, and lengths[b] own tokens after them in the pages of
+ * row b of block_table (own token t in entry t / block_rows).  Its query rows
+ * are rows q_start[b] .. q_start[b+1] - 1 of q: its last own tokens.  Row j of
+ * n sees the whole prefix and the own tokens t <= lengths[b] - n + j, and
+ *   out = sum_t softmax_t(scale q . k_t) v_t
+ * for each of n_heads heads (query head h reads kv head h / (n_heads /
+ * n_kv_heads)).  A row that sees no token comes out zero, and so does a row of
+ * q that belongs to no sequence.  Pool rows that hold no token of the batch
+ * (the ends of last pages among them) do not reach the result, whatever they
+ * hold.
+ *   q: device bf16 [M][ldq]; out: device [M][ldo] of out_dtype (LR_BF16 or
+ *   LR_F32); M < 2^31; 16-byte aligned, ldq and ldo multiples of 8 and >=
+ *   n_heads * head_dim.
+ *   prefix_blocks: device int32 [cap_prefix_blocks]; prefix_len: device int32
+ *   (both may be NULL when cap_prefix_blocks is 0: no shared part).
+ *   q_start: device int32 [n_seq + 1], not decreasing, within [0, M]; NULL
+ *   when every sequence has one row (M = n_seq then; M > n_seq leaves zero
+ *   rows).  max_q: the most rows that a sequence may have (1 for NULL).
+ *   block_table: device int32 [n_seq][blocks_per_seq]; lengths: device int32
+ *   [n_seq].
+ *   Lengths, pages and row offsets are read on the device: a captured call
+ *   serves every batch within the capacities.  A length outside its capacity
+ *   (block_rows times the pages it may use) is clamped and reported as
+ *   LR_ERR_INDEX_RANGE, as is a q_start outside [0, M], one that decreases, or
+ *   more than max_q rows (such a sequence's rows past max_q are unspecified).
+ *   A listed page outside [0, pool_blocks) reads as zeros and reports
+ *   LR_ERR_REMAP_RANGE.
+ *   head_dim 64 or 128; block_rows a multiple of 16; n_heads a multiple of
+ *   n_kv_heads with at most 64 query heads a kv head (LR_ERR_UNSUPPORTED
+ *   otherwise, LR_ERR_INVALID_ARG for a remainder); scale > 0 and finite.
+ *   workspace: device, 256-byte aligned, at least
+ *   lr_prefix_attention_workspace_bytes(M, d); contents on entry do not
+ *   matter; calls that share it must be ordered on one stream.
+ *   Scores, softmax statistics and sums are fp32; probabilities are rounded to
+ *   bf16 for the second product.  The result is deterministic.  M = 0 or
+ *   n_seq = 0 with M = 0 is a no-op. */
+typedef struct {
+  lr_kv_cache cache;
+  int32_t n_heads;
+  float scale;
+  const int32_t* prefix_blocks;
+  int32_t cap_prefix_blocks;
+  const int32_t* prefix_len;
+  int32_t n_seq;
+  const int32_t* q_start;
+  int32_t max_q;
+  const int32_t* block_table;
+  int32_t blocks_per_seq;
+  const int32_t* lengths;
+} lr_attn_desc;
+
+size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d);
+lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
+                              const lr_attn_desc* d, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                              lr_stream s);
 
 /* ---------------------------------------------------------------------------
  * A decode step of a layer stack over fixed buffers (English page section 2.C:

@@ -307,6 +307,82 @@ def kv_reconstruct_paged(latent_pool: np.ndarray, blocks, n_blocks: int, B: np.n
     return buf @ np.asarray(B, dtype=np.float64), bad
 
 
+# ---------------------------------------------- attention over a context
+def rope_angles(positions, rot_dim: int, theta: float = 10000.0) -> np.ndarray:
+    """fp64 angles [n][rot_dim / 2] of the given positions: p * theta^(-2 i / rot_dim)."""
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    return np.asarray(positions, dtype=np.float64)[:, None] * theta ** (-2.0 * i / rot_dim)
+
+
+def map_heads(x, head_dim: int, gain, eps: float, cos, sin, style: str) -> np.ndarray:
+    """Heads of x [n][heads * head_dim]: RMS norm (gain None: no norm), then rotation by cos, sin [n][rot / 2].
+
+    style "half" turns the pairs (i, i + rot/2), "pair" the pairs (2i, 2i + 1),
+    each as the complex number a + ib times cos + i sin; the elements past rot pass.
+    """
+    n = x.shape[0]
+    y = np.array(x, dtype=np.float64).reshape(n, -1, head_dim)
+    if gain is not None:
+        y = y / np.sqrt(np.mean(y * y, axis=-1, keepdims=True) + eps) * np.asarray(gain, dtype=np.float64)
+    half = cos.shape[1]
+    i = np.arange(half)
+    a, b = (i, i + half) if style == "half" else (2 * i, 2 * i + 1)
+    z = (y[..., a] + 1j * y[..., b]) * (cos + 1j * sin)[:, None, :]
+    y[..., a], y[..., b] = z.real, z.imag
+    return y.reshape(n, -1)
+
+
+def context_attention(q, keys, values, visible, scale: float):
+    """One head: softmax(scale q keys^T) values with row j seeing the keys t < visible[j].
+
+    q [n][d], keys and values [T][d].  A row that sees nothing is zero.  Returns
+    (out, sum_t p_t |v_t|): the second bounds what rounding the probabilities can do.
+    """
+    q, keys, values = (np.asarray(t, dtype=np.float64) for t in (q, keys, values))
+    out, mag = np.zeros_like(q), np.zeros_like(q)
+    for j, n in enumerate(visible):
+        n = max(0, min(int(n), keys.shape[0]))
+        if n == 0:
+            continue
+        s = scale * (keys[:n] @ q[j])
+        p = np.exp(s - s.max())
+        p /= p.sum()
+        out[j], mag[j] = p @ values[:n], p @ np.abs(values[:n])
+    return out, mag
+
+
+def prefix_attention(q, k_pool, v_pool, n_heads: int, n_kv: int, head_dim: int, block_rows: int, prefix_blocks,
+                     prefix_len: int, block_table, lengths, q_start, scale: float):
+    """Attention of a batch over a shared prefix and each sequence's own tokens, all in paged pools (fp64).
+
+    Row q_start[b] + j of n sees the prefix and the own tokens t <= lengths[b] - n + j.
+    Pages outside the pool read as zeros.  Returns (out, sum p |v|), zero for rows of no sequence.
+    """
+    rows = k_pool.shape[0]
+
+    def take(pool, pages, n):
+        at = np.asarray([int(pages[t // block_rows]) * block_rows + t % block_rows
+                         if 0 <= int(pages[t // block_rows]) < rows // block_rows else -1 for t in range(n)], dtype=np.int64)
+        x = np.zeros((n, n_kv * head_dim))
+        if n:
+            x[at >= 0] = pool[at[at >= 0], : n_kv * head_dim]
+        return x
+
+    group = n_heads // n_kv
+    out, mag = np.zeros(q.shape), np.zeros(q.shape)
+    kp, vp = take(k_pool, prefix_blocks, prefix_len), take(v_pool, prefix_blocks, prefix_len)
+    for b in range(len(lengths)):
+        L, r0, r1 = int(lengths[b]), int(q_start[b]), int(q_start[b + 1])
+        n = r1 - r0
+        keys = np.concatenate([kp, take(k_pool, block_table[b], L)])
+        vals = np.concatenate([vp, take(v_pool, block_table[b], L)])
+        visible = [prefix_len + max(0, L - n + j + 1) for j in range(n)]
+        for h in range(n_heads):
+            c, d = slice(h * head_dim, (h + 1) * head_dim), slice(h // group * head_dim, (h // group + 1) * head_dim)
+            out[r0:r1, c], mag[r0:r1, c] = context_attention(q[r0:r1, c], keys[:, d], vals[:, d], visible, scale)
+    return out, mag
+
+
 # ------------------------------------------------------ rank-space sharding
 def shard_columns(n: int, G: int):
     """Split n columns (a multiple of 64) over G processes in whole 64-column blocks.

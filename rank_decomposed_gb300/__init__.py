@@ -25,6 +25,7 @@ LR_ERR_CUDA = 3
 LR_ERR_TIMEOUT = 4
 LR_ERR_REMAP_RANGE = 5
 LR_ERR_STATE = 6
+LR_ERR_INDEX_RANGE = 7
 LR_BF16 = 0
 LR_F32 = 1
 PROJ = ("q", "k", "v", "o", "gate", "up", "down")
@@ -62,6 +63,29 @@ class StackDesc(ctypes.Structure):
                 ("dev_status", ctypes.c_void_p), ("mode", ctypes.c_int32)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("pool_blocks", ctypes.c_int64), ("block_rows", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class HeadMapDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("q_gain", ctypes.c_void_p), ("k_gain", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("rot_style", ctypes.c_int32), ("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int64)]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("cache", KvCache), ("n_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("prefix_blocks", ctypes.c_void_p), ("cap_prefix_blocks", ctypes.c_int32),
+                ("prefix_len", ctypes.c_void_p), ("n_seq", ctypes.c_int32), ("q_start", ctypes.c_void_p),
+                ("max_q", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("blocks_per_seq", ctypes.c_int32), ("lengths", ctypes.c_void_p)]
+
+
+ROT_HALF = 0
+ROT_PAIR = 1
+
 STACK_AUTO = 0
 STACK_LAYERED = 1
 
@@ -91,6 +115,13 @@ def _load():
         "lr_linear_forward_rank_sharded": (i32, [vp, i64, vp, i64, i32, i64, P(Factor), i32, vp, sz,
                                                  vp, vp]),
         "lr_rank_shard_comm_bytes": (i32, [i64, i32, i32, i32, i32, P(i64), P(i64)]),
+        "lr_rope_table": (i32, [i64, i32, ctypes.c_double, vp]),
+        "lr_qk_norm_rope": (i32, [vp, i64, i32, vp, i64, i32, i32, i64, vp, vp, P(HeadMapDesc), vp, i64, vp, i64,
+                                  vp, vp]),
+        "lr_kv_append": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i64, vp, vp, vp, P(HeadMapDesc), P(KvCache),
+                               vp, i64, vp, vp]),
+        "lr_prefix_attention_workspace_bytes": (sz, [i64, P(AttnDesc)]),
+        "lr_prefix_attention": (i32, [vp, i64, vp, i64, i32, i64, P(AttnDesc), vp, sz, vp, vp]),
         "lr_stack_forward": (i32, [P(StackDesc), vp]),
         "lr_graph_capture": (i32, [P(StackDesc), P(vp)]),
         "lr_graph_replay": (i32, [vp, vp]),
@@ -401,6 +432,198 @@ def kv_reconstruct_paged(latent_pool, blocks, n_blocks, Bt, out, status, stream=
                                      n_blocks.data_ptr(), blocks.shape[0], Bt.data_ptr(), Bt.shape[0],
                                      out.data_ptr(), _ptr(status), _stream(stream))
     _check("lr_kv_reconstruct_paged", st)
+
+
+# ------------------------------------------------- attention over a context
+def _i32(t, name, dims=1):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous %d-D int32 tensor" % (name, dims))
+    return t.data_ptr()
+
+
+def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0):
+    """Host table fp32 [max_pos][rot_dim] of a rotation's cosines, then sines (64-bit angles)."""
+    if max_pos < 0 or rot_dim < 0:
+        raise ValueError("rope_table: negative size")
+    out = np.empty((max_pos, rot_dim), dtype=np.float32)
+    _check("lr_rope_table", lib.lr_rope_table(max_pos, rot_dim, theta, out.ctypes.data))
+    return out
+
+
+@dataclass
+class HeadMap:
+    """How heads of queries and keys are prepared: RMS norm (gains bf16 [head_dim] or None), then rotation."""
+    head_dim: int
+    norm: bool = False
+    eps: float = 1e-6
+    q_gain: object = None
+    k_gain: object = None
+    rot_dim: int = 0
+    rot_style: int = ROT_HALF
+    cos_sin: object = None   # device fp32 [max_pos][rot_dim], see rope_table
+
+    def c(self) -> HeadMapDesc:
+        import torch
+        for name, g in (("q_gain", self.q_gain), ("k_gain", self.k_gain)):
+            if g is not None and (g.dtype != torch.bfloat16 or tuple(g.shape) != (self.head_dim,)
+                                  or not g.is_contiguous()):
+                raise TypeError("%s must be a contiguous bfloat16 [head_dim] tensor" % name)
+        d = HeadMapDesc(self.head_dim, 1 if self.norm else 0, self.eps, _ptr(self.q_gain), _ptr(self.k_gain),
+                        self.rot_dim, self.rot_style, None, 0)
+        if self.rot_dim > 0 and self.cos_sin is not None:
+            t = self.cos_sin
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != self.rot_dim or not t.is_contiguous():
+                raise TypeError("cos_sin must be a contiguous float32 [max_pos][rot_dim] tensor")
+            d.cos_sin, d.max_pos = t.data_ptr(), t.shape[0]
+        return d
+
+
+@dataclass
+class PagedKV:
+    """A paged cache: K and V pools bf16 [pages * block_rows][>= n_kv_heads * head_dim] on the device."""
+    k_pool: object
+    v_pool: object
+    n_kv_heads: int
+    head_dim: int
+    block_rows: int = 16
+
+    def c(self) -> KvCache:
+        _bf16(self.k_pool, "k_pool")
+        _bf16(self.v_pool, "v_pool")
+        if self.k_pool.shape != self.v_pool.shape or self.k_pool.stride(0) != self.v_pool.stride(0):
+            raise ValueError("k_pool and v_pool must have one shape and row stride")
+        if self.k_pool.shape[1] < self.n_kv_heads * self.head_dim:
+            raise ValueError("the pools' rows are narrower than n_kv_heads * head_dim")
+        if self.block_rows <= 0 or self.k_pool.shape[0] % self.block_rows:
+            raise ValueError("the pools' rows must be whole pages of block_rows")
+        return KvCache(self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.k_pool.stride(0),
+                       self.k_pool.shape[0] // self.block_rows, self.block_rows, self.n_kv_heads, self.head_dim)
+
+
+def _ld(t):
+    """Row stride; one row's stride says nothing, so it counts as at least its width."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def _rows_in(named, head_dim):
+    """(dtype code, row count) of the given [M][heads * head_dim] inputs, which must agree."""
+    import torch
+    first = None
+    for name, t in named:
+        if t is None:
+            continue
+        if t.dim() != 2 or t.stride(1) != 1:
+            raise ValueError("%s must be a row-major 2-D tensor" % name)
+        if head_dim <= 0 or t.shape[1] % head_dim:
+            raise ValueError("%s: the width is not whole heads of head_dim" % name)
+        if first is None:
+            first = t
+        elif t.dtype != first.dtype or t.shape[0] != first.shape[0]:
+            raise ValueError("%s: inputs disagree on dtype or rows" % name)
+    if first is None:
+        raise ValueError("no input given")
+    code = {torch.bfloat16: LR_BF16, torch.float32: LR_F32}.get(first.dtype)
+    if code is None:
+        raise TypeError("inputs must be bfloat16 or float32")
+    return code, first.shape[0]
+
+
+def _head_out(x, out, name):
+    if x is None:
+        return None, 0, 0, None, 0
+    if out is None:
+        raise ValueError("%s is missing" % name)
+    _bf16(out, name)
+    if out.shape != x.shape:
+        raise ValueError("%s must have its input's shape" % name)
+    return x.data_ptr(), _ld(x), x.shape[1], out.data_ptr(), _ld(out)
+
+
+def _per_row(t, name, m):
+    p = _i32(t, name)
+    if t is not None and t.shape[0] != m:
+        raise ValueError("%s must have one entry a row" % name)
+    return p
+
+
+def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None, stream=None):
+    """Norm and rotation of the heads of q and k (either may be None) into bf16 q_out and k_out, one launch.
+
+    In place (q_out is q, k_out is k) is allowed for bf16 inputs.
+    """
+    code, m = _rows_in((("q", q), ("k", k)), heads.head_dim)
+    qp, ldq, wq, qo, ldqo = _head_out(q, q_out, "q_out")
+    kp, ldk, wk, ko, ldko = _head_out(k, k_out, "k_out")
+    hm = heads.c()
+    st = lib.lr_qk_norm_rope(qp, ldq, wq // heads.head_dim, kp, ldk, wk // heads.head_dim, code, m,
+                             _per_row(pos, "pos", m), _i32(n_active, "n_active"), ctypes.byref(hm), qo, ldqo, ko,
+                             ldko, _ptr(status), _stream(stream))
+    _check("lr_qk_norm_rope", st)
+
+
+def kv_append(k, v, pos, rows, heads: HeadMap, cache: PagedKV, status, q=None, q_out=None, n_active=None,
+              stream=None):
+    """cache rows rows[m] = (norm and rotation of k[m], v[m]); with q also q_out as qk_norm_rope. One launch."""
+    code, m = _rows_in((("k", k), ("v", v), ("q", q)), heads.head_dim)
+    width = cache.n_kv_heads * cache.head_dim
+    if k.shape[1] != width or v.shape[1] != width:
+        raise ValueError("k and v must be [M][n_kv_heads * head_dim]")
+    qp, ldq, wq, qo, ldqo = _head_out(q, q_out, "q_out")
+    hm, cc = heads.c(), cache.c()
+    st = lib.lr_kv_append(k.data_ptr(), _ld(k), v.data_ptr(), _ld(v), qp, ldq, wq // heads.head_dim, code,
+                          m, _per_row(pos, "pos", m), _per_row(rows, "rows", m), _i32(n_active, "n_active"),
+                          ctypes.byref(hm), ctypes.byref(cc), qo, ldqo, _ptr(status), _stream(stream))
+    _check("lr_kv_append", st)
+
+
+def _attn_desc(M, n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale):
+    d = AttnDesc()
+    d.cache = cache.c()
+    d.n_heads = n_heads
+    d.scale = cache.head_dim ** -0.5 if scale is None else scale
+    d.prefix_blocks, d.prefix_len = _i32(prefix_blocks, "prefix_blocks"), _i32(prefix_len, "prefix_len")
+    d.cap_prefix_blocks = 0 if prefix_blocks is None else prefix_blocks.shape[0]
+    d.lengths, d.n_seq = _i32(lengths, "lengths"), lengths.shape[0]
+    d.block_table, d.blocks_per_seq = _i32(block_table, "block_table", 2), block_table.shape[1]
+    if block_table.shape[0] != lengths.shape[0]:
+        raise ValueError("block_table must be [n_seq][blocks_per_seq]")
+    d.q_start, d.max_q = _i32(q_start, "q_start"), max_q
+    if q_start is not None and q_start.shape[0] != lengths.shape[0] + 1:
+        raise ValueError("q_start must have n_seq + 1 entries")
+    return d
+
+
+def prefix_attention_workspace_bytes(M: int, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len, block_table,
+                                     lengths, q_start=None, max_q: int = 1) -> int:
+    d = _attn_desc(M, n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, None)
+    return int(lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(d)))
+
+
+def prefix_attention(q, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len, block_table, lengths, out, workspace,
+                     status, q_start=None, max_q: int = 1, scale=None, stream=None):
+    """Attention of q's rows over a shared prefix (or none: None) and each sequence's own paged tokens.
+
+    q: bf16 [M][n_heads * head_dim]; out: bf16 or fp32, the same shape.  Sequence b's rows are
+    q_start[b]..q_start[b + 1] - 1 (row b without q_start), its last own tokens.
+    """
+    import torch
+    _bf16(q, "q")
+    if out.dim() != 2 or out.stride(1) != 1 or out.shape != q.shape:
+        raise ValueError("out must be a row-major tensor of q's shape")
+    if q.shape[1] != n_heads * cache.head_dim:
+        raise ValueError("q must be [M][n_heads * head_dim]")
+    odt = {torch.bfloat16: LR_BF16, torch.float32: LR_F32}.get(out.dtype)
+    if odt is None:
+        raise TypeError("out must be bfloat16 or float32")
+    d = _attn_desc(q.shape[0], n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale)
+    st = lib.lr_prefix_attention(q.data_ptr(), _ld(q), out.data_ptr(), _ld(out), odt, q.shape[0],
+                                 ctypes.byref(d), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                 _ptr(status), _stream(stream))
+    _check("lr_prefix_attention", st)
 
 
 # ---------------------------------------------------------------- stack

@@ -13,6 +13,7 @@
 #include <mutex>
 #include <vector>
 
+#include "lr_attn.h"
 #include "lr_internal.h"
 
 namespace lr {
@@ -169,6 +170,8 @@ lr_status ensure_configured() {
   st = configure_prefill();
   if (st != LR_OK) return st;
   st = configure_prefill_pair();
+  if (st != LR_OK) return st;
+  st = configure_attn();
   if (st != LR_OK) return st;
   done[dev] = true;
   return LR_OK;
@@ -567,6 +570,7 @@ const char* lr_status_string(lr_status st) {
     case LR_ERR_TIMEOUT: return "device wait timed out";
     case LR_ERR_REMAP_RANGE: return "remap entry outside the pool";
     case LR_ERR_STATE: return "bad object state";
+    case LR_ERR_INDEX_RANGE: return "position, length or row offset outside its range";
   }
   return "unknown status";
 }

@@ -1,0 +1,568 @@
+// Attention of a batch that shares a prefix: entry point, the kernel for few
+// query rows, and the join of partial results.
+//
+// For a query row with visible keys t in parts i (the shared prefix and the
+// sequence's own tokens, each cut along the keys):
+//   m_i = max_t s_t,  l_i = sum_t 2^(s_t - m_i),  o_i = sum_t 2^(s_t - m_i) v_t,
+//   out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i,
+// with s_t = scale log2(e) q . k_t.  The prefix is read for all rows of the
+// batch at once, whichever sequences they belong to: M * group rows a key head
+// share each key, where a sequence's own keys serve only its own rows.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "lr_attn.h"
+#include "lr_ptx.cuh"
+
+namespace lr {
+namespace {
+
+// ------------------------------------------------------- rows kernel
+// Few query rows against many keys: bound by the bytes of K and V.  A CTA takes
+// 16 rows (query rows times the heads of one key head) and a range of keys;
+// each of its four warps walks chunks of 16 keys (they never cross a page) on
+// its own: a ring of chunks filled by 16-byte asynchronous copies, S = Q K^T
+// and O += P V by m16n8k16 products with Q and O in registers, and its own
+// running maximum and sum, so no warp waits for another until the end, where
+// the four join through shared memory.
+constexpr int kRowsWarps = 4;
+constexpr int kRowsTile = 16;
+constexpr int kRowsChunk = 16;
+constexpr int kRowsStages = 3;
+
+template <int HD>
+constexpr int rows_smem() {
+  return kRowsWarps * kRowsStages * kRowsChunk * HD * 2 * 2;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return static_cast<uint32_t>(f32_to_bf16_rn(lo)) | (static_cast<uint32_t>(f32_to_bf16_rn(hi)) << 16);
+}
+
+// Byte offset of 16-byte column c of row r in a [16][HD] tile: columns are
+// permuted by the row, so that the eight rows of a matrix load lie in
+// different banks.
+template <int HD>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return static_cast<uint32_t>(r * HD * 2 + ((c ^ (r & 7)) << 4));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kRowsWarps * 32)
+    attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPart part, int tiles) {
+  constexpr int kC16 = HD / 8;  // 16-byte columns of a row
+  extern __shared__ __align__(128) uint8_t sm[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kvh = blockIdx.y;
+  const int split = blockIdx.z;
+  const int G = p.group;
+
+  // This CTA's rows: r = (query row - q0) * G + head in the group.
+  int q0, n_rows, row0, len, nq;
+  const int32_t* pages;
+  const bool tell = kvh == 0 && threadIdx.x == 0 && split == 0;
+  if (part.prefix) {
+    q0 = 0;
+    nq = p.M;
+    len = prefix_view(p, tell);
+    pages = p.prefix_blocks;
+    row0 = blockIdx.x * kRowsTile;
+  } else {
+    const int b = blockIdx.x / tiles;
+    const SeqView v = seq_view(p, b, tell);
+    q0 = v.q0;
+    nq = v.nq;
+    len = v.len;
+    pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
+    row0 = (blockIdx.x % tiles) * kRowsTile;
+  }
+  n_rows = nq * G - row0;
+  if (n_rows <= 0) return;
+  if (n_rows > kRowsTile) n_rows = kRowsTile;
+
+  // Visible keys: all of the prefix; own tokens up to a row's own.
+  const int r_lo = lane >> 2;  // this lane's two rows in the tile: r_lo, r_lo + 8
+  int vis[2];
+  int kmax = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = row0 + r_lo + 8 * i;
+    vis[i] = part.prefix ? len : len - nq + r / G + 1;
+  }
+  kmax = part.prefix ? len : len - nq + (row0 + n_rows - 1) / G + 1;
+  if (kmax < 0) kmax = 0;
+  const int all_chunks = (kmax + kRowsChunk - 1) / kRowsChunk;
+  const int per = (all_chunks + part.slots - 1) / part.slots;
+  const int c_lo = split * per;
+  const int c_hi = c_lo + per < all_chunks ? c_lo + per : all_chunks;
+
+  // Q in the A layout of m16n8k16.
+  uint32_t qa[HD / 16][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int rr = r_lo + 8 * i;
+    const int r = row0 + rr;
+    const bool live = rr < n_rows;
+    const uint16_t* src = p.q + static_cast<int64_t>(q0 + r / G) * p.ldq + static_cast<int64_t>(kvh * G + r % G) * HD;
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk) {
+      const int col = kk * 16 + (lane & 3) * 2;
+      qa[kk][i] = live ? *reinterpret_cast<const uint32_t*>(src + col) : 0u;
+      qa[kk][i + 2] = live ? *reinterpret_cast<const uint32_t*>(src + col + 8) : 0u;
+    }
+  }
+
+  float o[HD / 8][4];
+#pragma unroll
+  for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+  float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+
+  // Ring of this warp: stage s holds K [16][HD] then V [16][HD].
+  constexpr uint32_t kTile = kRowsChunk * HD * 2;
+  const uint32_t ring = smem_u32(sm) + warp * kRowsStages * 2 * kTile;
+  const int mine = c_hi - c_lo > warp ? (c_hi - c_lo - warp + kRowsWarps - 1) / kRowsWarps : 0;
+  int ids = 0;  // lane i: page of this warp's chunk i of the current 32
+  auto page_of = [&](int i) {
+    if ((i & 31) == 0) {
+      const int c = c_lo + warp + (i + lane) * kRowsWarps;
+      ids = i + lane < mine ? pages[c * kRowsChunk / p.block_rows] : -1;
+      if (i + lane < mine && (ids < 0 || ids >= p.pool_blocks)) {
+        report_status(p.status, LR_ERR_REMAP_RANGE);
+        ids = -1;
+      }
+    }
+    return __shfl_sync(0xffffffffu, ids, i & 31);
+  };
+  const uint16_t* kh = p.k + static_cast<int64_t>(kvh) * HD;
+  const uint16_t* vh = p.v + static_cast<int64_t>(kvh) * HD;
+  auto issue = [&](int i) {
+    if (i < mine) {
+      const int c = c_lo + warp + i * kRowsWarps;
+      const int page = page_of(i);
+      const int t0 = c * kRowsChunk;
+      const int64_t row = static_cast<int64_t>(page < 0 ? 0 : page) * p.block_rows + t0 % p.block_rows;
+      const uint32_t st = ring + (i % kRowsStages) * 2 * kTile;
+#pragma unroll
+      for (int j = 0; j < kC16 / 2; ++j) {  // 16 rows * kC16 columns by 32 lanes
+        const int idx = j * 32 + lane;
+        const int r = idx / kC16, col = idx % kC16;
+        const bool live = page >= 0 && t0 + r < kmax;
+        const int64_t off = live ? (row + r) * p.ld + col * 8 : 0;
+        cp16(st + swz<HD>(r, col), kh + off, live);
+        cp16(st + kTile + swz<HD>(r, col), vh + off, live);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRowsStages - 1; ++i) issue(i);
+
+  for (int i = 0; i < mine; ++i) {
+    issue(i + kRowsStages - 1);
+    cp_wait<kRowsStages - 1>();
+    __syncwarp();
+    const uint32_t st = ring + (i % kRowsStages) * 2 * kTile;
+    const int t0 = (c_lo + warp + i * kRowsWarps) * kRowsChunk;
+    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    {
+      const int r = (lane & 7) + ((lane & 16) >> 1), cc = (lane >> 3) & 1;
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        uint32_t b0, b1, b2, b3;  // keys 0-7: k 0-7, 8-15; keys 8-15: the same
+        ldsm4(st + swz<HD>(r, kk * 2 + cc), b0, b1, b2, b3);
+        mma16816(s[0], qa[kk], b0, b1);
+        mma16816(s[1], qa[kk], b2, b3);
+      }
+    }
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + n * 8 + (lane & 3) * 2 + (j & 1);
+        s[n][j] = t < vis[j >> 1] ? s[n][j] * p.scale_log2 : -INFINITY;
+        top[j >> 1] = fmaxf(top[j >> 1], s[n][j]);
+      }
+    float ref[2], fac[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+      top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+      const float now = fmaxf(mx[k], top[k]);
+      ref[k] = now == -INFINITY ? 0.f : now;  // nothing visible yet: every power is 2^-inf = 0
+      fac[k] = exp2f(mx[k] - ref[k]);
+      mx[k] = now;
+    }
+    if (__any_sync(0xffffffffu, fac[0] != 1.f || fac[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < HD / 8; ++n) {
+        o[n][0] *= fac[0], o[n][1] *= fac[0];
+        o[n][2] *= fac[1], o[n][3] *= fac[1];
+      }
+      sum[0] *= fac[0], sum[1] *= fac[1];
+    }
+    uint32_t pa[4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[n][j] = exp2f(s[n][j] - ref[j >> 1]);
+        sum[j >> 1] += s[n][j];
+      }
+      // the accumulators' layout is that of the next product's A operand; the
+      // product takes bf16, so the probabilities round here (the sum does not)
+      pa[n * 2] = pack_bf16(s[n][0], s[n][1]);
+      pa[n * 2 + 1] = pack_bf16(s[n][2], s[n][3]);
+    }
+    {
+      const int r = lane & 15, cc = lane >> 4;
+#pragma unroll
+      for (int n = 0; n < HD / 16; ++n) {
+        uint32_t b0, b1, b2, b3;  // columns 0-7: keys 0-7, 8-15; columns 8-15: the same
+        ldsm4t(st + kTile + swz<HD>(r, n * 2 + cc), b0, b1, b2, b3);
+        mma16816(o[2 * n], pa, b0, b1);
+        mma16816(o[2 * n + 1], pa, b2, b3);
+      }
+    }
+    __syncwarp();
+  }
+  cp_wait<0>();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+    sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+  }
+
+  // Join the four warps: numerators in the ring's space, [warp][16][HD].
+  __shared__ float2 ml[kRowsWarps][kRowsTile];
+  __syncthreads();
+  float* jo = reinterpret_cast<float*>(sm) + warp * kRowsTile * HD;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r_lo + 8 * i;
+    if ((lane & 3) == 0) ml[warp][r] = make_float2(mx[i], sum[i]);
+#pragma unroll
+    for (int n = 0; n < HD / 8; ++n)
+      *reinterpret_cast<float2*>(jo + r * HD + n * 8 + (lane & 3) * 2) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+  }
+  __syncthreads();
+  const int64_t slot_rows = static_cast<int64_t>(p.M) * p.n_heads;
+  const int64_t base = (part.slot0 + split) * slot_rows;
+  for (int idx = threadIdx.x; idx < n_rows * (HD / 4); idx += kRowsWarps * 32) {
+    const int rr = idx / (HD / 4), c = idx % (HD / 4);
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) m = fmaxf(m, ml[w][rr].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) {
+      const float f = exp2f(ml[w][rr].x - ref);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm) + (w * kRowsTile + rr) * HD + c * 4);
+      l += f * ml[w][rr].y;
+      acc.x += f * x.x, acc.y += f * x.y, acc.z += f * x.z, acc.w += f * x.w;
+    }
+    const int r = row0 + rr;
+    const int64_t at = base + static_cast<int64_t>(q0 + r / G) * p.n_heads + kvh * G + r % G;
+    *reinterpret_cast<float4*>(p.po + at * HD + c * 4) = acc;
+    if (c == 0) p.pml[at] = make_float2(m, l);
+  }
+}
+
+// --------------------------------------------------------------- join
+// One warp per (row, head): the slots' numerators with their weights.  Bound
+// by the partial results, which were written just before and lie in L2.
+template <int HD>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
+  constexpr int kE = HD / 32;  // elements per lane
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(p.M) * p.n_heads;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int m = static_cast<int>(r / p.n_heads), h = static_cast<int>(r - static_cast<int64_t>(m) * p.n_heads);
+  int from = 0, to = p.n_seq;
+  if (p.q_start != nullptr) {
+    from = p.q_start[0];
+    to = p.n_seq > 0 ? p.q_start[p.n_seq] : from;
+  }
+  float acc[kE];
+#pragma unroll
+  for (int j = 0; j < kE; ++j) acc[j] = 0.f;
+  if (m >= from && m < to) {
+    const int slots = p.prefix_slots + p.own_slots;
+    float top = -INFINITY;
+    for (int i = 0; i < slots; ++i) top = fmaxf(top, p.pml[i * rows + r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    for (int i = 0; i < slots; ++i) {
+      const float2 ml = p.pml[i * rows + r];
+      if (ml.y == 0.f) continue;
+      const float f = exp2f(ml.x - ref);
+      l += f * ml.y;
+      const float* src = p.po + (i * rows + r) * HD + lane * kE;
+      if (kE == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] += f * x.x, acc[1] += f * x.y, acc[kE - 2] += f * x.z, acc[kE - 1] += f * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] += f * x.x, acc[1] += f * x.y;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
+#pragma unroll
+    for (int j = 0; j < kE; ++j) acc[j] *= inv;
+  }
+  const int64_t off = static_cast<int64_t>(m) * p.ldo + static_cast<int64_t>(h) * HD + lane * kE;
+  if (p.out_f32) {
+    float* dst = static_cast<float*>(p.out) + off;
+#pragma unroll
+    for (int j = 0; j < kE; j += 2) *reinterpret_cast<float2*>(dst + j) = make_float2(acc[j], acc[j + 1]);
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + off);
+#pragma unroll
+    for (int j = 0; j < kE; j += 2) dst[j / 2] = pack_bf16(acc[j], acc[j + 1]);
+  }
+}
+
+template <typename... KArgs, typename... Args>
+lr_status launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const char* what,
+                 Args... args) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (pdl_enabled()) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return LR_OK;
+}
+
+lr_status bad(lr_status st, const char* fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  set_error("%s", msg);
+  return st;
+}
+
+// How a call is cut, from its capacities alone (lengths are on the device).
+struct AttnPlan {
+  int32_t prefix_slots, own_slots;
+  size_t ml_off, bytes;
+};
+
+int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Key ranges per row tile: enough CTAs for two waves of the GPU's slots, each
+// of at least 128 keys.
+int slots_for(int64_t ctas, int64_t keys) {
+  if (keys <= 0) return 0;
+  const int64_t want = static_cast<int64_t>(num_sms()) * 4;
+  int64_t n = ctas >= want ? 1 : want / ctas;
+  const int64_t most = cdiv(keys, 128);
+  if (n > most) n = most;
+  if (n > 64) n = 64;
+  return static_cast<int>(n);
+}
+
+// No sequence has more rows than the call.
+int64_t most_q(int64_t M, const lr_attn_desc* d) { return d->max_q < M ? d->max_q : (M < 1 ? 1 : M); }
+
+AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
+  AttnPlan a;
+  const int G = d->n_heads / d->cache.n_kv_heads;
+  const int64_t kv = d->cache.n_kv_heads;
+  a.prefix_slots = slots_for(cdiv(M * G, kRowsTile) * kv, static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows);
+  a.own_slots = slots_for(static_cast<int64_t>(d->n_seq) * cdiv(most_q(M, d) * G, kRowsTile) * kv,
+                          static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows);
+  const size_t rows = static_cast<size_t>(M) * d->n_heads * (a.prefix_slots + a.own_slots);
+  a.ml_off = (rows * d->cache.head_dim * 4 + 255) / 256 * 256;
+  a.bytes = a.ml_off + (rows * 8 + 255) / 256 * 256;
+  return a;
+}
+
+lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
+  if (d == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null descriptor", who);
+  lr_status st = check_kv_cache(who, &d->cache);
+  if (st != LR_OK) return st;
+  const lr_kv_cache& c = d->cache;
+  if (M < 0 || M > 0x7FFFFFFF) return bad(LR_ERR_INVALID_ARG, "%s: bad M", who);
+  if (d->n_heads <= 0 || d->n_heads % c.n_kv_heads)
+    return bad(LR_ERR_INVALID_ARG, "%s: n_heads must be a positive multiple of n_kv_heads", who);
+  if (c.head_dim != 64 && c.head_dim != 128)
+    return bad(LR_ERR_UNSUPPORTED, "%s: head_dim %d is neither 64 nor 128", who, c.head_dim);
+  if (c.block_rows % 16) return bad(LR_ERR_UNSUPPORTED, "%s: block_rows %d is not a multiple of 16", who, c.block_rows);
+  if (d->n_heads / c.n_kv_heads > 64)
+    return bad(LR_ERR_UNSUPPORTED, "%s: more than 64 query heads a key head", who);
+  if (c.n_kv_heads > 65535) return bad(LR_ERR_UNSUPPORTED, "%s: more than 65535 key heads", who);
+  if (!(d->scale > 0.f) || std::isinf(d->scale)) return bad(LR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  if (d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
+    return bad(LR_ERR_INVALID_ARG, "%s: negative size", who);
+  if (static_cast<int64_t>(d->cap_prefix_blocks) * c.block_rows > 0x7FFFFF00 ||
+      static_cast<int64_t>(d->blocks_per_seq) * c.block_rows > 0x7FFFFF00)
+    return bad(LR_ERR_INVALID_ARG, "%s: a context's rows overflow int32", who);
+  if (d->cap_prefix_blocks > 0 && (!d->prefix_blocks || !d->prefix_len))
+    return bad(LR_ERR_INVALID_ARG, "%s: null prefix", who);
+  if (d->n_seq > 0 && (!d->lengths || (d->blocks_per_seq > 0 && !d->block_table)))
+    return bad(LR_ERR_INVALID_ARG, "%s: null lengths or block table", who);
+  if (d->q_start == nullptr ? (d->max_q != 1 || M < d->n_seq) : (d->max_q < 1))
+    return bad(LR_ERR_INVALID_ARG, "%s: max_q must be at least 1, and 1 with a row for each sequence without q_start", who);
+  if (M * d->n_heads > 0x7FFFFFFF ||
+      cdiv(most_q(M, d) * (d->n_heads / c.n_kv_heads), kRowsTile) * static_cast<int64_t>(d->n_seq) > 0x7FFFFFFF)
+    return bad(LR_ERR_UNSUPPORTED, "%s: too many rows for one launch", who);
+  return LR_OK;
+}
+
+}  // namespace
+
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s) {
+  const int tiles = cdiv(static_cast<int64_t>(part.prefix ? p.M : p.max_q) * p.group, kRowsTile);
+  const dim3 grid(part.prefix ? tiles : tiles * p.n_seq, p.n_kv, part.slots);
+  if (head_dim == 64)
+    return launch(attn_rows_kernel<64>, grid, dim3(kRowsWarps * 32), rows_smem<64>(), s, "attn_rows", p, part, tiles);
+  return launch(attn_rows_kernel<128>, grid, dim3(kRowsWarps * 32), rows_smem<128>(), s, "attn_rows", p, part, tiles);
+}
+
+lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s) {
+  const dim3 grid(cdiv(static_cast<int64_t>(p.M) * p.n_heads, 8));
+  if (head_dim == 64) return launch(attn_join_kernel<64>, grid, dim3(256), 0, s, "attn_join", p);
+  return launch(attn_join_kernel<128>, grid, dim3(256), 0, s, "attn_join", p);
+}
+
+lr_status configure_attn() {
+  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<64>());
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_rows_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem<128>());
+  if (e != cudaSuccess) return cuda_fail(e, "attention: set smem");
+  return LR_OK;
+}
+
+}  // namespace lr
+
+using namespace lr;
+
+extern "C" {
+
+size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d) {
+  if (d == nullptr || M <= 0 || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
+      d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
+    return 0;
+  return attn_plan(M, d).bytes;
+}
+
+lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
+                              const lr_attn_desc* d, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                              lr_stream s) {
+  const char* who = "prefix_attention";
+  lr_status st = check_desc(who, M, d);
+  if (st != LR_OK) return st;
+  if (out_dtype != LR_BF16 && out_dtype != LR_F32) return bad(LR_ERR_INVALID_ARG, "%s: bad output dtype", who);
+  if (M == 0) return LR_OK;
+  const lr_kv_cache& c = d->cache;
+  const int64_t width = static_cast<int64_t>(d->n_heads) * c.head_dim;
+  auto aligned = [](const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) & (a - 1)) == 0; };
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || ldq % 8 || ldo % 8 || ldq < width || ldo < width)
+    return bad(LR_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned with leading dimensions >= %lld, multiples of 8", who,
+               static_cast<long long>(width));
+  const AttnPlan plan = attn_plan(M, d);
+  if (plan.bytes > 0 && (workspace == nullptr || !aligned(workspace, 256)))
+    return bad(LR_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
+  if (ws_bytes < plan.bytes)
+    return bad(LR_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, ws_bytes, plan.bytes);
+  st = ensure_configured();
+  if (st != LR_OK) return st;
+
+  AttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q);
+  p.ldq = ldq;
+  p.k = static_cast<const uint16_t*>(c.k);
+  p.v = static_cast<const uint16_t*>(c.v);
+  p.ld = c.ld;
+  p.pool_blocks = c.pool_blocks;
+  p.pool_rows = c.pool_blocks * c.block_rows;
+  p.block_rows = c.block_rows;
+  p.n_heads = d->n_heads;
+  p.n_kv = c.n_kv_heads;
+  p.group = d->n_heads / c.n_kv_heads;
+  p.scale_log2 = d->scale * 1.4426950408889634f;
+  p.prefix_blocks = d->prefix_blocks;
+  p.prefix_len = d->prefix_len;
+  p.cap_prefix = d->cap_prefix_blocks * c.block_rows;
+  p.M = static_cast<int32_t>(M);
+  p.n_seq = d->n_seq;
+  p.max_q = static_cast<int32_t>(most_q(M, d));
+  p.q_start = d->q_start;
+  p.block_table = d->block_table;
+  p.blocks_per_seq = d->blocks_per_seq;
+  p.lengths = d->lengths;
+  p.cap_own = d->blocks_per_seq * c.block_rows;
+  p.po = static_cast<float*>(workspace);
+  p.pml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.ml_off);
+  p.prefix_slots = plan.prefix_slots;
+  p.own_slots = d->n_seq > 0 ? plan.own_slots : 0;
+  p.out = out;
+  p.ldo = ldo;
+  p.out_f32 = out_dtype == LR_F32;
+  p.status = dev_status;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
+  if (p.prefix_slots > 0) {
+    st = launch_attn_rows(p, c.head_dim, AttnPart{true, p.prefix_slots, 0}, cs);
+    if (st != LR_OK) return st;
+  }
+  if (p.own_slots > 0) {
+    st = launch_attn_rows(p, c.head_dim, AttnPart{false, p.own_slots, p.prefix_slots}, cs);
+    if (st != LR_OK) return st;
+  }
+  return launch_attn_join(p, c.head_dim, cs);
+}
+
+}  // extern "C"

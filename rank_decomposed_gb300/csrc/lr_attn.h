@@ -1,0 +1,88 @@
+// Shared by the attention kernels: device parameters and the layout of the
+// partial results.
+#pragma once
+
+#include "lr_internal.h"
+
+namespace lr {
+
+struct AttnParams {
+  const uint16_t* q;
+  int64_t ldq;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t ld;                 // row stride of both pools, elements
+  int64_t pool_rows, pool_blocks;
+  int32_t block_rows;
+  int32_t n_heads, n_kv, group;
+  float scale_log2;           // scale * log2(e): scores are kept in powers of two
+  const int32_t* prefix_blocks;
+  const int32_t* prefix_len;
+  int32_t cap_prefix;         // rows
+  int32_t M, n_seq, max_q;
+  const int32_t* q_start;
+  const int32_t* block_table;
+  int32_t blocks_per_seq;
+  const int32_t* lengths;
+  int32_t cap_own;            // rows
+  // Partial results.  Slot i of row r = m * n_heads + head: numerators
+  // po[(i * M * n_heads + r) * head_dim ..], and pml[i * M * n_heads + r] =
+  // (running maximum, sum), sum = 0 where the slot saw no key.  The prefix's
+  // slots come first.
+  float* po;
+  float2* pml;
+  int32_t prefix_slots, own_slots;
+  void* out;
+  int64_t ldo;
+  int32_t out_f32;
+  int32_t* status;
+};
+
+// The parts of a call that one kernel takes.
+struct AttnPart {
+  bool prefix;                // the shared prefix, or each sequence's own tokens
+  int32_t slots, slot0;
+};
+
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
+lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s);
+lr_status configure_attn();
+lr_status check_kv_cache(const char* who, const lr_kv_cache* c);
+
+#ifdef __CUDACC__
+// A sequence's query rows and own length, clamped to what the capacities allow.
+struct SeqView {
+  int32_t q0, nq, len;
+};
+__device__ __forceinline__ SeqView seq_view(const AttnParams& p, int b, bool tell) {
+  SeqView s;
+  bool bad = false;
+  if (p.q_start != nullptr) {
+    const int a = p.q_start[b], e = p.q_start[b + 1];
+    s.q0 = a < 0 ? 0 : (a > p.M ? p.M : a);
+    const int end = e < 0 ? 0 : (e > p.M ? p.M : e);
+    s.nq = end > s.q0 ? end - s.q0 : 0;
+    bad = a < 0 || e > p.M || e < a || s.nq > p.max_q;
+    if (s.nq > p.max_q) s.nq = p.max_q;
+  } else {
+    s.q0 = b;
+    s.nq = b < p.M ? 1 : 0;
+  }
+  const int len = p.lengths[b];
+  s.len = len < 0 ? 0 : (len > p.cap_own ? p.cap_own : len);
+  if (tell && (bad || s.len != len)) {
+    int32_t* st = p.status;
+    if (st != nullptr) atomicCAS(st, 0, LR_ERR_INDEX_RANGE);
+  }
+  return s;
+}
+__device__ __forceinline__ int prefix_view(const AttnParams& p, bool tell) {
+  if (p.cap_prefix == 0) return 0;
+  const int len = *p.prefix_len;
+  const int n = len < 0 ? 0 : (len > p.cap_prefix ? p.cap_prefix : len);
+  if (tell && n != len && p.status != nullptr) atomicCAS(p.status, 0, LR_ERR_INDEX_RANGE);
+  return n;
+}
+#endif
+
+}  // namespace lr

@@ -1,0 +1,431 @@
+// Norms of query and key heads with the position rotation in the same pass,
+// and the append of keys and values to a paged cache with both on the way.
+//
+// For a head x at position p:  y = x * gain / sqrt(mean(x^2) + eps), then the
+// pairs (a, b) of its first rot_dim elements become (a c - b s, b c + a s).
+// Everything is fp32 in registers; the one rounding is the store to bf16 (the
+// type of the cache and of the attention's operands).
+//
+// Bound by memory (a head is read and written once; about ten operations per
+// element) or, for a few rows, by the launch.  A head belongs to a group of
+// 8, 16 or 32 lanes with 8 neighbouring elements each: one 16-byte load and
+// store per lane for bf16, the sum of squares by butterflies in the group, and
+// the partner elements of the half style by shuffles.  A warp keeps the angles
+// and the gains of its lanes in registers and walks several heads of one row
+// with them: read per head, the angles (64 bytes a lane) would be four times
+// the head's own bytes.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "lr_ptx.cuh"
+
+namespace lr {
+namespace {
+
+struct HeadParams {
+  const void* src[3];   // q, k, v
+  int64_t ld[3];
+  void* dst[3];         // q_out, k_out or the K pool, the V pool
+  int64_t ldo[3];
+  int32_t end[3];       // heads of q; of q and k; of q, k and v
+  int32_t head_dim, lanes;
+  int32_t norm;
+  float eps;
+  const uint16_t* gain[2];
+  int32_t rot_dim, rot_style;
+  const float* cos_sin;
+  int64_t max_pos;
+  const int32_t* pos;
+  const int32_t* rows;  // append: the pool rows of k and v
+  int64_t pool_rows;
+  const int32_t* n_active;
+  int32_t M;
+  int32_t chunk, chunks;  // heads per warp, warps per row
+  int32_t* status;
+};
+
+template <bool F32>
+struct Raw;
+template <>
+struct Raw<false> {
+  uint4 a;
+};
+template <>
+struct Raw<true> {
+  float4 a, b;
+};
+
+__device__ __forceinline__ void load_raw(Raw<false>& r, const void* base, int64_t off) {
+  r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
+}
+__device__ __forceinline__ void load_raw(Raw<true>& r, const void* base, int64_t off) {
+  const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
+  r.a = p[0];
+  r.b = p[1];
+}
+__device__ __forceinline__ void widen8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<false>& r, float (&x)[8]) { widen8(r.a, x); }
+__device__ __forceinline__ void unpack(const Raw<true>& r, float (&x)[8]) {
+  x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w;
+  x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
+}
+
+// Heads in flight per group: their loads are issued together.
+constexpr int kFlight = 4;
+
+template <bool F32>
+__global__ void __launch_bounds__(256) heads_kernel(const __grid_constant__ HeadParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t m64 = w / p.chunks;
+  int n = p.M;
+  if (p.n_active != nullptr) {
+    const int a = *p.n_active;
+    n = a < 0 ? 0 : (a < n ? a : n);
+  }
+  if (m64 >= n) return;  // whole warps
+  const int m = static_cast<int>(m64);
+  const int first = static_cast<int>(w - m64 * p.chunks) * p.chunk;
+  const int sub = lane & (p.lanes - 1);      // lane in its group
+  const int grp = lane / p.lanes, groups = 32 / p.lanes;
+  const int e = sub * 8;                     // first element of this lane
+  const bool lives = e < p.head_dim;         // a head of 192 leaves 8 lanes idle
+
+  bool pos_ok = true;
+  float c[8], s[8];
+  int partner = lane;
+  float sign = 0.f;  // half style: -1 where this lane holds the pairs' a, +1 their b; 0: nothing here turns
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
+  if (p.rot_dim > 0) {
+    const int64_t at = p.pos[m];
+    pos_ok = at >= 0 && at < p.max_pos;
+    if (!pos_ok && lane == 0) report_status(p.status, LR_ERR_INDEX_RANGE);
+    if (pos_ok && e < p.rot_dim) {
+      const float* row = p.cos_sin + at * p.rot_dim;
+      const int half = p.rot_dim >> 1;
+      if (p.rot_style == LR_ROT_HALF) {
+        const int i = e < half ? e : e - half;
+        sign = e < half ? -1.f : 1.f;
+        partner = e < half ? lane + (half >> 3) : lane - (half >> 3);
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 cv = *reinterpret_cast<const float4*>(row + i + j);
+          const float4 sv = *reinterpret_cast<const float4*>(row + half + i + j);
+          c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
+          s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+        }
+      } else {
+        const float4 cv = *reinterpret_cast<const float4*>(row + (e >> 1));
+        const float4 sv = *reinterpret_cast<const float4*>(row + half + (e >> 1));
+        sign = 1.f;
+        c[0] = c[1] = cv.x, c[2] = c[3] = cv.y, c[4] = c[5] = cv.z, c[6] = c[7] = cv.w;
+        s[0] = s[1] = sv.x, s[2] = s[3] = sv.y, s[4] = s[5] = sv.z, s[6] = s[7] = sv.w;
+      }
+    }
+  }
+  const bool half_style = p.rot_style == LR_ROT_HALF;
+  int64_t pool_row = m;
+  bool row_ok = true;
+  if (p.rows != nullptr) {
+    pool_row = p.rows[m];
+    row_ok = pool_row >= 0 && pool_row < p.pool_rows;
+    if (!row_ok && lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
+  }
+
+  const int heads = p.end[2];
+  const int last = first + p.chunk < heads ? first + p.chunk : heads;
+  const float inv_d = 1.f / static_cast<float>(p.head_dim);
+  int kind_of_gain = -1;
+  float g[8];
+  for (int h0 = first; h0 < last; h0 += kFlight * groups) {
+    Raw<F32> raw[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int h = h0 + u * groups + grp;
+      if (h < last && lives) {
+        const int kind = h < p.end[0] ? 0 : (h < p.end[1] ? 1 : 2);
+        const int head = h - (kind ? p.end[kind - 1] : 0);
+        load_raw(raw[u], p.src[kind], m * p.ld[kind] + static_cast<int64_t>(head) * p.head_dim + e);
+      } else {
+        memset(&raw[u], 0, sizeof(raw[u]));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (h0 + u * groups >= last) break;  // the whole warp is past its heads
+      const int h = h0 + u * groups + grp;
+      const int kind = h < p.end[0] ? 0 : (h < p.end[1] ? 1 : 2);
+      const int head = h - (kind ? p.end[kind - 1] : 0);
+      float x[8];
+      unpack(raw[u], x);
+      // Values pass through; q and k are normed and turned.  Both halves of a
+      // warp take part in the shuffles whatever their heads are.
+      if (p.norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (kind < 2) {
+          if (kind != kind_of_gain) {
+            kind_of_gain = kind;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = 1.f;
+            if (p.gain[kind] != nullptr && lives)
+              widen8(*reinterpret_cast<const uint4*>(p.gain[kind] + e), g);
+          }
+          const float inv = 1.f / sqrtf(ss * inv_d + p.eps);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
+        }
+      }
+      if (p.rot_dim > 0) {
+        if (half_style) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float other = __shfl_sync(0xffffffffu, x[j], partner);
+            if (kind < 2 && sign != 0.f) x[j] = x[j] * c[j] + sign * (other * s[j]);
+          }
+        } else if (kind < 2 && sign != 0.f) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const float a = x[j], b = x[j + 1];
+            x[j] = a * c[j] - b * s[j];
+            x[j + 1] = b * c[j] + a * s[j];
+          }
+        }
+      }
+      if (h < last && lives) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = static_cast<uint32_t>(f32_to_bf16_rn(x[2 * j])) |
+                 (static_cast<uint32_t>(f32_to_bf16_rn(x[2 * j + 1])) << 16);
+        const bool pooled = kind > 0 && p.rows != nullptr;
+        if (!pos_ok) o[0] = o[1] = o[2] = o[3] = 0u;
+        if (!pooled || (row_ok && pos_ok)) {
+          const int64_t row = pooled ? pool_row : m;
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dst[kind]) + row * p.ldo[kind] +
+                                    static_cast<int64_t>(head) * p.head_dim + e) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+  }
+}
+
+lr_status bad(lr_status st, const char* fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  set_error("%s", msg);
+  return st;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+lr_status check_map(const char* who, const lr_head_map* hm) {
+  if (hm == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null head map", who);
+  if (hm->head_dim <= 0 || hm->rot_dim < 0) return bad(LR_ERR_INVALID_ARG, "%s: non-positive head_dim or negative rot_dim", who);
+  if (hm->head_dim % 64 || hm->head_dim > 256)
+    return bad(LR_ERR_UNSUPPORTED, "%s: head_dim %d is not a multiple of 64 up to 256", who, hm->head_dim);
+  if (hm->rot_dim % 16 || hm->rot_dim > hm->head_dim)
+    return bad(LR_ERR_UNSUPPORTED, "%s: rot_dim %d is not a multiple of 16 up to head_dim", who, hm->rot_dim);
+  if (hm->norm && !(hm->eps >= 0.f)) return bad(LR_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  if (!aligned16(hm->q_gain) || !aligned16(hm->k_gain))
+    return bad(LR_ERR_INVALID_ARG, "%s: gains must be 16-byte aligned", who);
+  if (hm->rot_dim > 0) {
+    if (hm->rot_style != LR_ROT_HALF && hm->rot_style != LR_ROT_PAIR)
+      return bad(LR_ERR_INVALID_ARG, "%s: bad rot_style", who);
+    if (hm->cos_sin == nullptr || !aligned16(hm->cos_sin) || hm->max_pos <= 0)
+      return bad(LR_ERR_INVALID_ARG, "%s: cos_sin must be a 16-byte aligned table of max_pos > 0 positions", who);
+  }
+  return LR_OK;
+}
+
+// One of the tensors whose heads are read or written.
+lr_status check_rows(const char* who, const char* name, const void* p, int64_t ld, int64_t width) {
+  if (p == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null %s", who, name);
+  if (!aligned16(p) || ld % 8 || ld < width)
+    return bad(LR_ERR_INVALID_ARG, "%s: %s must be 16-byte aligned with a leading dimension >= %lld that is a multiple of 8",
+               who, name, static_cast<long long>(width));
+  return LR_OK;
+}
+
+lr_status launch_heads(HeadParams& p, const lr_head_map* hm, lr_dtype in_dtype, cudaStream_t s) {
+  p.head_dim = hm->head_dim;
+  p.lanes = hm->head_dim <= 64 ? 8 : (hm->head_dim <= 128 ? 16 : 32);
+  p.norm = hm->norm;
+  p.eps = hm->eps;
+  p.gain[0] = static_cast<const uint16_t*>(hm->q_gain);
+  p.gain[1] = static_cast<const uint16_t*>(hm->k_gain);
+  p.rot_dim = hm->rot_dim;
+  p.rot_style = hm->rot_style;
+  p.cos_sin = hm->cos_sin;
+  p.max_pos = hm->max_pos;
+  // Heads per warp: as few as one a group while the rows do not fill the GPU
+  // (16 warps an SM), then more, so that the angles are read once for them.
+  const int groups = 32 / p.lanes, heads = p.end[2];
+  const int64_t want = static_cast<int64_t>(num_sms()) * 16;
+  int chunk = groups;
+  while (chunk < heads && chunk < kFlight * groups * 4 &&
+         static_cast<int64_t>(p.M) * ((heads + chunk - 1) / chunk) > want)
+    chunk += groups;
+  p.chunk = chunk;
+  p.chunks = (heads + chunk - 1) / chunk;
+  const int64_t blocks = (static_cast<int64_t>(p.M) * p.chunks + 7) / 8;
+  if (blocks > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "heads: too many rows and heads for one launch");
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (pdl_enabled()) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  cudaError_t e = in_dtype == LR_F32 ? cudaLaunchKernelEx(&cfg, heads_kernel<true>, p)
+                                     : cudaLaunchKernelEx(&cfg, heads_kernel<false>, p);
+  if (e != cudaSuccess) return cuda_fail(e, "heads");
+  return LR_OK;
+}
+
+lr_status check_common(const char* who, lr_dtype in_dtype, int64_t M, const int32_t* pos, const lr_head_map* hm,
+                       int32_t n_heads, int32_t n_kv_heads) {
+  lr_status st = check_map(who, hm);
+  if (st != LR_OK) return st;
+  if (in_dtype != LR_BF16 && in_dtype != LR_F32) return bad(LR_ERR_INVALID_ARG, "%s: bad input dtype", who);
+  if (n_heads < 0 || n_kv_heads < 0) return bad(LR_ERR_INVALID_ARG, "%s: negative head count", who);
+  if (n_heads > 65536 || n_kv_heads > 65536) return bad(LR_ERR_UNSUPPORTED, "%s: more than 65536 heads", who);
+  if (M < 0 || M > 0x7FFFFFFF) return bad(LR_ERR_INVALID_ARG, "%s: bad M", who);
+  if (M > 0 && hm->rot_dim > 0 && pos == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null positions", who);
+  return LR_OK;
+}
+
+}  // namespace
+
+lr_status check_kv_cache(const char* who, const lr_kv_cache* c) {
+  if (c == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null cache", who);
+  if (c->n_kv_heads <= 0 || c->head_dim <= 0 || c->block_rows <= 0 || c->pool_blocks < 0)
+    return bad(LR_ERR_INVALID_ARG, "%s: bad cache sizes", who);
+  if (c->pool_blocks > 0x7FFFFFFF / c->block_rows)
+    return bad(LR_ERR_INVALID_ARG, "%s: the cache's rows overflow int32", who);
+  const int64_t width = static_cast<int64_t>(c->n_kv_heads) * c->head_dim;
+  lr_status st = check_rows(who, "K pool", c->k, c->ld, width);
+  if (st != LR_OK) return st;
+  return check_rows(who, "V pool", c->v, c->ld, width);
+}
+
+}  // namespace lr
+
+using namespace lr;
+
+extern "C" {
+
+lr_status lr_rope_table(int64_t max_pos, int32_t rot_dim, double theta, float* out) {
+  if (max_pos < 0 || rot_dim <= 0 || rot_dim % 2 || !(theta > 0) || std::isinf(theta))
+    return bad(LR_ERR_INVALID_ARG, "rope_table: max_pos >= 0, an even rot_dim > 0 and a finite theta > 0 are wanted");
+  if (max_pos > 0 && out == nullptr) return bad(LR_ERR_INVALID_ARG, "rope_table: null output");
+  const int half = rot_dim / 2;
+  for (int i = 0; i < half; ++i) {
+    const double f = std::pow(theta, -2.0 * i / rot_dim);
+    for (int64_t p = 0; p < max_pos; ++p) {
+      out[p * rot_dim + i] = static_cast<float>(std::cos(static_cast<double>(p) * f));
+      out[p * rot_dim + half + i] = static_cast<float>(std::sin(static_cast<double>(p) * f));
+    }
+  }
+  return LR_OK;
+}
+
+lr_status lr_qk_norm_rope(const void* q, int64_t ldq, int32_t n_heads, const void* k, int64_t ldk,
+                          int32_t n_kv_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
+                          const int32_t* n_active, const lr_head_map* hm, void* q_out, int64_t ldqo,
+                          void* k_out, int64_t ldko, int32_t* dev_status, lr_stream s) {
+  const char* who = "qk_norm_rope";
+  lr_status st = check_common(who, in_dtype, M, pos, hm, n_heads, n_kv_heads);
+  if (st != LR_OK) return st;
+  if (M == 0 || n_heads + n_kv_heads == 0) return LR_OK;
+  const int64_t wq = static_cast<int64_t>(n_heads) * hm->head_dim, wk = static_cast<int64_t>(n_kv_heads) * hm->head_dim;
+  if (n_heads > 0) {
+    if ((st = check_rows(who, "q", q, ldq, wq)) != LR_OK) return st;
+    if ((st = check_rows(who, "q_out", q_out, ldqo, wq)) != LR_OK) return st;
+    if (q == q_out && (in_dtype != LR_BF16 || ldq != ldqo))
+      return bad(LR_ERR_INVALID_ARG, "%s: in place needs bf16 and one leading dimension", who);
+  }
+  if (n_kv_heads > 0) {
+    if ((st = check_rows(who, "k", k, ldk, wk)) != LR_OK) return st;
+    if ((st = check_rows(who, "k_out", k_out, ldko, wk)) != LR_OK) return st;
+    if (k == k_out && (in_dtype != LR_BF16 || ldk != ldko))
+      return bad(LR_ERR_INVALID_ARG, "%s: in place needs bf16 and one leading dimension", who);
+  }
+  HeadParams p;
+  memset(&p, 0, sizeof(p));
+  p.src[0] = q, p.src[1] = k;
+  p.ld[0] = ldq, p.ld[1] = ldk;
+  p.dst[0] = q_out, p.dst[1] = k_out;
+  p.ldo[0] = ldqo, p.ldo[1] = ldko;
+  p.end[0] = n_heads, p.end[1] = p.end[2] = n_heads + n_kv_heads;
+  p.pos = pos;
+  p.n_active = n_active;
+  p.M = static_cast<int32_t>(M);
+  p.status = dev_status;
+  return launch_heads(p, hm, in_dtype, reinterpret_cast<cudaStream_t>(s));
+}
+
+lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq,
+                       int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
+                       const int32_t* rows, const int32_t* n_active, const lr_head_map* hm,
+                       const lr_kv_cache* cache, void* q_out, int64_t ldqo, int32_t* dev_status, lr_stream s) {
+  const char* who = "kv_append";
+  lr_status st = check_kv_cache(who, cache);
+  if (st != LR_OK) return st;
+  st = check_common(who, in_dtype, M, pos, hm, n_heads, cache->n_kv_heads);
+  if (st != LR_OK) return st;
+  if (hm->head_dim != cache->head_dim) return bad(LR_ERR_INVALID_ARG, "%s: the head map's head_dim is not the cache's", who);
+  if (M == 0) return LR_OK;
+  if (rows == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null rows", who);
+  const int64_t wk = static_cast<int64_t>(cache->n_kv_heads) * hm->head_dim;
+  if ((st = check_rows(who, "k", k, ldk, wk)) != LR_OK) return st;
+  if ((st = check_rows(who, "v", v, ldv, wk)) != LR_OK) return st;
+  if (n_heads > 0) {
+    const int64_t wq = static_cast<int64_t>(n_heads) * hm->head_dim;
+    if ((st = check_rows(who, "q", q, ldq, wq)) != LR_OK) return st;
+    if ((st = check_rows(who, "q_out", q_out, ldqo, wq)) != LR_OK) return st;
+    if (q == q_out && (in_dtype != LR_BF16 || ldq != ldqo))
+      return bad(LR_ERR_INVALID_ARG, "%s: in place needs bf16 and one leading dimension", who);
+  }
+  HeadParams p;
+  memset(&p, 0, sizeof(p));
+  p.src[0] = q, p.src[1] = k, p.src[2] = v;
+  p.ld[0] = ldq, p.ld[1] = ldk, p.ld[2] = ldv;
+  p.dst[0] = q_out, p.dst[1] = cache->k, p.dst[2] = cache->v;
+  p.ldo[0] = ldqo, p.ldo[1] = p.ldo[2] = cache->ld;
+  p.end[0] = n_heads, p.end[1] = n_heads + cache->n_kv_heads, p.end[2] = n_heads + 2 * cache->n_kv_heads;
+  p.pos = pos;
+  p.rows = rows;
+  p.pool_rows = cache->pool_blocks * cache->block_rows;
+  p.n_active = n_active;
+  p.M = static_cast<int32_t>(M);
+  p.status = dev_status;
+  return launch_heads(p, hm, in_dtype, reinterpret_cast<cudaStream_t>(s));
+}
+
+}  // extern "C"

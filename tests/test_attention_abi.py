@@ -1,0 +1,172 @@
+"""Cached-attention entry points without a GPU: the host table, argument checks, workspace rule, oracle pins."""
+
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+import rank_decomposed_gb300 as lr
+
+BIG = 1 << 40
+
+
+def test_rope_table_matches_oracle_angles_at_far_positions():
+    n, rot = 70000, 32
+    t = lr.rope_table(n, rot, 10000.0)
+    a = oracle.rope_angles(np.arange(n), rot)
+    want = np.concatenate([np.cos(a), np.sin(a)], axis=1)
+    # one rounding to fp32 of values at most 1, and the 64-bit angle's own (70000 * 2^-53)
+    assert np.abs(t - want).max() <= 2.0 ** -25 + 1e-10
+
+
+def test_rope_table_refusals():
+    out = np.zeros(64, np.float32)
+    f = lambda n, rot, theta, p=out.ctypes.data: lr.lib.lr_rope_table(n, rot, theta, p)
+    assert f(0, 16, 1e4, None) == lr.LR_OK
+    assert f(4, 16, 1e4) == lr.LR_OK
+    for a in ((-1, 16, 1e4), (4, 0, 1e4), (4, 7, 1e4), (4, 16, 0.0), (4, 16, float("nan")), (4, 16, float("inf"))):
+        assert f(*a) == lr.LR_ERR_INVALID_ARG
+    assert f(4, 16, 1e4, None) == lr.LR_ERR_INVALID_ARG
+
+
+def _map(hd=128, rot=128, **kw):
+    d = lr.HeadMapDesc(hd, 1, 1e-6, 0x1000, 0x2000, rot, lr.ROT_HALF, 0x3000, 100)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def _rope(hm=None, M=4, q=0x10000, ldq=1024, nh=8, k=0x20000, ldk=256, nkv=2, dt=lr.LR_BF16, pos=0x100, qo=0x30000,
+          ldqo=1024, ko=0x40000, ldko=256):
+    hm = hm or _map()
+    return lr.lib.lr_qk_norm_rope(q, ldq, nh, k, ldk, nkv, dt, M, pos, None, ctypes.byref(hm), qo, ldqo, ko, ldko, None,
+                                  None)
+
+
+def test_qk_norm_rope_refusals_launch_nothing():
+    assert _rope(M=0, q=None, pos=None) == lr.LR_OK
+    assert _rope(nh=0, nkv=0) == lr.LR_OK
+    bad = lr.LR_ERR_INVALID_ARG
+    for kw in (dict(q=None), dict(q=0x10008), dict(ldq=1000), dict(ldq=1028), dict(k=None), dict(qo=None), dict(ko=None),
+               dict(ldko=128), dict(dt=7), dict(M=-1), dict(nh=-1), dict(pos=None), dict(M=1 << 31),
+               dict(dt=lr.LR_F32, qo=0x10000),                      # in place with another type
+               dict(qo=0x10000, ldq=1032)):                         # in place with another stride
+        assert _rope(**kw) == bad, kw
+    for kw in (dict(eps=-1.0), dict(eps=float("nan")), dict(q_gain=0x1008), dict(rot_style=5), dict(cos_sin=None),
+               dict(cos_sin=0x3004), dict(max_pos=0), dict(head_dim=0), dict(rot_dim=-16)):
+        assert _rope(hm=_map(**kw)) == bad, kw
+    for kw in (dict(head_dim=96), dict(head_dim=320), dict(rot_dim=24), dict(rot_dim=144)):
+        assert _rope(hm=_map(**kw)) == lr.LR_ERR_UNSUPPORTED, kw
+    assert "rot_dim" in lr.last_error()
+    assert lr.lib.lr_qk_norm_rope(0x10000, 1024, 8, 0x20000, 256, 2, 0, 4, 0x100, None, None, 0x30000, 1024, 0x40000,
+                                  256, None, None) == bad
+
+
+def _cache(**kw):
+    c = lr.KvCache(0x100000, 0x200000, 256, 64, 16, 2, 128)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _append(cache=None, hm=None, M=4, k=0x1000, v=0x2000, q=0x3000, nh=8, rows=0x200, pos=0x100, qo=0x4000):
+    hm, cache = hm or _map(), cache or _cache()
+    return lr.lib.lr_kv_append(k, 256, v, 256, q, 1024, nh, lr.LR_BF16, M, pos, rows, None, ctypes.byref(hm),
+                               ctypes.byref(cache), qo, 1024, None, None)
+
+
+def test_kv_append_refusals_launch_nothing():
+    assert _append(M=0) == lr.LR_OK
+    for kw in (dict(k=None), dict(v=None), dict(v=0x2002), dict(q=None), dict(qo=None), dict(rows=None), dict(pos=None),
+               dict(hm=_map(hd=64, rot=64))):
+        assert _append(**kw) == lr.LR_ERR_INVALID_ARG, kw
+    for kw in (dict(k=None), dict(v=0x200008), dict(ld=250), dict(ld=128), dict(n_kv_heads=0), dict(block_rows=0),
+               dict(pool_blocks=-1), dict(pool_blocks=1 << 28)):
+        assert _append(cache=_cache(**kw)) == lr.LR_ERR_INVALID_ARG, kw
+
+
+def _desc(**kw):
+    d = lr.AttnDesc(_cache(), 8, 0.1, 0x100, 10, 0x200, 3, 0x300, 5, 0x400, 4, 0x500)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def _attn(d=None, M=9, q=0x10000, ldq=1024, out=0x20000, ldo=1024, dt=lr.LR_BF16, ws=0x30000, ws_bytes=BIG):
+    d = d or _desc()
+    return lr.lib.lr_prefix_attention(q, ldq, out, ldo, dt, M, ctypes.byref(d), ws, ws_bytes, None, None)
+
+
+def test_prefix_attention_refusals_launch_nothing():
+    assert _attn(M=0) == lr.LR_OK
+    bad, no = lr.LR_ERR_INVALID_ARG, lr.LR_ERR_UNSUPPORTED
+    need = lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(_desc()))
+    assert need > 0
+    for kw in (dict(q=None), dict(out=None), dict(q=0x10002), dict(ldq=1000), dict(ldo=1028), dict(dt=3), dict(M=-1),
+               dict(ws=None), dict(ws=0x30010), dict(ws_bytes=need - 1)):
+        assert _attn(**kw) == bad, kw
+    for kw in (dict(n_heads=7), dict(n_heads=0), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(prefix_blocks=None), dict(prefix_len=None), dict(cap_prefix_blocks=-1), dict(n_seq=-1),
+               dict(lengths=None), dict(block_table=None), dict(max_q=0), dict(q_start=None),  # max_q 5 without q_start
+               dict(cap_prefix_blocks=1 << 28), dict(blocks_per_seq=1 << 28),
+               dict(q_start=None, max_q=1, n_seq=10),                                          # more sequences than rows
+               dict(cache=_cache(ld=100)), dict(cache=_cache(k=None))):
+        assert _attn(d=_desc(**kw)) == bad, kw
+    for kw in (dict(cache=_cache(head_dim=192, ld=512)), dict(cache=_cache(block_rows=8)), dict(n_heads=2 * 65)):
+        assert _attn(d=_desc(**kw), ldq=1 << 15, ldo=1 << 15) == no, kw
+    assert lr.lib.lr_prefix_attention(0x10000, 1024, 0x20000, 1024, 0, 9, None, 0x30000, BIG, None, None) == bad
+
+
+def test_workspace_covers_capacities_and_is_zero_for_nothing():
+    f = lambda M, **kw: lr.lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(_desc(**kw)))
+    assert f(0) == 0 and f(-3) == 0
+    assert lr.lib.lr_prefix_attention_workspace_bytes(9, None) == 0
+    assert f(9, cap_prefix_blocks=100) >= f(9) > 0
+
+
+def test_status_string_of_index_range():
+    assert "range" in lr.status_string(lr.LR_ERR_INDEX_RANGE)
+
+
+# ------------------------------------------------------------ oracle pins
+def test_oracle_rotation_keeps_pair_norms_and_adds_angles():
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((3, 2 * 64))
+    for style in ("half", "pair"):
+        a1, a2 = oracle.rope_angles([3, 5, 9], 32), oracle.rope_angles([4, 1, 30], 32)
+        turn = lambda t, a: oracle.map_heads(t, 64, None, 0.0, np.cos(a), np.sin(a), style)
+        assert np.allclose(turn(turn(x, a1), a2), turn(x, a1 + a2), atol=1e-12)
+        assert np.allclose(np.linalg.norm(turn(x, a1)), np.linalg.norm(x))
+        assert np.array_equal(turn(x, a1).reshape(3, 2, 64)[..., 32:], x.reshape(3, 2, 64)[..., 32:])
+
+
+def test_oracle_scores_depend_on_distance_alone():
+    rng = np.random.default_rng(1)
+    q, k = rng.standard_normal((1, 64)), rng.standard_normal((1, 64))
+    def score(p, t):
+        turn = lambda x, n: oracle.map_heads(x, 64, None, 0.0, np.cos(oracle.rope_angles([n], 64)),
+                                             np.sin(oracle.rope_angles([n], 64)), "half")
+        return float((turn(q, p) @ turn(k, t).T)[0, 0])
+    assert abs(score(100, 60) - score(1040, 1000)) < 1e-9
+
+
+def test_oracle_prefix_attention_is_attention_over_the_joined_context():
+    """Pages shuffled and split into prefix and own tokens give plain attention over the same tokens in order."""
+    rng = np.random.default_rng(2)
+    d, nkv, nh, br = 8, 2, 4, 4
+    K, V = rng.standard_normal((11, nkv * d)), rng.standard_normal((11, nkv * d))
+    kp, vp = np.full((24, nkv * d), np.nan), np.full((24, nkv * d), np.nan)
+    pre, own = [4, 1], [5, 0]
+    for t in range(11):
+        at = pre[t // br] * br + t % br if t < 6 else own[(t - 6) // br] * br + (t - 6) % br
+        kp[at], vp[at] = K[t], V[t]
+    q = rng.standard_normal((3, nh * d))
+    out, _ = oracle.prefix_attention(q, kp, vp, nh, nkv, d, br, pre, 6, [own], [5], [0, 3], 0.3)
+    for j in range(3):
+        for h in range(nh):
+            n, c = 9 + j, slice(h // 2 * d, h // 2 * d + d)
+            w = np.exp(0.3 * K[:n, c] @ q[j, h * d:(h + 1) * d])
+            assert np.allclose(out[j, h * d:(h + 1) * d], w @ V[:n, c] / w.sum())
+    empty, _ = oracle.prefix_attention(q, kp, vp, nh, nkv, d, br, pre, 0, [own], [1], [0, 3], 0.3)
+    assert not empty[:2].any() and empty[2].any()      # one own token: the first two rows see nothing
