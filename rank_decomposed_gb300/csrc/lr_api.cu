@@ -156,6 +156,29 @@ lr_status encode_map_bf16_chunks(CUtensorMap* map, const void* base, uint64_t ro
   return LR_OK;
 }
 
+lr_status encode_map_heads(CUtensorMap* map, const void* base, uint64_t head_dim, uint64_t heads, uint64_t rows,
+                           uint64_t ld, uint32_t box_heads, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) {
+    set_error("cuTensorMapEncodeTiled unavailable");
+    return LR_ERR_CUDA;
+  }
+  cuuint64_t dims[3] = {head_dim, heads, rows};
+  cuuint64_t strides[2] = {head_dim * 2, ld * 2};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled (heads) failed (%d): head_dim=%llu heads=%llu rows=%llu ld=%llu box=%ux%u",
+              static_cast<int>(r), (unsigned long long)head_dim, (unsigned long long)heads, (unsigned long long)rows,
+              (unsigned long long)ld, box_heads, box_rows);
+    return LR_ERR_CUDA;
+  }
+  return LR_OK;
+}
+
 lr_status ensure_configured() {
   static bool done[64] = {false};
   static std::mutex mu;
@@ -172,6 +195,8 @@ lr_status ensure_configured() {
   st = configure_prefill_pair();
   if (st != LR_OK) return st;
   st = configure_attn();
+  if (st != LR_OK) return st;
+  st = configure_attn_tiles();
   if (st != LR_OK) return st;
   done[dev] = true;
   return LR_OK;

@@ -393,36 +393,48 @@ lr_status bad(lr_status st, const char* fmt, ...) {
   return st;
 }
 
-// How a call is cut, from its capacities alone (lengths are on the device).
-struct AttnPlan {
-  int32_t prefix_slots, own_slots;
-  size_t ml_off, bytes;
-};
-
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
-// Key ranges per row tile: enough CTAs for two waves of the GPU's slots, each
-// of at least 128 keys.
-int slots_for(int64_t ctas, int64_t keys) {
+// No sequence has more rows than the call.
+int64_t most_q(int64_t M, const lr_attn_desc* d) { return d->max_q < M ? d->max_q : (M < 1 ? 1 : M); }
+
+// Key ranges for `ctas` row tiles: as many as fill `want` CTAs, none shorter
+// than min_keys.
+int slots_for(int64_t ctas, int64_t keys, int64_t want, int64_t min_keys) {
   if (keys <= 0) return 0;
-  const int64_t want = static_cast<int64_t>(num_sms()) * 4;
   int64_t n = ctas >= want ? 1 : want / ctas;
-  const int64_t most = cdiv(keys, 128);
+  const int64_t most = cdiv(keys, min_keys);
   if (n > most) n = most;
   if (n > 64) n = 64;
   return static_cast<int>(n);
 }
 
-// No sequence has more rows than the call.
-int64_t most_q(int64_t M, const lr_attn_desc* d) { return d->max_q < M ? d->max_q : (M < 1 ? 1 : M); }
+// How a call is cut, from its capacities alone (lengths are on the device).
+struct AttnPlan {
+  bool whole;         // prefix and own tokens in one tensor-core pass per sequence
+  bool tiles;         // the prefix on the tensor-core tiles
+  int32_t prefix_slots, own_slots;  // whole: prefix_slots counts the ranges, 0 when there is but one
+  size_t ml_off, bytes;
+};
 
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   AttnPlan a;
+  memset(&a, 0, sizeof(a));
   const int G = d->n_heads / d->cache.n_kv_heads;
-  const int64_t kv = d->cache.n_kv_heads;
-  a.prefix_slots = slots_for(cdiv(M * G, kRowsTile) * kv, static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows);
-  a.own_slots = slots_for(static_cast<int64_t>(d->n_seq) * cdiv(most_q(M, d) * G, kRowsTile) * kv,
-                          static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows);
+  const int64_t kv = d->cache.n_kv_heads, mq = most_q(M, d);
+  const int64_t cap_prefix = static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows;
+  const int64_t cap_own = static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows;
+  const int64_t pair = 2 * attn_tile_rows(G);
+  a.whole = d->n_seq > 0 && mq * G > 64;
+  if (a.whole) {
+    const int n = slots_for(d->n_seq * cdiv(mq, pair) * kv, cap_prefix + cap_own, num_sms(), 512);
+    a.prefix_slots = n > 1 ? n : 0;
+  } else {
+    a.tiles = M * G > kRowsTile;
+    a.prefix_slots = a.tiles ? slots_for(cdiv(M, pair) * kv, cap_prefix, num_sms(), 256)
+                             : slots_for(cdiv(M * G, kRowsTile) * kv, cap_prefix, num_sms() * 4, 128);
+    a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, num_sms() * 4, 128);
+  }
   const size_t rows = static_cast<size_t>(M) * d->n_heads * (a.prefix_slots + a.own_slots);
   a.ml_off = (rows * d->cache.head_dim * 4 + 255) / 256 * 256;
   a.bytes = a.ml_off + (rows * 8 + 255) / 256 * 256;
@@ -548,19 +560,25 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
   p.po = static_cast<float*>(workspace);
   p.pml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + plan.ml_off);
   p.prefix_slots = plan.prefix_slots;
-  p.own_slots = d->n_seq > 0 ? plan.own_slots : 0;
+  p.own_slots = plan.own_slots;
   p.out = out;
   p.ldo = ldo;
   p.out_f32 = out_dtype == LR_F32;
   p.status = dev_status;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-  if (p.prefix_slots > 0) {
-    st = launch_attn_rows(p, c.head_dim, AttnPart{true, p.prefix_slots, 0}, cs);
-    if (st != LR_OK) return st;
-  }
-  if (p.own_slots > 0) {
-    st = launch_attn_rows(p, c.head_dim, AttnPart{false, p.own_slots, p.prefix_slots}, cs);
-    if (st != LR_OK) return st;
+  if (plan.whole) {
+    st = launch_attn_tiles(p, c.head_dim, AttnPart{true, true, plan.prefix_slots > 0 ? plan.prefix_slots : 1, 0}, cs);
+    if (st != LR_OK || plan.prefix_slots == 0) return st;
+  } else {
+    if (p.prefix_slots > 0) {
+      const AttnPart part{true, false, p.prefix_slots, 0};
+      st = plan.tiles ? launch_attn_tiles(p, c.head_dim, part, cs) : launch_attn_rows(p, c.head_dim, part, cs);
+      if (st != LR_OK) return st;
+    }
+    if (p.own_slots > 0) {
+      st = launch_attn_rows(p, c.head_dim, AttnPart{false, false, p.own_slots, p.prefix_slots}, cs);
+      if (st != LR_OK) return st;
+    }
   }
   return launch_attn_join(p, c.head_dim, cs);
 }

@@ -38,13 +38,26 @@ struct AttnParams {
   int32_t* status;
 };
 
-// The parts of a call that one kernel takes.
+// The part of a call that one launch takes: the prefix for all rows of the
+// batch, each sequence's own tokens, or (whole) both for each sequence's rows;
+// cut along the keys into `slots` ranges, whose results are slots slot0 and on.
 struct AttnPart {
-  bool prefix;                // the shared prefix, or each sequence's own tokens
+  bool prefix;
+  bool whole;
   int32_t slots, slot0;
 };
 
+// Query rows of a tensor-core tile: their heads of one key head fill its 128
+// rows as far as whole rows do.
+inline int attn_tile_rows(int group) { return 128 / group; }
+
 lr_status launch_attn_rows(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
+lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
+lr_status configure_attn_tiles();
+// Tensor map over query rows [M][ld]: element (c, h, m) is column h * head_dim
+// + c of row m; a box takes 64 columns of box_heads heads of box_rows rows.
+lr_status encode_map_heads(CUtensorMap* map, const void* base, uint64_t head_dim, uint64_t heads, uint64_t rows,
+                           uint64_t ld, uint32_t box_heads, uint32_t box_rows);
 lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s);
 lr_status configure_attn();
 lr_status check_kv_cache(const char* who, const lr_kv_cache* c);

@@ -1,0 +1,663 @@
+// Attention of many query rows on the 5th-generation tensor cores: the shared
+// prefix against all rows of the batch, and whole ragged turns (prefix and own
+// tokens in one pass).
+//
+// Rows are query rows times the G query heads of one key head: a tile is
+// floor(128 / G) query rows, so its G heads share every key that is loaded.
+// A CTA holds two row tiles against the same keys, or, when there are rows for
+// one tile only, one row tile against alternate keys twice; either way two
+// independent softmax rings keep the tensor pipe busy while the other one's
+// powers are computed:
+//   warps 0-3, 4-7  softmax of ring 0 and 1, one row per thread;
+//   warp 8          TMA producer (K and V tiles of 128 keys, 16-row boxes: a
+//                   box never crosses a page);
+//   warp 9          tcgen05.mma issue: S = Q K^T (Q, K in shared memory) and
+//                   O += P V (P in TMEM, where the softmax warps put it over
+//                   S; V in shared memory as it lies in the cache, keys along
+//                   the reduction, which is the operand's MN-major form).
+// The order of the products is  S0 S1 | PV0 S0' PV1 S1' | ...: S0' needs
+// softmax 0 to be through with S0 (its P has been consumed by PV0, issued just
+// before), and runs while softmax 1 works.
+//
+// The running maximum moves only when it would grow by more than 2^8 in the
+// powers: until then powers up to 256 are summed against the older maximum
+// (exact in fp32 and in bf16's range), and O in TMEM needs no rescaling.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "lr_attn.h"
+#include "lr_ptx.cuh"
+
+namespace lr {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kKeys = 128;           // keys per tile
+constexpr int kPage = 16;            // rows per TMA box
+constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 each), O0, O1 (head_dim each)
+constexpr float kSlack = 8.f;
+
+template <int HD>
+struct Shape {
+  static constexpr int kChunks = HD / 64;              // 128-byte swizzled columns of a tile
+  static constexpr int kChunkBytes = 128 * 128;        // 128 rows of 64 bf16
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kSlots = HD == 128 ? 5 : 10;    // ring of K and V tiles
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+};
+
+struct TileParams {
+  AttnParams p;
+  int32_t whole;      // one pass over prefix and own tokens of a sequence; else the prefix for all rows
+  int32_t mt;         // query rows per tile
+  int32_t pairs;      // tile pairs per sequence (whole)
+  int32_t slots, slot0;
+  int32_t direct;     // one key range: results go straight to out
+  int32_t stall;      // fault-injection hook: the producer issues nothing
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+#define LR_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define LR_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+
+// 32 lanes x 32 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31}, [%32];"
+      : LR_R8(r, 0), LR_R8(r, 8), LR_R8(r, 16), LR_R8(r, 24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31};" ::LR_I8(r, 0),
+      LR_I8(r, 8), LR_I8(r, 16), LR_I8(r, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulator.
+__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 3-D tiled load, as tma_load_2d.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
+// Descriptor of a V tile: element (key, column) of [128 keys][64 columns]
+// chunks with the 128-byte swizzle, columns contiguous (MN-major).  Groups of
+// eight keys are 1024 bytes apart (stride offset), chunks of 64 columns
+// chunk_bytes apart (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+
+struct Bars {
+  uint64_t q_full;
+  uint64_t full[10], empty[10];
+  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t tail, drain;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tiles_kernel(const __grid_constant__ TileParams a, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using S = Shape<HD>;
+  constexpr int kSlots = S::kSlots;
+  __shared__ __align__(8) Bars bars;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ float2 ml_sh[128];
+  extern __shared__ uint8_t dyn_smem[];
+  const AttnParams& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_u32(dyn_smem);
+  uint8_t* smem = dyn_smem + (((raw + 1023u) & ~1023u) - raw);
+  uint8_t* q_sm = smem;                            // two row tiles
+  uint8_t* ring = smem + 2 * S::kTileBytes;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars.q_full, 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars.s_full[t], 1);
+      mbar_init(&bars.p_ready[t], 4);
+      mbar_init(&bars.o_done[t], 1);
+    }
+    mbar_init(&bars.tail, 1);
+    mbar_init(&bars.drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- this CTA's rows and keys
+  const int kvh = blockIdx.y, split = blockIdx.z, G = p.group;
+  const bool tell = threadIdx.x == 0 && kvh == 0 && split == 0;
+  const int P = prefix_view(p, tell && blockIdx.x == 0);
+  int q0 = 0, nq = p.M, own = 0, mrel;
+  const int32_t* own_pages = nullptr;
+  if (a.whole) {
+    const int b = blockIdx.x / a.pairs;
+    const SeqView v = seq_view(p, b, tell && blockIdx.x % a.pairs == 0);
+    q0 = v.q0, nq = v.nq, own = v.len;
+    own_pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
+    mrel = (blockIdx.x % a.pairs) * 2 * a.mt;
+  } else {
+    mrel = blockIdx.x * 2 * a.mt;
+  }
+  if (a.direct && kvh == 0 && threadIdx.x < 32 * 8) {  // rows of no sequence: zeros
+    const int from = p.q_start ? p.q_start[0] : 0, to = p.q_start ? p.q_start[p.n_seq] : p.n_seq;
+    const int esz = p.out_f32 ? 4 : 2;
+    const int vecs = p.n_heads * HD * esz / 16;
+    for (int m = blockIdx.x; m < p.M; m += gridDim.x)
+      if (m < from || m >= to) {
+        uint4* row = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + m * p.ldo * esz);
+        for (int i = threadIdx.x; i < vecs; i += 32 * 8) row[i] = make_uint4(0, 0, 0, 0);
+      }
+  }
+  if (nq - mrel <= 0) return;
+  int nrow[2];  // query rows of each tile
+  nrow[0] = nq - mrel < a.mt ? nq - mrel : a.mt;
+  nrow[1] = nq - mrel - a.mt < a.mt ? nq - mrel - a.mt : a.mt;
+  if (nrow[1] < 0) nrow[1] = 0;
+  const bool dual = nrow[1] == 0;  // one row tile, both rings
+  // own tokens that a tile's last row sees
+  auto seen = [&](int m) {
+    const int v = own - nq + m + 1;
+    return v < 0 ? 0 : v;
+  };
+  const int np = (P + kKeys - 1) / kKeys;
+  const int see0 = a.whole ? seen(mrel + nrow[0] - 1) : 0;
+  const int see1 = a.whole && !dual ? seen(mrel + a.mt + nrow[1] - 1) : 0;
+  const int see = see0 > see1 ? see0 : see1;
+  const int t_all = np + (see + kKeys - 1) / kKeys;
+  const int per = (t_all + a.slots - 1) / a.slots;
+  const int k_lo = split * per;
+  const int k_hi = k_lo + per < t_all ? k_lo + per : t_all;
+  const int n = k_hi > k_lo ? k_hi - k_lo : 0;     // key tiles of this CTA
+  int nt[2];                                       // and of each ring
+  if (dual) {
+    nt[0] = (n + 1) >> 1;
+    nt[1] = n >> 1;
+  } else {
+    const int e0 = np + (see0 + kKeys - 1) / kKeys, e1 = np + (see1 + kKeys - 1) / kKeys;
+    nt[0] = (e0 < k_hi ? e0 : k_hi) - k_lo;
+    nt[1] = (e1 < k_hi ? e1 : k_hi) - k_lo;
+    if (nt[0] < 0) nt[0] = 0;
+    if (nt[1] < 0) nt[1] = 0;
+  }
+
+  if (warp == 9) {
+    tmem_alloc(&tmem_base_sh, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+
+  // softmax state of this thread's row
+  const int ringi = warp >> 2;                     // 0, 1: softmax warps
+  const int trow = threadIdx.x & 127;
+  const int tile = dual ? 0 : (ringi & 1);
+  const int live_rows = nrow[tile] * G;
+  float mref = -INFINITY, sum = 0.f;
+
+  if (warp == 8) {
+    // ------------------------------------------------------ producer
+    if (lane == 0) {
+      prefetch_tensormap(&map_q);
+      prefetch_tensormap(&map_k);
+      prefetch_tensormap(&map_v);
+    }
+    const uint64_t pol = l2_policy_evict_last();
+    if (!a.stall && n > 0) {
+      if (lane == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(a.mt * G * 128 * S::kChunks) * (dual ? 1u : 2u);
+        mbar_arrive_expect_tx(&bars.q_full, bytes);
+        for (int t = 0; t < (dual ? 1 : 2); ++t)
+          for (int c = 0; c < S::kChunks; ++c)
+            tma_load_3d(q_sm + t * S::kTileBytes + c * S::kChunkBytes, &map_q, &bars.q_full, c * 64, kvh * G,
+                        q0 + mrel + t * a.mt, pol);
+      }
+      const int grp = lane / S::kChunks, ch = lane % S::kChunks;
+      const bool mine = grp < kKeys / kPage;
+      // pool row of this lane's 16 keys of tile k; past the pool (reads as zeros) where there are none
+      auto row_of = [&](int k) {
+        int t, limit;
+        const int32_t* pages;
+        if (k < np) {
+          t = k * kKeys + grp * kPage, limit = P, pages = p.prefix_blocks;
+        } else {
+          t = (k - np) * kKeys + grp * kPage, limit = see, pages = own_pages;
+        }
+        int64_t row = p.pool_rows;
+        if (mine && t < limit) {
+          const int64_t page = pages[t / p.block_rows];
+          if (page < 0 || page >= p.pool_blocks)
+            report_status(p.status, LR_ERR_REMAP_RANGE);
+          else
+            row = page * p.block_rows + t % p.block_rows;
+        }
+        return static_cast<int32_t>(row);
+      };
+      int ld = 0, tails = 0;
+      bool ok = true;
+      // keys of tile k that hold tokens
+      auto filled = [&](int k) {
+        const int f = k < np ? P - k * kKeys : see - (k - np) * kKeys;
+        return f < kKeys ? f : kKeys;
+      };
+      auto load = [&](const CUtensorMap* map, int row, int fill, bool is_v) {
+        if (!ok) return;
+        const int s = ld % kSlots;
+        ok = mbar_wait(&bars.empty[s], ((ld / kSlots) & 1) ^ 1, &abort_sh);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        uint8_t* dst = ring + s * S::kTileBytes;
+        // A last page's rows past the tokens may hold anything, and 0 * NaN is
+        // NaN: such a V tile is patched to zeros before it is handed on.
+        const bool patch = is_v && (fill & (kPage - 1)) != 0;
+        uint64_t* bar = patch ? &bars.tail : &bars.full[s];
+        if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
+        __syncwarp();
+        if (mine)
+          tma_load_2d(dst + ch * S::kChunkBytes + grp * kPage * 128, map, bar, kvh * HD + ch * 64, row, pol);
+        if (patch) {
+          ok = mbar_wait(bar, tails & 1, &abort_sh);
+          ok = __all_sync(0xffffffffu, ok);
+          ++tails;
+          if (ok) {
+            const int end = (fill + kPage - 1) / kPage * kPage;
+            for (int i = lane; i < (end - fill) * 8 * S::kChunks; i += 32) {
+              const int c = i / ((end - fill) * 8), j = i % ((end - fill) * 8);
+              *reinterpret_cast<uint4*>(dst + c * S::kChunkBytes + (fill + j / 8) * 128 + (j % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.full[s]);
+          }
+        }
+        ++ld;
+      };
+      const int ahead = dual ? 2 : 1;
+      int r_now = row_of(k_lo), r_next = 0;
+      load(&map_k, r_now, kKeys, false);
+      if (dual && n > 1) {
+        r_next = row_of(k_lo + 1);
+        load(&map_k, r_next, kKeys, false);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int r_new = i + ahead < n ? row_of(k_lo + i + ahead) : 0;
+        load(&map_v, r_now, filled(k_lo + i), true);
+        if (i + ahead < n) load(&map_k, r_new, kKeys, false);
+        r_now = dual ? r_next : r_new;
+        r_next = r_new;
+      }
+      if (!ok) {
+        if (lane == 0) {
+          abort_sh = 1;
+          report_status(p.status, LR_ERR_TIMEOUT);
+        }
+        // copies in flight land before the CTA's shared memory goes away
+        mbar_wait(&bars.q_full, 0, nullptr);
+        for (int i = ld > kSlots ? ld - kSlots : 0; i < ld; ++i) mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1, nullptr);
+        if (tails > 0) mbar_wait(&bars.tail, (tails - 1) & 1, nullptr);
+      }
+    }
+  } else if (warp == 9) {
+    // ----------------------------------------------------------- MMA
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
+      bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
+      tc_fence_after();
+      int ld = 0;
+      int done[2] = {0, 0};  // softmax rounds of each ring whose P was taken
+      auto slot_wait = [&](int l) {
+        if (ok) ok = mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh);
+        tc_fence_after();
+      };
+      auto qk = [&](int t, int l) {
+        if (!ok) return;
+        const uint32_t qa = smem_u32(q_sm + (dual ? 0 : t) * S::kTileBytes);
+        const uint32_t ka = smem_u32(ring + (l % kSlots) * S::kTileBytes);
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_bf16(tmem + t * kKeys, smem_desc_sw128(qa + c * S::kChunkBytes) + 2 * k,
+                        smem_desc_sw128(ka + c * S::kChunkBytes) + 2 * k, kIdS, (c | k) != 0 ? 1u : 0u);
+        tc_commit(&bars.s_full[t]);
+      };
+      auto pv = [&](int t, int l) {
+        if (ok) ok = mbar_wait(&bars.p_ready[t], done[t] & 1, &abort_sh);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t va = smem_u32(ring + (l % kSlots) * S::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc_mma_bf16_ta(tmem + 256 + t * HD, tmem + t * kKeys + k * 8,
+                         smem_desc_mn_sw128(va + k * 16 * 128, S::kChunkBytes), kIdO, (done[t] | k) != 0 ? 1u : 0u);
+        ++done[t];
+        if (done[t] == nt[t]) tc_commit(&bars.o_done[t]);
+      };
+      auto release = [&](int l) {
+        if (ok) tc_commit(&bars.empty[l % kSlots]);
+      };
+      slot_wait(0);
+      if (dual) {
+        qk(0, 0);
+        release(0);
+        ld = 1;
+        if (n > 1) {
+          slot_wait(1);
+          qk(1, 1);
+          release(1);
+          ld = 2;
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const int t = i & 1, lv = ld++;
+          slot_wait(lv);
+          pv(t, lv);
+          release(lv);
+          if (i + 2 < n) {
+            const int lk = ld++;
+            slot_wait(lk);
+            qk(t, lk);
+            release(lk);
+          }
+        }
+      } else {
+        for (int t = 0; t < 2; ++t)
+          if (nt[t] > 0) qk(t, 0);
+        release(0);
+        ld = 1;
+        for (int i = 0; i < n && ok; ++i) {
+          const int lv = ld++;
+          const bool more = i + 1 < n;
+          const int lk = more ? ld++ : 0;
+          slot_wait(lv);
+          for (int t = 0; t < 2; ++t) {
+            if (i < nt[t]) {
+              pv(t, lv);
+              if (i + 1 < nt[t]) {
+                slot_wait(lk);
+                qk(t, lk);
+              }
+            }
+          }
+          release(lv);
+          if (more) release(lk);
+        }
+      }
+      if (!ok) {
+        abort_sh = 1;
+        report_status(p.status, LR_ERR_TIMEOUT);
+      }
+      // every MMA issued by this thread completes before TMEM is released
+      tc_commit(&bars.drain);
+      mbar_wait(&bars.drain, 0, nullptr);
+    }
+  } else if (n > 0) {
+    // ------------------------------------------------------- softmax
+    const int t = ringi;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * HD + lanes;
+    // own tokens that this row sees (rows past the tile's are never stored)
+    const int m_row = mrel + tile * a.mt + trow / G;
+    const int vis = a.whole ? seen(m_row) : 0;
+    const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
+    bool ok = true;
+    for (int i = 0; i < nt[t] && ok; ++i) {
+      ok = mbar_wait(&bars.s_full[t], i & 1, &abort_sh);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (busy) {
+        const int k = k_lo + (dual ? 2 * i + t : i);
+        const int lim = k < np ? P - k * kKeys : vis - (k - np) * kKeys;
+        uint32_t s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
+        tmem_ld_wait();
+        if (__any_sync(0xffffffffu, lim < kKeys)) {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j)
+            if (j >= lim) s[j] = 0xFF800000u;  // -inf
+        }
+        float top = __uint_as_float(s[0]);
+#pragma unroll
+        for (int j = 1; j < kKeys; ++j) top = fmaxf(top, __uint_as_float(s[j]));
+        const float now = fmaxf(mref, top * p.scale_log2);
+        const bool move = now > mref + kSlack;  // -inf + 8 is -inf: the first key moves it
+        if (__any_sync(0xffffffffu, move)) {
+          const float next = move ? now : mref;
+          const float f = next == -INFINITY ? 1.f : ex2(mref - next);
+          sum *= f;
+          mref = next;
+          if (i > 0) {
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(o_at + c * 32, o);
+            }
+          }
+        }
+        const float neg = mref == -INFINITY ? 0.f : -mref;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKeys / 64; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * j]), p.scale_log2, neg));
+            const float y = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * j + 1]), p.scale_log2, neg));
+            part[(2 * j) & 3] += x;
+            part[(2 * j + 1) & 3] += y;
+            // the product takes bf16: the powers round here, their sum does not
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
+          }
+          tmem_st32(s_at + c * 32, w);
+        }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.p_ready[t]);
+    }
+    if (ok && nt[t] > 0) {
+      ok = mbar_wait(&bars.o_done[t], 0, &abort_sh);
+      // the ring is the other one's too: its products end before it is written below
+      if (ok && dual && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
+      tc_fence_after();
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0) {
+      abort_sh = 1;
+      report_status(p.status, LR_ERR_TIMEOUT);
+    }
+    if (ok && dual && t == 1 && nt[1] > 0 && busy) {  // ring 1 hands its part to ring 0
+      ml_sh[trow] = make_float2(mref, sum);
+      float* dst = reinterpret_cast<float*>(ring) + trow * (HD + 4);
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(o_at + c * 32, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<uint4*>(dst + c * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp < 8 && !(dual && ringi == 1) && abort_sh == 0) {
+    // ------------------------------------------------- rows to memory
+    const int t = ringi;
+    const bool busy = (warp & 3) * 32 < live_rows;
+    const bool live = trow < live_rows;
+    if (busy) {
+      const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const bool both = dual && nt[1] > 0;
+      float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
+      if (both) {
+        const float2 o = ml_sh[trow];
+        m = fmaxf(mref, o.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = ex2(mref - ref);
+        f1 = ex2(o.x - ref);
+        l = f0 * sum + f1 * o.y;
+      }
+      if (nt[t] == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
+      const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
+      const int head = kvh * G + trow % G;
+      const int64_t at = (static_cast<int64_t>(a.slot0 + split) * p.M + qrow) * p.n_heads + head;
+      if (a.direct) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        f0 *= inv;
+        f1 *= inv;
+      } else if (live) {
+        p.pml[at] = make_float2(m, l);
+      }
+      const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t r[32];
+        float x[32];
+        tmem_ld32(o_at + c * 32, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = f0 == 0.f ? 0.f : __uint_as_float(r[j]) * f0;
+        if (both) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(other + c * 32 + j);
+            x[j] = fmaf(y.x, f1, x[j]), x[j + 1] = fmaf(y.y, f1, x[j + 1]);
+            x[j + 2] = fmaf(y.z, f1, x[j + 2]), x[j + 3] = fmaf(y.w, f1, x[j + 3]);
+          }
+        }
+        if (!live) continue;
+        if (a.direct && !p.out_f32) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + qrow * p.ldo + head * HD + c * 32);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x[j + 2 * e + 1]), "f"(x[j + 2 * e]));
+            dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          float4* dst = a.direct ? reinterpret_cast<float4*>(static_cast<float*>(p.out) + qrow * p.ldo + head * HD + c * 32)
+                                 : reinterpret_cast<float4*>(p.po + at * HD + c * 32);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int HD>
+lr_status launch_tiles(const TileParams& a, dim3 grid, cudaStream_t s) {
+  using Sh = Shape<HD>;
+  CUtensorMap mq, mk, mv;
+  lr_status st = encode_map_heads(&mq, a.p.q, HD, a.p.n_heads, a.p.M, a.p.ldq, a.p.group, a.mt);
+  const uint64_t cols = static_cast<uint64_t>(a.p.n_kv) * HD;
+  if (st == LR_OK) st = encode_map_bf16(&mk, a.p.k, a.p.pool_rows, cols, a.p.ld, kPage);
+  if (st == LR_OK) st = encode_map_bf16(&mv, a.p.v, a.p.pool_rows, cols, a.p.ld, kPage);
+  if (st != LR_OK) return st;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Sh::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (pdl_enabled()) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<HD>, a, mq, mk, mv);
+  if (e != cudaSuccess) return cuda_fail(e, "attn_tiles");
+  return LR_OK;
+}
+
+}  // namespace
+
+lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s) {
+  TileParams a;
+  memset(&a, 0, sizeof(a));
+  a.p = p;
+  a.whole = part.whole;
+  a.mt = attn_tile_rows(p.group);
+  const int per_pair = 2 * a.mt;
+  a.pairs = ((part.whole ? p.max_q : p.M) + per_pair - 1) / per_pair;
+  a.slots = part.slots;
+  a.slot0 = part.slot0;
+  a.direct = part.whole && part.slots == 1;
+  a.stall = test_stall_producer();
+  const dim3 grid(part.whole ? a.pairs * p.n_seq : a.pairs, p.n_kv, part.slots);
+  return head_dim == 64 ? launch_tiles<64>(a, grid, s) : launch_tiles<128>(a, grid, s);
+}
+
+lr_status configure_attn_tiles() {
+  cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<64>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attn_tiles_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<128>::kSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "attention tiles: set smem");
+  return LR_OK;
+}
+
+}  // namespace lr
