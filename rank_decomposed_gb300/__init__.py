@@ -435,13 +435,64 @@ def kv_reconstruct_paged(latent_pool, blocks, n_blocks, Bt, out, status, stream=
 
 
 # ------------------------------------------------- attention over a context
+# These calls sit in a decode step whose kernels take a few microseconds, so
+# their checks read each tensor's properties once.
+_torch = None
+_raw_stream = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _stream_of(stream):
+    """The raw handle of `stream`, or of the current stream of the current device."""
+    global _raw_stream
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    if _raw_stream is None:
+        c = _th()._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+        else:
+            _raw_stream = lambda: _torch.cuda.current_stream().cuda_stream  # noqa: E731
+        _torch.cuda.init()
+    return _raw_stream()
+
+
 def _i32(t, name, dims=1):
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous():
+    if t.dtype != _th().int32 or t.dim() != dims or not t.is_contiguous():
         raise TypeError("%s must be a contiguous %d-D int32 tensor" % (name, dims))
     return t.data_ptr()
+
+
+def _per_row(t, name, m):
+    if t is None:
+        return None
+    if t.dtype != _th().int32 or t.shape != (m,) or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous int32 tensor with one entry a row" % name)
+    return t.data_ptr()
+
+
+def _mat(t, name, dtype, rows=None, cols=None):
+    """(pointer, row stride, rows, columns) of a row-major matrix of `dtype`."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError("%s must be a row-major 2-D tensor" % name)
+    n, w = shape
+    if (rows is not None and n != rows) or (cols is not None and w != cols):
+        raise ValueError("%s must be [%s][%s]" % (name, rows, cols))
+    # one row's stride says nothing: it counts as at least the row's width
+    ld = strides[0] if n > 1 or strides[0] >= w else (w + 7) // 8 * 8
+    return t.data_ptr(), ld, n, w
 
 
 def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0):
@@ -465,20 +516,23 @@ class HeadMap:
     rot_style: int = ROT_HALF
     cos_sin: object = None   # device fp32 [max_pos][rot_dim], see rope_table
 
+    def _gain(self, g, name):
+        if g is None:
+            return None
+        if g.dtype != _th().bfloat16 or g.shape != (self.head_dim,) or not g.is_contiguous():
+            raise TypeError("%s must be a contiguous bfloat16 [head_dim] tensor" % name)
+        return g.data_ptr()
+
     def c(self) -> HeadMapDesc:
-        import torch
-        for name, g in (("q_gain", self.q_gain), ("k_gain", self.k_gain)):
-            if g is not None and (g.dtype != torch.bfloat16 or tuple(g.shape) != (self.head_dim,)
-                                  or not g.is_contiguous()):
-                raise TypeError("%s must be a contiguous bfloat16 [head_dim] tensor" % name)
-        d = HeadMapDesc(self.head_dim, 1 if self.norm else 0, self.eps, _ptr(self.q_gain), _ptr(self.k_gain),
-                        self.rot_dim, self.rot_style, None, 0)
+        table, n = None, 0
         if self.rot_dim > 0 and self.cos_sin is not None:
             t = self.cos_sin
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != self.rot_dim or not t.is_contiguous():
+            n = t.shape[0]
+            if t.dtype != _th().float32 or t.shape != (n, self.rot_dim) or not t.is_contiguous():
                 raise TypeError("cos_sin must be a contiguous float32 [max_pos][rot_dim] tensor")
-            d.cos_sin, d.max_pos = t.data_ptr(), t.shape[0]
-        return d
+            table = t.data_ptr()
+        return HeadMapDesc(self.head_dim, 1 if self.norm else 0, self.eps, self._gain(self.q_gain, "q_gain"),
+                           self._gain(self.k_gain, "k_gain"), self.rot_dim, self.rot_style, table, n)
 
 
 @dataclass
@@ -491,62 +545,29 @@ class PagedKV:
     block_rows: int = 16
 
     def c(self) -> KvCache:
-        _bf16(self.k_pool, "k_pool")
-        _bf16(self.v_pool, "v_pool")
-        if self.k_pool.shape != self.v_pool.shape or self.k_pool.stride(0) != self.v_pool.stride(0):
-            raise ValueError("k_pool and v_pool must have one shape and row stride")
-        if self.k_pool.shape[1] < self.n_kv_heads * self.head_dim:
+        bf16 = _th().bfloat16
+        kp, ld, n, w = _mat(self.k_pool, "k_pool", bf16)
+        vp, ldv, _, _ = _mat(self.v_pool, "v_pool", bf16, n, w)
+        if ldv != ld:
+            raise ValueError("k_pool and v_pool must have one row stride")
+        if w < self.n_kv_heads * self.head_dim:
             raise ValueError("the pools' rows are narrower than n_kv_heads * head_dim")
-        if self.block_rows <= 0 or self.k_pool.shape[0] % self.block_rows:
+        br = self.block_rows
+        if br <= 0 or n % br:
             raise ValueError("the pools' rows must be whole pages of block_rows")
-        return KvCache(self.k_pool.data_ptr(), self.v_pool.data_ptr(), self.k_pool.stride(0),
-                       self.k_pool.shape[0] // self.block_rows, self.block_rows, self.n_kv_heads, self.head_dim)
+        return KvCache(kp, vp, ld, n // br, br, self.n_kv_heads, self.head_dim)
 
 
-def _ld(t):
-    """Row stride; one row's stride says nothing, so it counts as at least its width."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+def _dtype_code(t):
+    torch = _th()
+    if t.dtype == torch.bfloat16:
+        return LR_BF16
+    if t.dtype == torch.float32:
+        return LR_F32
+    raise TypeError("a tensor of heads must be bfloat16 or float32")
 
 
-def _rows_in(named, head_dim):
-    """(dtype code, row count) of the given [M][heads * head_dim] inputs, which must agree."""
-    import torch
-    first = None
-    for name, t in named:
-        if t is None:
-            continue
-        if t.dim() != 2 or t.stride(1) != 1:
-            raise ValueError("%s must be a row-major 2-D tensor" % name)
-        if head_dim <= 0 or t.shape[1] % head_dim:
-            raise ValueError("%s: the width is not whole heads of head_dim" % name)
-        if first is None:
-            first = t
-        elif t.dtype != first.dtype or t.shape[0] != first.shape[0]:
-            raise ValueError("%s: inputs disagree on dtype or rows" % name)
-    if first is None:
-        raise ValueError("no input given")
-    code = {torch.bfloat16: LR_BF16, torch.float32: LR_F32}.get(first.dtype)
-    if code is None:
-        raise TypeError("inputs must be bfloat16 or float32")
-    return code, first.shape[0]
-
-
-def _head_out(x, out, name):
-    if x is None:
-        return None, 0, 0, None, 0
-    if out is None:
-        raise ValueError("%s is missing" % name)
-    _bf16(out, name)
-    if out.shape != x.shape:
-        raise ValueError("%s must have its input's shape" % name)
-    return x.data_ptr(), _ld(x), x.shape[1], out.data_ptr(), _ld(out)
-
-
-def _per_row(t, name, m):
-    p = _i32(t, name)
-    if t is not None and t.shape[0] != m:
-        raise ValueError("%s must have one entry a row" % name)
-    return p
+_NONE = (None, 0, None, 0)
 
 
 def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None, stream=None):
@@ -554,51 +575,64 @@ def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None,
 
     In place (q_out is q, k_out is k) is allowed for bf16 inputs.
     """
-    code, m = _rows_in((("q", q), ("k", k)), heads.head_dim)
-    qp, ldq, wq, qo, ldqo = _head_out(q, q_out, "q_out")
-    kp, ldk, wk, ko, ldko = _head_out(k, k_out, "k_out")
-    hm = heads.c()
-    st = lib.lr_qk_norm_rope(qp, ldq, wq // heads.head_dim, kp, ldk, wk // heads.head_dim, code, m,
-                             _per_row(pos, "pos", m), _i32(n_active, "n_active"), ctypes.byref(hm), qo, ldqo, ko,
-                             ldko, _ptr(status), _stream(stream))
-    _check("lr_qk_norm_rope", st)
+    hd = heads.head_dim
+    first = q if q is not None else k
+    if first is None or hd <= 0:
+        raise ValueError("qk_norm_rope: q or k and a positive head_dim are needed")
+    code, dt, bf16, m = _dtype_code(first), first.dtype, _torch.bfloat16, None
+    (qp, ldq, wq, _), (qo, ldqo), (kp, ldk, wk, _), (ko, ldko) = _NONE, (None, 0), _NONE, (None, 0)
+    wq = wk = 0
+    if q is not None:
+        qp, ldq, m, wq = _mat(q, "q", dt)
+        qo, ldqo, _, _ = _mat(q_out, "q_out", bf16, m, wq)
+    if k is not None:
+        kp, ldk, m, wk = _mat(k, "k", dt, m)
+        ko, ldko, _, _ = _mat(k_out, "k_out", bf16, m, wk)
+    if wq % hd or wk % hd:
+        raise ValueError("qk_norm_rope: a width is not whole heads of head_dim")
+    st = lib.lr_qk_norm_rope(qp, ldq, wq // hd, kp, ldk, wk // hd, code, m, _per_row(pos, "pos", m),
+                             _i32(n_active, "n_active"), ctypes.byref(heads.c()), qo, ldqo, ko, ldko, _ptr(status),
+                             _stream_of(stream))
+    if st != LR_OK:
+        _check("lr_qk_norm_rope", st)
 
 
 def kv_append(k, v, pos, rows, heads: HeadMap, cache: PagedKV, status, q=None, q_out=None, n_active=None,
               stream=None):
     """cache rows rows[m] = (norm and rotation of k[m], v[m]); with q also q_out as qk_norm_rope. One launch."""
-    code, m = _rows_in((("k", k), ("v", v), ("q", q)), heads.head_dim)
-    width = cache.n_kv_heads * cache.head_dim
-    if k.shape[1] != width or v.shape[1] != width:
-        raise ValueError("k and v must be [M][n_kv_heads * head_dim]")
-    qp, ldq, wq, qo, ldqo = _head_out(q, q_out, "q_out")
-    hm, cc = heads.c(), cache.c()
-    st = lib.lr_kv_append(k.data_ptr(), _ld(k), v.data_ptr(), _ld(v), qp, ldq, wq // heads.head_dim, code,
-                          m, _per_row(pos, "pos", m), _per_row(rows, "rows", m), _i32(n_active, "n_active"),
-                          ctypes.byref(hm), ctypes.byref(cc), qo, ldqo, _ptr(status), _stream(stream))
-    _check("lr_kv_append", st)
+    hd = heads.head_dim
+    code, dt = _dtype_code(k), k.dtype
+    kp, ldk, m, w = _mat(k, "k", dt, None, cache.n_kv_heads * cache.head_dim)
+    vp, ldv, _, _ = _mat(v, "v", dt, m, w)
+    qp, ldq, wq, qo, ldqo = None, 0, 0, None, 0
+    if q is not None:
+        qp, ldq, _, wq = _mat(q, "q", dt, m)
+        qo, ldqo, _, _ = _mat(q_out, "q_out", _torch.bfloat16, m, wq)
+        if hd <= 0 or wq % hd:
+            raise ValueError("kv_append: q's width is not whole heads of head_dim")
+        wq //= hd
+    st = lib.lr_kv_append(kp, ldk, vp, ldv, qp, ldq, wq, code, m, _per_row(pos, "pos", m), _per_row(rows, "rows", m),
+                          _i32(n_active, "n_active"), ctypes.byref(heads.c()), ctypes.byref(cache.c()), qo, ldqo,
+                          _ptr(status), _stream_of(stream))
+    if st != LR_OK:
+        _check("lr_kv_append", st)
 
 
-def _attn_desc(M, n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale):
-    d = AttnDesc()
-    d.cache = cache.c()
-    d.n_heads = n_heads
-    d.scale = cache.head_dim ** -0.5 if scale is None else scale
-    d.prefix_blocks, d.prefix_len = _i32(prefix_blocks, "prefix_blocks"), _i32(prefix_len, "prefix_len")
-    d.cap_prefix_blocks = 0 if prefix_blocks is None else prefix_blocks.shape[0]
-    d.lengths, d.n_seq = _i32(lengths, "lengths"), lengths.shape[0]
-    d.block_table, d.blocks_per_seq = _i32(block_table, "block_table", 2), block_table.shape[1]
-    if block_table.shape[0] != lengths.shape[0]:
+def _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale):
+    n_seq = lengths.shape[0]
+    if block_table.shape[0] != n_seq:
         raise ValueError("block_table must be [n_seq][blocks_per_seq]")
-    d.q_start, d.max_q = _i32(q_start, "q_start"), max_q
-    if q_start is not None and q_start.shape[0] != lengths.shape[0] + 1:
+    if q_start is not None and q_start.shape[0] != n_seq + 1:
         raise ValueError("q_start must have n_seq + 1 entries")
-    return d
+    return AttnDesc(cache.c(), n_heads, cache.head_dim ** -0.5 if scale is None else scale,
+                    _i32(prefix_blocks, "prefix_blocks"), 0 if prefix_blocks is None else prefix_blocks.shape[0],
+                    _i32(prefix_len, "prefix_len"), n_seq, _i32(q_start, "q_start"), max_q,
+                    _i32(block_table, "block_table", 2), block_table.shape[1], _i32(lengths, "lengths"))
 
 
 def prefix_attention_workspace_bytes(M: int, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len, block_table,
                                      lengths, q_start=None, max_q: int = 1) -> int:
-    d = _attn_desc(M, n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, None)
+    d = _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, None)
     return int(lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(d)))
 
 
@@ -609,21 +643,14 @@ def prefix_attention(q, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len,
     q: bf16 [M][n_heads * head_dim]; out: bf16 or fp32, the same shape.  Sequence b's rows are
     q_start[b]..q_start[b + 1] - 1 (row b without q_start), its last own tokens.
     """
-    import torch
-    _bf16(q, "q")
-    if out.dim() != 2 or out.stride(1) != 1 or out.shape != q.shape:
-        raise ValueError("out must be a row-major tensor of q's shape")
-    if q.shape[1] != n_heads * cache.head_dim:
-        raise ValueError("q must be [M][n_heads * head_dim]")
-    odt = {torch.bfloat16: LR_BF16, torch.float32: LR_F32}.get(out.dtype)
-    if odt is None:
-        raise TypeError("out must be bfloat16 or float32")
-    d = _attn_desc(q.shape[0], n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale)
-    st = lib.lr_prefix_attention(q.data_ptr(), _ld(q), out.data_ptr(), _ld(out), odt, q.shape[0],
-                                 ctypes.byref(d), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                 _ptr(status), _stream(stream))
-    _check("lr_prefix_attention", st)
+    odt = _dtype_code(out)
+    qp, ldq, m, w = _mat(q, "q", _torch.bfloat16, None, n_heads * cache.head_dim)
+    op, ldo, _, _ = _mat(out, "out", out.dtype, m, w)
+    d = _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale)
+    st = lib.lr_prefix_attention(qp, ldq, op, ldo, odt, m, ctypes.byref(d), _ptr(workspace),
+                                 0 if workspace is None else workspace.nbytes, _ptr(status), _stream_of(stream))
+    if st != LR_OK:
+        _check("lr_prefix_attention", st)
 
 
 # ---------------------------------------------------------------- stack

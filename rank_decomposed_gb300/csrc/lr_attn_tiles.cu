@@ -32,7 +32,10 @@
 namespace lr {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;        // 8 softmax warps, a producer, an MMA issuer, two idle
+// Registers: the launch gives 168 a thread; the softmax warps hold a row of
+// 128 scores and take what the other four leave (256 * 208 + 128 * 88 = 384 * 168).
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kKeys = 128;           // keys per tile
 constexpr int kPage = 16;            // rows per TMA box
 constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 each), O0, O1 (head_dim each)
@@ -120,6 +123,40 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
   return d;
 }
 
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two fp32 values as one operand of the packed instructions.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 struct Bars {
   uint64_t q_full;
   uint64_t full[10], empty[10];
@@ -190,35 +227,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   if (nq - mrel <= 0) return;
-  int nrow[2];  // query rows of each tile
-  nrow[0] = nq - mrel < a.mt ? nq - mrel : a.mt;
-  nrow[1] = nq - mrel - a.mt < a.mt ? nq - mrel - a.mt : a.mt;
-  if (nrow[1] < 0) nrow[1] = 0;
-  const bool dual = nrow[1] == 0;  // one row tile, both rings
+  // query rows of each tile
+  const int rows0 = nq - mrel < a.mt ? nq - mrel : a.mt;
+  const int left = nq - mrel - a.mt;
+  const int rows1 = left < 0 ? 0 : (left < a.mt ? left : a.mt);
+  const bool dual = rows1 == 0;  // one row tile, both rings
   // own tokens that a tile's last row sees
   auto seen = [&](int m) {
     const int v = own - nq + m + 1;
     return v < 0 ? 0 : v;
   };
   const int np = (P + kKeys - 1) / kKeys;
-  const int see0 = a.whole ? seen(mrel + nrow[0] - 1) : 0;
-  const int see1 = a.whole && !dual ? seen(mrel + a.mt + nrow[1] - 1) : 0;
+  const int see0 = a.whole ? seen(mrel + rows0 - 1) : 0;
+  const int see1 = a.whole && !dual ? seen(mrel + a.mt + rows1 - 1) : 0;
   const int see = see0 > see1 ? see0 : see1;
   const int t_all = np + (see + kKeys - 1) / kKeys;
   const int per = (t_all + a.slots - 1) / a.slots;
   const int k_lo = split * per;
   const int k_hi = k_lo + per < t_all ? k_lo + per : t_all;
   const int n = k_hi > k_lo ? k_hi - k_lo : 0;     // key tiles of this CTA
-  int nt[2];                                       // and of each ring
+  int n0, n1;                                      // and of each ring
   if (dual) {
-    nt[0] = (n + 1) >> 1;
-    nt[1] = n >> 1;
+    n0 = (n + 1) >> 1;
+    n1 = n >> 1;
   } else {
     const int e0 = np + (see0 + kKeys - 1) / kKeys, e1 = np + (see1 + kKeys - 1) / kKeys;
-    nt[0] = (e0 < k_hi ? e0 : k_hi) - k_lo;
-    nt[1] = (e1 < k_hi ? e1 : k_hi) - k_lo;
-    if (nt[0] < 0) nt[0] = 0;
-    if (nt[1] < 0) nt[1] = 0;
+    n0 = (e0 < k_hi ? e0 : k_hi) - k_lo;
+    n1 = (e1 < k_hi ? e1 : k_hi) - k_lo;
+    if (n0 < 0) n0 = 0;
+    if (n1 < 0) n1 = 0;
   }
 
   if (warp == 9) {
@@ -234,300 +271,319 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ringi = warp >> 2;                     // 0, 1: softmax warps
   const int trow = threadIdx.x & 127;
   const int tile = dual ? 0 : (ringi & 1);
-  const int live_rows = nrow[tile] * G;
+  const int live_rows = (tile ? rows1 : rows0) * G;
+  const int my_n = (ringi & 1) ? n1 : n0;
   float mref = -INFINITY, sum = 0.f;
 
-  if (warp == 8) {
-    // ------------------------------------------------------ producer
-    if (lane == 0) {
-      prefetch_tensormap(&map_q);
-      prefetch_tensormap(&map_k);
-      prefetch_tensormap(&map_v);
-    }
-    const uint64_t pol = l2_policy_evict_last();
-    if (!a.stall && n > 0) {
+  if (warp >= 8) {
+    regs_fewer<kRegsOther>();
+    if (warp == 8) {
+      // ------------------------------------------------------ producer
       if (lane == 0) {
-        const uint32_t bytes = static_cast<uint32_t>(a.mt * G * 128 * S::kChunks) * (dual ? 1u : 2u);
-        mbar_arrive_expect_tx(&bars.q_full, bytes);
-        for (int t = 0; t < (dual ? 1 : 2); ++t)
-          for (int c = 0; c < S::kChunks; ++c)
-            tma_load_3d(q_sm + t * S::kTileBytes + c * S::kChunkBytes, &map_q, &bars.q_full, c * 64, kvh * G,
-                        q0 + mrel + t * a.mt, pol);
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
       }
-      const int grp = lane / S::kChunks, ch = lane % S::kChunks;
-      const bool mine = grp < kKeys / kPage;
-      // pool row of this lane's 16 keys of tile k; past the pool (reads as zeros) where there are none
-      auto row_of = [&](int k) {
-        int t, limit;
-        const int32_t* pages;
-        if (k < np) {
-          t = k * kKeys + grp * kPage, limit = P, pages = p.prefix_blocks;
-        } else {
-          t = (k - np) * kKeys + grp * kPage, limit = see, pages = own_pages;
+      const uint64_t pol = l2_policy_evict_last();
+      if (!a.stall && n > 0) {
+        if (lane == 0) {
+          const uint32_t bytes = static_cast<uint32_t>(a.mt * G * 128 * S::kChunks) * (dual ? 1u : 2u);
+          mbar_arrive_expect_tx(&bars.q_full, bytes);
+          for (int t = 0; t < (dual ? 1 : 2); ++t)
+            for (int c = 0; c < S::kChunks; ++c)
+              tma_load_3d(q_sm + t * S::kTileBytes + c * S::kChunkBytes, &map_q, &bars.q_full, c * 64, kvh * G,
+                          q0 + mrel + t * a.mt, pol);
         }
-        int64_t row = p.pool_rows;
-        if (mine && t < limit) {
-          const int64_t page = pages[t / p.block_rows];
-          if (page < 0 || page >= p.pool_blocks)
-            report_status(p.status, LR_ERR_REMAP_RANGE);
-          else
-            row = page * p.block_rows + t % p.block_rows;
-        }
-        return static_cast<int32_t>(row);
-      };
-      int ld = 0, tails = 0;
-      bool ok = true;
-      // keys of tile k that hold tokens
-      auto filled = [&](int k) {
-        const int f = k < np ? P - k * kKeys : see - (k - np) * kKeys;
-        return f < kKeys ? f : kKeys;
-      };
-      auto load = [&](const CUtensorMap* map, int row, int fill, bool is_v) {
-        if (!ok) return;
-        const int s = ld % kSlots;
-        ok = mbar_wait(&bars.empty[s], ((ld / kSlots) & 1) ^ 1, &abort_sh);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        uint8_t* dst = ring + s * S::kTileBytes;
-        // A last page's rows past the tokens may hold anything, and 0 * NaN is
-        // NaN: such a V tile is patched to zeros before it is handed on.
-        const bool patch = is_v && (fill & (kPage - 1)) != 0;
-        uint64_t* bar = patch ? &bars.tail : &bars.full[s];
-        if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
-        __syncwarp();
-        if (mine)
-          tma_load_2d(dst + ch * S::kChunkBytes + grp * kPage * 128, map, bar, kvh * HD + ch * 64, row, pol);
-        if (patch) {
-          ok = mbar_wait(bar, tails & 1, &abort_sh);
+        const int grp = lane / S::kChunks, ch = lane % S::kChunks;
+        const bool mine = grp < kKeys / kPage;
+        // pool row of this lane's 16 keys of tile k; past the pool (reads as zeros) where there are none
+        auto row_of = [&](int k) {
+          int t, limit;
+          const int32_t* pages;
+          if (k < np) {
+            t = k * kKeys + grp * kPage, limit = P, pages = p.prefix_blocks;
+          } else {
+            t = (k - np) * kKeys + grp * kPage, limit = see, pages = own_pages;
+          }
+          int64_t row = p.pool_rows;
+          if (mine && t < limit) {
+            const int64_t page = pages[t / p.block_rows];
+            if (page < 0 || page >= p.pool_blocks)
+              report_status(p.status, LR_ERR_REMAP_RANGE);
+            else
+              row = page * p.block_rows + t % p.block_rows;
+          }
+          return static_cast<int32_t>(row);
+        };
+        int ld = 0, tails = 0;
+        bool ok = true;
+        // keys of tile k that hold tokens
+        auto filled = [&](int k) {
+          const int f = k < np ? P - k * kKeys : see - (k - np) * kKeys;
+          return f < kKeys ? f : kKeys;
+        };
+        auto load = [&](const CUtensorMap* map, int row, int fill, bool is_v) {
+          if (!ok) return;
+          const int s = ld % kSlots;
+          ok = mbar_wait(&bars.empty[s], ((ld / kSlots) & 1) ^ 1, &abort_sh);
           ok = __all_sync(0xffffffffu, ok);
-          ++tails;
-          if (ok) {
-            const int end = (fill + kPage - 1) / kPage * kPage;
-            for (int i = lane; i < (end - fill) * 8 * S::kChunks; i += 32) {
-              const int c = i / ((end - fill) * 8), j = i % ((end - fill) * 8);
-              *reinterpret_cast<uint4*>(dst + c * S::kChunkBytes + (fill + j / 8) * 128 + (j % 8) * 16) =
-                  make_uint4(0, 0, 0, 0);
+          if (!ok) return;
+          uint8_t* dst = ring + s * S::kTileBytes;
+          // A last page's rows past the tokens may hold anything, and 0 * NaN is
+          // NaN: such a V tile is patched to zeros before it is handed on.
+          const bool patch = is_v && (fill & (kPage - 1)) != 0;
+          uint64_t* bar = patch ? &bars.tail : &bars.full[s];
+          if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
+          __syncwarp();
+          if (mine)
+            tma_load_2d(dst + ch * S::kChunkBytes + grp * kPage * 128, map, bar, kvh * HD + ch * 64, row, pol);
+          if (patch) {
+            ok = mbar_wait(bar, tails & 1, &abort_sh);
+            ok = __all_sync(0xffffffffu, ok);
+            ++tails;
+            if (ok) {
+              const int end = (fill + kPage - 1) / kPage * kPage;
+              for (int i = lane; i < (end - fill) * 8 * S::kChunks; i += 32) {
+                const int c = i / ((end - fill) * 8), j = i % ((end - fill) * 8);
+                *reinterpret_cast<uint4*>(dst + c * S::kChunkBytes + (fill + j / 8) * 128 + (j % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.full[s]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.full[s]);
+          }
+          ++ld;
+        };
+        const int ahead = dual ? 2 : 1;
+        int r_now = row_of(k_lo), r_next = 0;
+        load(&map_k, r_now, kKeys, false);
+        if (dual && n > 1) {
+          r_next = row_of(k_lo + 1);
+          load(&map_k, r_next, kKeys, false);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const int r_new = i + ahead < n ? row_of(k_lo + i + ahead) : 0;
+          load(&map_v, r_now, filled(k_lo + i), true);
+          if (i + ahead < n) load(&map_k, r_new, kKeys, false);
+          r_now = dual ? r_next : r_new;
+          r_next = r_new;
+        }
+        if (!ok) {
+          if (lane == 0) {
+            abort_sh = 1;
+            report_status(p.status, LR_ERR_TIMEOUT);
+          }
+          // copies in flight land before the CTA's shared memory goes away
+          mbar_wait(&bars.q_full, 0, nullptr);
+          for (int i = ld > kSlots ? ld - kSlots : 0; i < ld; ++i) mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1, nullptr);
+          if (tails > 0) mbar_wait(&bars.tail, (tails - 1) & 1, nullptr);
+        }
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------------------- MMA
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
+        constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
+        bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
+        tc_fence_after();
+        int ld = 0;
+        auto slot_wait = [&](int l) {
+          if (ok) ok = mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh);
+          tc_fence_after();
+        };
+        auto qk = [&](int t, int l) {
+          if (!ok) return;
+          const uint64_t qa = smem_desc_sw128(smem_u32(q_sm + (dual ? 0 : t) * S::kTileBytes));
+          const uint64_t ka = smem_desc_sw128(smem_u32(ring + (l % kSlots) * S::kTileBytes));
+#pragma unroll
+          for (int c = 0; c < S::kChunks; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc_mma_bf16(tmem + t * kKeys, qa + (c * S::kChunkBytes >> 4) + 2 * k, ka + (c * S::kChunkBytes >> 4) + 2 * k,
+                          kIdS, (c | k) != 0 ? 1u : 0u);
+          tc_commit(&bars.s_full[t]);
+        };
+        // round r of ring t; its last one completes the ring's O
+        auto pv = [&](int t, int l, int r, bool last) {
+          if (ok) ok = mbar_wait(&bars.p_ready[t], r & 1, &abort_sh);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t va = smem_desc_mn_sw128(smem_u32(ring + (l % kSlots) * S::kTileBytes), S::kChunkBytes);
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc_mma_bf16_ta(tmem + 256 + t * HD, tmem + t * kKeys + k * 8, va + (k * 16 * 128 >> 4), kIdO,
+                           (r | k) != 0 ? 1u : 0u);
+          if (last) tc_commit(&bars.o_done[t]);
+        };
+        auto release = [&](int l) {
+          if (ok) tc_commit(&bars.empty[l % kSlots]);
+        };
+        slot_wait(0);
+        if (dual) {
+          qk(0, 0);
+          release(0);
+          ld = 1;
+          if (n > 1) {
+            slot_wait(1);
+            qk(1, 1);
+            release(1);
+            ld = 2;
+          }
+          for (int i = 0; i < n && ok; ++i) {
+            const int t = i & 1, lv = ld++;
+            slot_wait(lv);
+            pv(t, lv, i >> 1, i + 2 >= n);
+            release(lv);
+            if (i + 2 < n) {
+              const int lk = ld++;
+              slot_wait(lk);
+              qk(t, lk);
+              release(lk);
+            }
+          }
+        } else {
+          if (n0 > 0) qk(0, 0);
+          if (n1 > 0) qk(1, 0);
+          release(0);
+          ld = 1;
+          for (int i = 0; i < n && ok; ++i) {
+            const int lv = ld++;
+            const bool more = i + 1 < n;
+            const int lk = more ? ld++ : 0;
+            slot_wait(lv);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int mine = t ? n1 : n0;
+              if (i < mine) {
+                pv(t, lv, i, i + 1 == mine);
+                if (i + 1 < mine) {
+                  slot_wait(lk);
+                  qk(t, lk);
+                }
+              }
+            }
+            release(lv);
+            if (more) release(lk);
           }
         }
-        ++ld;
-      };
-      const int ahead = dual ? 2 : 1;
-      int r_now = row_of(k_lo), r_next = 0;
-      load(&map_k, r_now, kKeys, false);
-      if (dual && n > 1) {
-        r_next = row_of(k_lo + 1);
-        load(&map_k, r_next, kKeys, false);
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const int r_new = i + ahead < n ? row_of(k_lo + i + ahead) : 0;
-        load(&map_v, r_now, filled(k_lo + i), true);
-        if (i + ahead < n) load(&map_k, r_new, kKeys, false);
-        r_now = dual ? r_next : r_new;
-        r_next = r_new;
-      }
-      if (!ok) {
-        if (lane == 0) {
+        if (!ok) {
           abort_sh = 1;
           report_status(p.status, LR_ERR_TIMEOUT);
         }
-        // copies in flight land before the CTA's shared memory goes away
-        mbar_wait(&bars.q_full, 0, nullptr);
-        for (int i = ld > kSlots ? ld - kSlots : 0; i < ld; ++i) mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1, nullptr);
-        if (tails > 0) mbar_wait(&bars.tail, (tails - 1) & 1, nullptr);
+        // every MMA issued by this thread completes before TMEM is released
+        tc_commit(&bars.drain);
+        mbar_wait(&bars.drain, 0, nullptr);
       }
     }
-  } else if (warp == 9) {
-    // ----------------------------------------------------------- MMA
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
-      constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
-      bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
-      tc_fence_after();
-      int ld = 0;
-      int done[2] = {0, 0};  // softmax rounds of each ring whose P was taken
-      auto slot_wait = [&](int l) {
-        if (ok) ok = mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh);
+  } else {
+    regs_more<kRegsSoftmax>();
+    if (n > 0) {
+      // ------------------------------------------------------- softmax
+      const int t = ringi;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * HD + lanes;
+      // own tokens that this row sees (rows past the tile's are never stored)
+      const int m_row = mrel + tile * a.mt + trow / G;
+      const int vis = a.whole ? seen(m_row) : 0;
+      const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
+      bool ok = true;
+      for (int i = 0; i < my_n && ok; ++i) {
+        ok = mbar_wait(&bars.s_full[t], i & 1, &abort_sh);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tc_fence_after();
-      };
-      auto qk = [&](int t, int l) {
-        if (!ok) return;
-        const uint32_t qa = smem_u32(q_sm + (dual ? 0 : t) * S::kTileBytes);
-        const uint32_t ka = smem_u32(ring + (l % kSlots) * S::kTileBytes);
+        if (busy) {
+          const int k = k_lo + (dual ? 2 * i + t : i);
+          const int lim = k < np ? P - k * kKeys : vis - (k - np) * kKeys;
+          uint32_t s[kKeys];
 #pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
+          for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
+          tmem_ld_wait();
+          if (__any_sync(0xffffffffu, lim < kKeys)) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_bf16(tmem + t * kKeys, smem_desc_sw128(qa + c * S::kChunkBytes) + 2 * k,
-                        smem_desc_sw128(ka + c * S::kChunkBytes) + 2 * k, kIdS, (c | k) != 0 ? 1u : 0u);
-        tc_commit(&bars.s_full[t]);
-      };
-      auto pv = [&](int t, int l) {
-        if (ok) ok = mbar_wait(&bars.p_ready[t], done[t] & 1, &abort_sh);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t va = smem_u32(ring + (l % kSlots) * S::kTileBytes);
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc_mma_bf16_ta(tmem + 256 + t * HD, tmem + t * kKeys + k * 8,
-                         smem_desc_mn_sw128(va + k * 16 * 128, S::kChunkBytes), kIdO, (done[t] | k) != 0 ? 1u : 0u);
-        ++done[t];
-        if (done[t] == nt[t]) tc_commit(&bars.o_done[t]);
-      };
-      auto release = [&](int l) {
-        if (ok) tc_commit(&bars.empty[l % kSlots]);
-      };
-      slot_wait(0);
-      if (dual) {
-        qk(0, 0);
-        release(0);
-        ld = 1;
-        if (n > 1) {
-          slot_wait(1);
-          qk(1, 1);
-          release(1);
-          ld = 2;
-        }
-        for (int i = 0; i < n && ok; ++i) {
-          const int t = i & 1, lv = ld++;
-          slot_wait(lv);
-          pv(t, lv);
-          release(lv);
-          if (i + 2 < n) {
-            const int lk = ld++;
-            slot_wait(lk);
-            qk(t, lk);
-            release(lk);
+            for (int j = 0; j < kKeys; ++j)
+              if (j >= lim) s[j] = 0xFF800000u;  // -inf
           }
-        }
-      } else {
-        for (int t = 0; t < 2; ++t)
-          if (nt[t] > 0) qk(t, 0);
-        release(0);
-        ld = 1;
-        for (int i = 0; i < n && ok; ++i) {
-          const int lv = ld++;
-          const bool more = i + 1 < n;
-          const int lk = more ? ld++ : 0;
-          slot_wait(lv);
-          for (int t = 0; t < 2; ++t) {
-            if (i < nt[t]) {
-              pv(t, lv);
-              if (i + 1 < nt[t]) {
-                slot_wait(lk);
-                qk(t, lk);
+          float tops[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tops[j] = fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 4]));
+#pragma unroll
+          for (int j = 8; j < kKeys; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + e + 4]));
+          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+          const float now = fmaxf(mref, top * p.scale_log2);
+          const bool move = now > mref + kSlack;  // -inf + 8 is -inf: the first key moves it
+          if (__any_sync(0xffffffffu, move)) {
+            const float next = move ? now : mref;
+            const float f = next == -INFINITY ? 1.f : ex2(mref - next);
+            sum *= f;
+            mref = next;
+            if (i > 0) {
+#pragma unroll
+              for (int c = 0; c < HD / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_at + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(o_at + c * 32, o);
               }
             }
           }
-          release(lv);
-          if (more) release(lk);
+          const float neg = mref == -INFINITY ? 0.f : -mref;
+          const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), neg2 = pack2(neg, neg);
+          uint64_t part[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < kKeys / 64; ++c) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint64_t e =
+                  fma2(pack2(__uint_as_float(s[c * 64 + 2 * j]), __uint_as_float(s[c * 64 + 2 * j + 1])), scale2, neg2);
+              float x, y;
+              unpack2(e, x, y);
+              x = ex2(x);
+              y = ex2(y);
+              part[j & 1] = add2(part[j & 1], pack2(x, y));
+              // the product takes bf16: the powers round here, their sum does not
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
+            }
+            tmem_st32(s_at + c * 32, w);
+          }
+          float pa, pb;
+          unpack2(add2(part[0], part[1]), pa, pb);
+          sum += pa + pb;
+          tmem_st_wait();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_ready[t]);
       }
-      if (!ok) {
+      if (ok && my_n > 0) {
+        ok = mbar_wait(&bars.o_done[t], 0, &abort_sh);
+        // the ring is the other one's too: its products end before it is written below
+        if (ok && dual && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
+        tc_fence_after();
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) {
         abort_sh = 1;
         report_status(p.status, LR_ERR_TIMEOUT);
       }
-      // every MMA issued by this thread completes before TMEM is released
-      tc_commit(&bars.drain);
-      mbar_wait(&bars.drain, 0, nullptr);
-    }
-  } else if (n > 0) {
-    // ------------------------------------------------------- softmax
-    const int t = ringi;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * HD + lanes;
-    // own tokens that this row sees (rows past the tile's are never stored)
-    const int m_row = mrel + tile * a.mt + trow / G;
-    const int vis = a.whole ? seen(m_row) : 0;
-    const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
-    bool ok = true;
-    for (int i = 0; i < nt[t] && ok; ++i) {
-      ok = mbar_wait(&bars.s_full[t], i & 1, &abort_sh);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      if (busy) {
-        const int k = k_lo + (dual ? 2 * i + t : i);
-        const int lim = k < np ? P - k * kKeys : vis - (k - np) * kKeys;
-        uint32_t s[kKeys];
+      if (ok && dual && t == 1 && n1 > 0 && busy) {  // ring 1 hands its part to ring 0
+        ml_sh[trow] = make_float2(mref, sum);
+        float* dst = reinterpret_cast<float*>(ring) + trow * (HD + 4);
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
-        tmem_ld_wait();
-        if (__any_sync(0xffffffffu, lim < kKeys)) {
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_at + c * 32, o);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j)
-            if (j >= lim) s[j] = 0xFF800000u;  // -inf
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<uint4*>(dst + c * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
-        float top = __uint_as_float(s[0]);
-#pragma unroll
-        for (int j = 1; j < kKeys; ++j) top = fmaxf(top, __uint_as_float(s[j]));
-        const float now = fmaxf(mref, top * p.scale_log2);
-        const bool move = now > mref + kSlack;  // -inf + 8 is -inf: the first key moves it
-        if (__any_sync(0xffffffffu, move)) {
-          const float next = move ? now : mref;
-          const float f = next == -INFINITY ? 1.f : ex2(mref - next);
-          sum *= f;
-          mref = next;
-          if (i > 0) {
-#pragma unroll
-            for (int c = 0; c < HD / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_at + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(o_at + c * 32, o);
-            }
-          }
-        }
-        const float neg = mref == -INFINITY ? 0.f : -mref;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < kKeys / 64; ++c) {
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float x = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * j]), p.scale_log2, neg));
-            const float y = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * j + 1]), p.scale_log2, neg));
-            part[(2 * j) & 3] += x;
-            part[(2 * j + 1) & 3] += y;
-            // the product takes bf16: the powers round here, their sum does not
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
-          }
-          tmem_st32(s_at + c * 32, w);
-        }
-        sum += (part[0] + part[1]) + (part[2] + part[3]);
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.p_ready[t]);
-    }
-    if (ok && nt[t] > 0) {
-      ok = mbar_wait(&bars.o_done[t], 0, &abort_sh);
-      // the ring is the other one's too: its products end before it is written below
-      if (ok && dual && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
-      tc_fence_after();
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok && lane == 0) {
-      abort_sh = 1;
-      report_status(p.status, LR_ERR_TIMEOUT);
-    }
-    if (ok && dual && t == 1 && nt[1] > 0 && busy) {  // ring 1 hands its part to ring 0
-      ml_sh[trow] = make_float2(mref, sum);
-      float* dst = reinterpret_cast<float*>(ring) + trow * (HD + 4);
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(o_at + c * 32, o);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<uint4*>(dst + c * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
       }
     }
   }
@@ -541,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = trow < live_rows;
     if (busy) {
       const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const bool both = dual && nt[1] > 0;
+      const bool both = dual && n1 > 0;
       float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
       if (both) {
         const float2 o = ml_sh[trow];
@@ -551,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = ex2(o.x - ref);
         l = f0 * sum + f1 * o.y;
       }
-      if (nt[t] == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
+      if (my_n == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
       const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
       const int head = kvh * G + trow % G;
       const int64_t at = (static_cast<int64_t>(a.slot0 + split) * p.M + qrow) * p.n_heads + head;
