@@ -9,12 +9,17 @@
 // independent softmax rings keep the tensor pipe busy while the other one's
 // powers are computed:
 //   warps 0-3, 4-7  softmax of ring 0 and 1, one row per thread;
-//   warp 8          TMA producer (K and V tiles of 128 keys, 16-row boxes: a
-//                   box never crosses a page);
-//   warp 9          tcgen05.mma issue: S = Q K^T (Q, K in shared memory) and
+//   warps 8-11      load K and V tiles of 128 keys;
+//   warp 12         tcgen05.mma issue: S = Q K^T (Q, K in shared memory) and
 //                   O += P V (P in TMEM, where the softmax warps put it over
 //                   S; V in shared memory as it lies in the cache, keys along
 //                   the reduction, which is the operand's MN-major form).
+// The tiles come by 16-byte asynchronous copies into the layout of the 128-byte
+// swizzle.  A page may be 16 rows long and a TMA box cannot cross one: sixteen
+// boxes a tile took 1340 cycles from L2, where one 128-row box takes 630, and
+// the products of two rings take 2048 for two tiles.  The copies also fill with
+// zeros where no token lies, so that whatever a last page holds behind its
+// tokens stays out (0 * NaN would be NaN).
 // The order of the products is  S0 S1 | PV0 S0' PV1 S1' | ...: S0' needs
 // softmax 0 to be through with S0 (its P has been consumed by PV0, issued just
 // before), and runs while softmax 1 works.
@@ -32,12 +37,13 @@
 namespace lr {
 namespace {
 
-constexpr int kThreads = 384;        // 8 softmax warps, a producer, an MMA issuer, two idle
-// Registers: the launch gives 168 a thread; the softmax warps hold a row of
-// 128 scores and take what the other four leave (256 * 208 + 128 * 88 = 384 * 168).
-constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, three idle
+constexpr int kMmaWarp = 12;
+// Registers: the launch gives 128 a thread; the softmax warps hold a row of 128
+// scores and take what the others leave (256 * 200 + 256 * 56 = 512 * 128).
+constexpr int kRegsSoftmax = 200, kRegsOther = 56;
 constexpr int kKeys = 128;           // keys per tile
-constexpr int kPage = 16;            // rows per TMA box
+constexpr int kPage = 16;            // rows of a page, at least
 constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 each), O0, O1 (head_dim each)
 constexpr float kSlack = 8.f;
 
@@ -47,6 +53,9 @@ struct Shape {
   static constexpr int kChunkBytes = 128 * 128;        // 128 rows of 64 bf16
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kSlots = HD == 128 ? 5 : 10;    // ring of K and V tiles
+  // Tiles that a producer has in flight beyond the one it hands on.  A slot is
+  // freed once the tile after it is there, so kLag + 2 < kSlots.
+  static constexpr int kLag = HD == 128 ? 2 : 5;
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
 };
 
@@ -59,6 +68,16 @@ struct TileParams {
   int32_t direct;     // one key range: results go straight to out
   int32_t stall;      // fault-injection hook: the producer issues nothing
 };
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;  // 0: sixteen zero bytes
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -88,15 +107,66 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulator.
-__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
+// The products of one tile pair, each issued as one block: eight or four
+// instructions whose operands differ by constants.  The issuing warp shares its
+// scheduler with softmax warps, and every instruction between two products
+// delays the tensor pipe: with one lane of a divergent warp computing 64-bit
+// descriptors, a pair of 128 x 128 x 128 products took 1630 cycles beside
+// warps that issue all the time; so, from a converged warp, it takes 1130 (1030
+// alone; the pipe needs 1024).
+//
+// Descriptor words: a shared-memory tile with the 128-byte swizzle has the low
+// word address / 16 | (leading offset / 16) << 16 and this high word (stride
+// between groups of eight rows 1024 bytes, version 1, 128-byte swizzle).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lead_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lead_bytes >> 4) << 16);
+}
+
+// S = Q K^T over one chunk of 64 columns of the head, both K-major: four
+// products of 16 columns (32 bytes) each.  acc: add to D from the first on.
+__device__ __forceinline__ void mma_qk_chunk(uint32_t d, uint32_t q_lo, uint32_t k_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 x, y;\n\t.reg .b32 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t"
+      "add.u32 a, %1, 2;\n\tadd.u32 b, %2, 2;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 a, %1, 4;\n\tadd.u32 b, %2, 4;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t"
+      "add.u32 a, %1, 6;\n\tadd.u32 b, %2, 6;\n\tmov.b64 x, {a, %3};\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n\t}" ::"r"(d),
+      "r"(q_lo), "r"(k_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// O += P V over 64 keys: P in TMEM (two keys a column), V with the keys along
+// the reduction, in steps of 16 keys (2048 bytes; element (key, column) of
+// chunks [128 keys][64 columns], columns contiguous: MN-major; groups of eight
+// keys 1024 bytes apart, chunks of columns the leading offset).
+__device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p_at, uint32_t v_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n\t}" ::"r"(d),
+      "r"(p_at), "r"(v_lo), "r"(kDescHi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // 3-D tiled load, as tma_load_2d.
@@ -107,20 +177,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
-}
-
-// Descriptor of a V tile: element (key, column) of [128 keys][64 columns]
-// chunks with the 128-byte swizzle, columns contiguous (MN-major).  Groups of
-// eight keys are 1024 bytes apart (stride offset), chunks of 64 columns
-// chunk_bytes apart (leading offset).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t chunk_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(chunk_bytes >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
 }
 
 template <int N>
@@ -161,13 +217,12 @@ struct Bars {
   uint64_t q_full;
   uint64_t full[10], empty[10];
   uint64_t s_full[2], p_ready[2], o_done[2];
-  uint64_t tail, drain;
+  uint64_t drain;
 };
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const __grid_constant__ TileParams a, const __grid_constant__ CUtensorMap map_q,
-                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    attn_tiles_kernel(const __grid_constant__ TileParams a, const __grid_constant__ CUtensorMap map_q) {
   using S = Shape<HD>;
   constexpr int kSlots = S::kSlots;
   __shared__ __align__(8) Bars bars;
@@ -185,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.full[s], 4);  // one arrival per producer warp
       mbar_init(&bars.empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -193,7 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.p_ready[t], 4);
       mbar_init(&bars.o_done[t], 1);
     }
-    mbar_init(&bars.tail, 1);
     mbar_init(&bars.drain, 1);
     abort_sh = 0;
     fence_mbar_init();
@@ -258,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n1 < 0) n1 = 0;
   }
 
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&tmem_base_sh, kTmemCols);
     tmem_relinquish();
   }
@@ -277,149 +331,145 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     regs_fewer<kRegsOther>();
-    if (warp == 8) {
-      // ------------------------------------------------------ producer
-      if (lane == 0) {
-        prefetch_tensormap(&map_q);
-        prefetch_tensormap(&map_k);
-        prefetch_tensormap(&map_v);
-      }
-      const uint64_t pol = l2_policy_evict_last();
+    if (warp < kMmaWarp) {
+      // ---------------------------------------------------- producers
       if (!a.stall && n > 0) {
-        if (lane == 0) {
+        if (warp == 8 && lane == 0) {
           const uint32_t bytes = static_cast<uint32_t>(a.mt * G * 128 * S::kChunks) * (dual ? 1u : 2u);
+          const uint64_t pol = l2_policy_evict_last();
           mbar_arrive_expect_tx(&bars.q_full, bytes);
           for (int t = 0; t < (dual ? 1 : 2); ++t)
             for (int c = 0; c < S::kChunks; ++c)
               tma_load_3d(q_sm + t * S::kTileBytes + c * S::kChunkBytes, &map_q, &bars.q_full, c * 64, kvh * G,
                           q0 + mrel + t * a.mt, pol);
         }
-        const int grp = lane / S::kChunks, ch = lane % S::kChunks;
-        const bool mine = grp < kKeys / kPage;
-        // pool row of this lane's 16 keys of tile k; past the pool (reads as zeros) where there are none
-        auto row_of = [&](int k) {
-          int t, limit;
-          const int32_t* pages;
-          if (k < np) {
-            t = k * kKeys + grp * kPage, limit = P, pages = p.prefix_blocks;
-          } else {
-            t = (k - np) * kKeys + grp * kPage, limit = see, pages = own_pages;
-          }
-          int64_t row = p.pool_rows;
-          if (mine && t < limit) {
-            const int64_t page = pages[t / p.block_rows];
-            if (page < 0 || page >= p.pool_blocks)
-              report_status(p.status, LR_ERR_REMAP_RANGE);
-            else
+        // Each warp takes two groups of 16 keys of a tile; an instruction
+        // copies kRows whole rows.
+        constexpr int kCols = HD / 8, kRows = 32 / kCols;
+        const int g0 = (warp - 8) * 2;
+        const int r_in = lane / kCols, col = lane % kCols;
+        const int64_t head_off = static_cast<int64_t>(kvh) * HD + col * 8;
+        const uint32_t dst0 = smem_u32(ring) + (col >> 3) * S::kChunkBytes;
+        // first pool row of the keys of group g of tile k, or -1 where there are none (or no such page)
+        auto row_of = [&](int k, int g) {
+          const bool pre = k < np;
+          const int t = (pre ? k : k - np) * kKeys + g * kPage;
+          int64_t row = -1;
+          if (t < (pre ? P : see)) {
+            const int64_t page = (pre ? p.prefix_blocks : own_pages)[t / p.block_rows];
+            if (page < 0 || page >= p.pool_blocks) {
+              if (lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
+            } else {
               row = page * p.block_rows + t % p.block_rows;
+            }
           }
           return static_cast<int32_t>(row);
         };
-        int ld = 0, tails = 0;
+        int ld = 0;
         bool ok = true;
-        // keys of tile k that hold tokens
-        auto filled = [&](int k) {
-          const int f = k < np ? P - k * kKeys : see - (k - np) * kKeys;
-          return f < kKeys ? f : kKeys;
+        auto hand_on = [&](int l) {  // this warp's copies of tile l have landed
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.full[l % kSlots]);
         };
-        auto load = [&](const CUtensorMap* map, int row, int fill, bool is_v) {
+        auto load = [&](const uint16_t* pool, int row_a, int row_b, int k) {
           if (!ok) return;
           const int s = ld % kSlots;
           ok = mbar_wait(&bars.empty[s], ((ld / kSlots) & 1) ^ 1, &abort_sh);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
-          uint8_t* dst = ring + s * S::kTileBytes;
-          // A last page's rows past the tokens may hold anything, and 0 * NaN is
-          // NaN: such a V tile is patched to zeros before it is handed on.
-          const bool patch = is_v && (fill & (kPage - 1)) != 0;
-          uint64_t* bar = patch ? &bars.tail : &bars.full[s];
-          if (lane == 0) mbar_arrive_expect_tx(bar, S::kTileBytes);
-          __syncwarp();
-          if (mine)
-            tma_load_2d(dst + ch * S::kChunkBytes + grp * kPage * 128, map, bar, kvh * HD + ch * 64, row, pol);
-          if (patch) {
-            ok = mbar_wait(bar, tails & 1, &abort_sh);
-            ok = __all_sync(0xffffffffu, ok);
-            ++tails;
-            if (ok) {
-              const int end = (fill + kPage - 1) / kPage * kPage;
-              for (int i = lane; i < (end - fill) * 8 * S::kChunks; i += 32) {
-                const int c = i / ((end - fill) * 8), j = i % ((end - fill) * 8);
-                *reinterpret_cast<uint4*>(dst + c * S::kChunkBytes + (fill + j / 8) * 128 + (j % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&bars.full[s]);
+          const int fill = (k < np ? P - k * kKeys : see - (k - np) * kKeys) - g0 * kPage;  // keys from the first group on
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = h ? row_b : row_a;
+            const uint16_t* src = pool + (row < 0 ? 0 : static_cast<int64_t>(row) * p.ld) + head_off;
+            const int live = row < 0 ? 0 : fill - h * kPage;
+#pragma unroll
+            for (int j = 0; j < kPage / kRows; ++j) {
+              const int r = j * kRows + r_in;
+              const int kr = (g0 + h) * kPage + r;
+              const uint32_t dst = dst0 + s * S::kTileBytes + kr * 128 + (((col & 7) ^ (kr & 7)) << 4);
+              const bool in = r < live;
+              cp_async16(dst, in ? src + static_cast<int64_t>(r) * p.ld : pool, in);
             }
           }
+          cp_async_commit();
           ++ld;
+          if (ld > S::kLag) {
+            cp_async_wait<S::kLag>();
+            hand_on(ld - 1 - S::kLag);
+          }
         };
         const int ahead = dual ? 2 : 1;
-        int r_now = row_of(k_lo), r_next = 0;
-        load(&map_k, r_now, kKeys, false);
+        int now_a = row_of(k_lo, g0), now_b = row_of(k_lo, g0 + 1), next_a = 0, next_b = 0;
+        load(p.k, now_a, now_b, k_lo);
         if (dual && n > 1) {
-          r_next = row_of(k_lo + 1);
-          load(&map_k, r_next, kKeys, false);
+          next_a = row_of(k_lo + 1, g0), next_b = row_of(k_lo + 1, g0 + 1);
+          load(p.k, next_a, next_b, k_lo + 1);
         }
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
-          const int r_new = i + ahead < n ? row_of(k_lo + i + ahead) : 0;
-          load(&map_v, r_now, filled(k_lo + i), true);
-          if (i + ahead < n) load(&map_k, r_new, kKeys, false);
-          r_now = dual ? r_next : r_new;
-          r_next = r_new;
+          const int kn = k_lo + i + ahead;
+          int new_a = 0, new_b = 0;
+          if (i + ahead < n) new_a = row_of(kn, g0), new_b = row_of(kn, g0 + 1);
+          load(p.v, now_a, now_b, k_lo + i);
+          if (i + ahead < n) load(p.k, new_a, new_b, kn);
+          now_a = dual ? next_a : new_a, now_b = dual ? next_b : new_b;
+          next_a = new_a, next_b = new_b;
         }
-        if (!ok) {
-          if (lane == 0) {
-            abort_sh = 1;
-            report_status(p.status, LR_ERR_TIMEOUT);
-          }
-          // copies in flight land before the CTA's shared memory goes away
-          mbar_wait(&bars.q_full, 0, nullptr);
-          for (int i = ld > kSlots ? ld - kSlots : 0; i < ld; ++i) mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1, nullptr);
-          if (tails > 0) mbar_wait(&bars.tail, (tails - 1) & 1, nullptr);
+        cp_async_wait<0>();
+        if (ok) {
+          for (int l = ld > S::kLag ? ld - S::kLag : 0; l < ld; ++l) hand_on(l);
+        } else if (lane == 0) {
+          abort_sh = 1;
+          report_status(p.status, LR_ERR_TIMEOUT);
+          if (warp == 8) mbar_wait(&bars.q_full, 0, nullptr);  // the copy in flight lands before the CTA ends
         }
       }
-    } else if (warp == 9) {
+    } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA
-      if (lane == 0 && n > 0) {
+      // The whole warp walks the loop; one lane issues.
+      if (n > 0) {
         constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
         constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
-        bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
+        const bool lead = elect_lane();
+        const uint32_t q_lo = desc_lo(smem_u32(q_sm), 16), r_k = desc_lo(smem_u32(ring), 16);
+        const uint32_t r_v = desc_lo(smem_u32(ring), S::kChunkBytes);
+        const uint32_t q_step = dual ? 0 : S::kTileBytes >> 4;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, &abort_sh));
         tc_fence_after();
-        int ld = 0;
         auto slot_wait = [&](int l) {
-          if (ok) ok = mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh);
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh));
           tc_fence_after();
         };
         auto qk = [&](int t, int l) {
-          if (!ok) return;
-          const uint64_t qa = smem_desc_sw128(smem_u32(q_sm + (dual ? 0 : t) * S::kTileBytes));
-          const uint64_t ka = smem_desc_sw128(smem_u32(ring + (l % kSlots) * S::kTileBytes));
+          if (ok && lead) {
+            const uint32_t k_at = r_k + (l % kSlots) * (S::kTileBytes >> 4), q_at = q_lo + t * q_step;
 #pragma unroll
-          for (int c = 0; c < S::kChunks; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_bf16(tmem + t * kKeys, qa + (c * S::kChunkBytes >> 4) + 2 * k, ka + (c * S::kChunkBytes >> 4) + 2 * k,
-                          kIdS, (c | k) != 0 ? 1u : 0u);
-          tc_commit(&bars.s_full[t]);
+            for (int c = 0; c < S::kChunks; ++c)
+              mma_qk_chunk(tmem + t * kKeys, q_at + c * (S::kChunkBytes >> 4), k_at + c * (S::kChunkBytes >> 4), kIdS, c);
+            tc_commit(&bars.s_full[t]);
+          }
+          __syncwarp();
         };
         // round r of ring t; its last one completes the ring's O
         auto pv = [&](int t, int l, int r, bool last) {
-          if (ok) ok = mbar_wait(&bars.p_ready[t], r & 1, &abort_sh);
-          if (!ok) return;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t], r & 1, &abort_sh));
           tc_fence_after();
-          const uint64_t va = smem_desc_mn_sw128(smem_u32(ring + (l % kSlots) * S::kTileBytes), S::kChunkBytes);
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_bf16_ta(tmem + 256 + t * HD, tmem + t * kKeys + k * 8, va + (k * 16 * 128 >> 4), kIdO,
-                           (r | k) != 0 ? 1u : 0u);
-          if (last) tc_commit(&bars.o_done[t]);
+          if (ok && lead) {
+            const uint32_t v_at = r_v + (l % kSlots) * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
+            mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
+            mma_pv_half(tmem + 256 + t * HD, p_at + 32, v_at + (64 * 128 >> 4), kIdO, 1);
+            if (last) tc_commit(&bars.o_done[t]);
+          }
+          __syncwarp();
         };
         auto release = [&](int l) {
-          if (ok) tc_commit(&bars.empty[l % kSlots]);
+          if (ok && lead) tc_commit(&bars.empty[l % kSlots]);
+          __syncwarp();
         };
         slot_wait(0);
+        int ld = 0;
         if (dual) {
           qk(0, 0);
           release(0);
@@ -430,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             release(1);
             ld = 2;
           }
+#pragma unroll 1
           for (int i = 0; i < n && ok; ++i) {
             const int t = i & 1, lv = ld++;
             slot_wait(lv);
@@ -447,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n1 > 0) qk(1, 0);
           release(0);
           ld = 1;
+#pragma unroll 1
           for (int i = 0; i < n && ok; ++i) {
             const int lv = ld++;
             const bool more = i + 1 < n;
@@ -467,13 +519,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) release(lk);
           }
         }
-        if (!ok) {
-          abort_sh = 1;
-          report_status(p.status, LR_ERR_TIMEOUT);
+        if (lead) {
+          if (!ok) {
+            abort_sh = 1;
+            report_status(p.status, LR_ERR_TIMEOUT);
+          }
+          // every MMA issued by this thread completes before TMEM is released
+          tc_commit(&bars.drain);
+          mbar_wait(&bars.drain, 0, nullptr);
         }
-        // every MMA issued by this thread completes before TMEM is released
-        tc_commit(&bars.drain);
-        mbar_wait(&bars.drain, 0, nullptr);
+        __syncwarp();
       }
     }
   } else {
@@ -586,78 +641,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp < 8 && !(dual && ringi == 1) && abort_sh == 0) {
-    // ------------------------------------------------- rows to memory
-    const int t = ringi;
-    const bool busy = (warp & 3) * 32 < live_rows;
-    const bool live = trow < live_rows;
-    if (busy) {
-      const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const bool both = dual && n1 > 0;
-      float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
-      if (both) {
-        const float2 o = ml_sh[trow];
-        m = fmaxf(mref, o.x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        f0 = ex2(mref - ref);
-        f1 = ex2(o.x - ref);
-        l = f0 * sum + f1 * o.y;
-      }
-      if (my_n == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
-      const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
-      const int head = kvh * G + trow % G;
-      const int64_t at = (static_cast<int64_t>(a.slot0 + split) * p.M + qrow) * p.n_heads + head;
-      if (a.direct) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        f0 *= inv;
-        f1 *= inv;
-      } else if (live) {
-        p.pml[at] = make_float2(m, l);
-      }
-      const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
-#pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t r[32];
-        float x[32];
-        tmem_ld32(o_at + c * 32, r);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = f0 == 0.f ? 0.f : __uint_as_float(r[j]) * f0;
+    tc_fence_before();
+    named_bar_sync(1, 256);  // the softmax warps
+    tc_fence_after();
+    if (!(dual && ringi == 1) && *static_cast<volatile int*>(&abort_sh) == 0) {
+      // ------------------------------------------------- rows to memory
+      const int t = ringi;
+      const bool busy = (warp & 3) * 32 < live_rows;
+      const bool live = trow < live_rows;
+      if (busy) {
+        const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const bool both = dual && n1 > 0;
+        float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
         if (both) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 y = *reinterpret_cast<const float4*>(other + c * 32 + j);
-            x[j] = fmaf(y.x, f1, x[j]), x[j + 1] = fmaf(y.y, f1, x[j + 1]);
-            x[j + 2] = fmaf(y.z, f1, x[j + 2]), x[j + 3] = fmaf(y.w, f1, x[j + 3]);
-          }
+          const float2 o = ml_sh[trow];
+          m = fmaxf(mref, o.x);
+          const float ref = m == -INFINITY ? 0.f : m;
+          f0 = ex2(mref - ref);
+          f1 = ex2(o.x - ref);
+          l = f0 * sum + f1 * o.y;
         }
-        if (!live) continue;
-        if (a.direct && !p.out_f32) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + qrow * p.ldo + head * HD + c * 32);
+        if (my_n == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
+        const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
+        const int head = kvh * G + trow % G;
+        const int64_t at = (static_cast<int64_t>(a.slot0 + split) * p.M + qrow) * p.n_heads + head;
+        if (a.direct) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          f0 *= inv;
+          f1 *= inv;
+        } else if (live) {
+          p.pml[at] = make_float2(m, l);
+        }
+        const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t r[32];
+          float x[32];
+          tmem_ld32(o_at + c * 32, r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t w[4];
+          for (int j = 0; j < 32; ++j) x[j] = f0 == 0.f ? 0.f : __uint_as_float(r[j]) * f0;
+          if (both) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x[j + 2 * e + 1]), "f"(x[j + 2 * e]));
-            dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(other + c * 32 + j);
+              x[j] = fmaf(y.x, f1, x[j]), x[j + 1] = fmaf(y.y, f1, x[j + 1]);
+              x[j + 2] = fmaf(y.z, f1, x[j + 2]), x[j + 3] = fmaf(y.w, f1, x[j + 3]);
+            }
           }
-        } else {
-          float4* dst = a.direct ? reinterpret_cast<float4*>(static_cast<float*>(p.out) + qrow * p.ldo + head * HD + c * 32)
-                                 : reinterpret_cast<float4*>(p.po + at * HD + c * 32);
+          if (!live) continue;
+          if (a.direct && !p.out_f32) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + qrow * p.ldo + head * HD + c * 32);
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x[j + 2 * e + 1]), "f"(x[j + 2 * e]));
+              dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* dst = a.direct ? reinterpret_cast<float4*>(static_cast<float*>(p.out) + qrow * p.ldo + head * HD + c * 32)
+                                   : reinterpret_cast<float4*>(p.po + at * HD + c * 32);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+          }
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -666,11 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int HD>
 lr_status launch_tiles(const TileParams& a, dim3 grid, cudaStream_t s) {
   using Sh = Shape<HD>;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq;
   lr_status st = encode_map_heads(&mq, a.p.q, HD, a.p.n_heads, a.p.M, a.p.ldq, a.p.group, a.mt);
-  const uint64_t cols = static_cast<uint64_t>(a.p.n_kv) * HD;
-  if (st == LR_OK) st = encode_map_bf16(&mk, a.p.k, a.p.pool_rows, cols, a.p.ld, kPage);
-  if (st == LR_OK) st = encode_map_bf16(&mv, a.p.v, a.p.pool_rows, cols, a.p.ld, kPage);
   if (st != LR_OK) return st;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
@@ -685,7 +737,7 @@ lr_status launch_tiles(const TileParams& a, dim3 grid, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<HD>, a, mq, mk, mv);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<HD>, a, mq);
   if (e != cudaSuccess) return cuda_fail(e, "attn_tiles");
   return LR_OK;
 }
