@@ -542,6 +542,9 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
   p.pool_blocks = c.pool_blocks;
   p.pool_rows = c.pool_blocks * c.block_rows;
   p.block_rows = c.block_rows;
+  p.block_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (c.block_rows == 1 << i) p.block_shift = i;
   p.n_heads = d->n_heads;
   p.n_kv = c.n_kv_heads;
   p.group = d->n_heads / c.n_kv_heads;

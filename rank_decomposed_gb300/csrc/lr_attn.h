@@ -14,6 +14,7 @@ struct AttnParams {
   int64_t ld;                 // row stride of both pools, elements
   int64_t pool_rows, pool_blocks;
   int32_t block_rows;
+  int32_t block_shift;        // log2(block_rows), or -1
   int32_t n_heads, n_kv, group;
   float scale_log2;           // scale * log2(e): scores are kept in powers of two
   const int32_t* prefix_blocks;

@@ -69,8 +69,11 @@ struct TileParams {
   int32_t stall;      // fault-injection hook: the producer issues nothing
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  const int n = live ? 16 : 0;  // 0: sixteen zero bytes
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;  // bytes read; the rest of the sixteen are zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -216,7 +219,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct Bars {
   uint64_t q_full;
   uint64_t full[10], empty[10];
-  uint64_t s_full[2], p_ready[2], o_done[2];
+  uint64_t s_full[2], p_ready[2][2], o_done[2];  // P is handed on in two halves of its keys
   uint64_t drain;
 };
 
@@ -245,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars.s_full[t], 1);
-      mbar_init(&bars.p_ready[t], 4);
+      mbar_init(&bars.p_ready[t][0], 4);
+      mbar_init(&bars.p_ready[t][1], 4);
       mbar_init(&bars.o_done[t], 1);
     }
     mbar_init(&bars.drain, 1);
@@ -344,23 +348,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                           q0 + mrel + t * a.mt, pol);
         }
         // Each warp takes two groups of 16 keys of a tile; an instruction
-        // copies kRows whole rows.
-        constexpr int kCols = HD / 8, kRows = 32 / kCols;
+        // copies kRows whole rows, and the swizzle repeats after kTurn of them.
+        constexpr int kCols = HD / 8, kRows = 32 / kCols, kTurn = 8 / kRows;
         const int g0 = (warp - 8) * 2;
         const int r_in = lane / kCols, col = lane % kCols;
         const int64_t head_off = static_cast<int64_t>(kvh) * HD + col * 8;
-        const uint32_t dst0 = smem_u32(ring) + (col >> 3) * S::kChunkBytes;
+        const int64_t step = static_cast<int64_t>(kRows) * p.ld;
+        uint32_t dst0[kTurn];
+#pragma unroll
+        for (int j = 0; j < kTurn; ++j) {
+          const int r = j * kRows + r_in;
+          dst0[j] = smem_u32(ring) + (col >> 3) * S::kChunkBytes + (g0 * kPage + r) * 128 + (((col & 7) ^ r) << 4);
+        }
         // first pool row of the keys of group g of tile k, or -1 where there are none (or no such page)
         auto row_of = [&](int k, int g) {
           const bool pre = k < np;
           const int t = (pre ? k : k - np) * kKeys + g * kPage;
           int64_t row = -1;
           if (t < (pre ? P : see)) {
-            const int64_t page = (pre ? p.prefix_blocks : own_pages)[t / p.block_rows];
+            const int i = p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows;
+            const int64_t page = (pre ? p.prefix_blocks : own_pages)[i];
             if (page < 0 || page >= p.pool_blocks) {
               if (lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
             } else {
-              row = page * p.block_rows + t % p.block_rows;
+              row = page * p.block_rows + (t - i * p.block_rows);
             }
           }
           return static_cast<int32_t>(row);
@@ -382,15 +393,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int row = h ? row_b : row_a;
-            const uint16_t* src = pool + (row < 0 ? 0 : static_cast<int64_t>(row) * p.ld) + head_off;
             const int live = row < 0 ? 0 : fill - h * kPage;
+            const uint16_t* src = pool + (row < 0 ? 0 : static_cast<int64_t>(row + r_in) * p.ld) + head_off;
+            const uint32_t at = s * S::kTileBytes + h * kPage * 128;
+            if (live >= kPage) {
 #pragma unroll
-            for (int j = 0; j < kPage / kRows; ++j) {
-              const int r = j * kRows + r_in;
-              const int kr = (g0 + h) * kPage + r;
-              const uint32_t dst = dst0 + s * S::kTileBytes + kr * 128 + (((col & 7) ^ (kr & 7)) << 4);
-              const bool in = r < live;
-              cp_async16(dst, in ? src + static_cast<int64_t>(r) * p.ld : pool, in);
+              for (int j = 0; j < kPage / kRows; ++j, src += step)
+                cp_async16(dst0[j % kTurn] + at + j / kTurn * 1024, src);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kPage / kRows; ++j, src += step) {
+                const bool in = j * kRows + r_in < live;
+                cp_async16_or_zero(dst0[j % kTurn] + at + j / kTurn * 1024, in ? src : pool, in);
+              }
             }
           }
           cp_async_commit();
@@ -454,11 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // round r of ring t; its last one completes the ring's O
         auto pv = [&](int t, int l, int r, bool last) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t], r & 1, &abort_sh));
+          const uint32_t v_at = r_v + (l % kSlots) * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t][0], r & 1, &abort_sh));
+          tc_fence_after();
+          if (ok && lead) mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
+          __syncwarp();
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t][1], r & 1, &abort_sh));
           tc_fence_after();
           if (ok && lead) {
-            const uint32_t v_at = r_v + (l % kSlots) * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
-            mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
             mma_pv_half(tmem + 256 + t * HD, p_at + 32, v_at + (64 * 128 >> 4), kIdO, 1);
             if (last) tc_commit(&bars.o_done[t]);
           }
@@ -606,15 +624,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
             }
             tmem_st32(s_at + c * 32, w);
+            if (c == 0) {
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.p_ready[t][0]);
+            }
           }
           float pa, pb;
           unpack2(add2(part[0], part[1]), pa, pb);
           sum += pa + pb;
           tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(&bars.p_ready[t][0]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_ready[t]);
+        if (lane == 0) mbar_arrive(&bars.p_ready[t][1]);
       }
       if (ok && my_n > 0) {
         ok = mbar_wait(&bars.o_done[t], 0, &abort_sh);
