@@ -53,9 +53,6 @@ struct Shape {
   static constexpr int kChunkBytes = 128 * 128;        // 128 rows of 64 bf16
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kSlots = HD == 128 ? 5 : 10;    // ring of K and V tiles
-  // Tiles that a producer has in flight beyond the one it hands on.  A slot is
-  // freed once the tile after it is there, so kLag + 2 < kSlots.
-  static constexpr int kLag = HD == 128 ? 2 : 5;
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
 };
 
@@ -76,15 +73,22 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
   const int n = live ? 16 : 0;  // bytes read; the rest of the sixteen are zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrives on `bar` (which counts this thread) once its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The same in program order with the stores to TMEM, so that the first half of
+// P is stored before the second half's powers are begun.
+__device__ __forceinline__ float ex2_in_order(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bars.full[s], 4);  // one arrival per producer warp
+      mbar_init(&bars.full[s], 128);  // every producer thread's copies
       mbar_init(&bars.empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -360,29 +364,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = j * kRows + r_in;
           dst0[j] = smem_u32(ring) + (col >> 3) * S::kChunkBytes + (g0 * kPage + r) * 128 + (((col & 7) ^ r) << 4);
         }
-        // first pool row of the keys of group g of tile k, or -1 where there are none (or no such page)
-        auto row_of = [&](int k, int g) {
+        // Page of the keys of group g of tile k, fetched some tiles ahead of its
+        // use; kNone where there are no keys.
+        constexpr int kNone = INT32_MIN;
+        auto index_of = [&](int t) { return p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows; };
+        auto page_of = [&](int k, int g) {
           const bool pre = k < np;
           const int t = (pre ? k : k - np) * kKeys + g * kPage;
-          int64_t row = -1;
-          if (t < (pre ? P : see)) {
-            const int i = p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows;
-            const int64_t page = (pre ? p.prefix_blocks : own_pages)[i];
-            if (page < 0 || page >= p.pool_blocks) {
-              if (lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
-            } else {
-              row = page * p.block_rows + (t - i * p.block_rows);
-            }
+          if (k >= k_hi || t >= (pre ? P : see)) return kNone;
+          return (pre ? p.prefix_blocks : own_pages)[index_of(t)];
+        };
+        // Its first pool row, or -1 for none (a page outside the pool among them).
+        auto row_of = [&](int page, int k, int g) {
+          if (page == kNone) return -1;
+          if (page < 0 || page >= p.pool_blocks) {
+            if (lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
+            return -1;
           }
-          return static_cast<int32_t>(row);
+          const int t = (k < np ? k : k - np) * kKeys + g * kPage;
+          return page * p.block_rows + (t - index_of(t) * p.block_rows);
         };
         int ld = 0;
         bool ok = true;
-        auto hand_on = [&](int l) {  // this warp's copies of tile l have landed
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.full[l % kSlots]);
-        };
         auto load = [&](const uint16_t* pool, int row_a, int row_b, int k) {
           if (!ok) return;
           const int s = ld % kSlots;
@@ -408,34 +411,33 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          cp_async_commit();
+          cp_async_arrive(&bars.full[s]);
           ++ld;
-          if (ld > S::kLag) {
-            cp_async_wait<S::kLag>();
-            hand_on(ld - 1 - S::kLag);
-          }
         };
+        // K runs `ahead` tiles before V; the pages two tiles before K.
         const int ahead = dual ? 2 : 1;
-        int now_a = row_of(k_lo, g0), now_b = row_of(k_lo, g0 + 1), next_a = 0, next_b = 0;
+        int now_a = row_of(page_of(k_lo, g0), k_lo, g0), now_b = row_of(page_of(k_lo, g0 + 1), k_lo, g0 + 1);
+        int next_a = 0, next_b = 0;
         load(p.k, now_a, now_b, k_lo);
         if (dual && n > 1) {
-          next_a = row_of(k_lo + 1, g0), next_b = row_of(k_lo + 1, g0 + 1);
+          next_a = row_of(page_of(k_lo + 1, g0), k_lo + 1, g0), next_b = row_of(page_of(k_lo + 1, g0 + 1), k_lo + 1, g0 + 1);
           load(p.k, next_a, next_b, k_lo + 1);
         }
+        int page_a = page_of(k_lo + ahead, g0), page_b = page_of(k_lo + ahead, g0 + 1);
+        int page2_a = page_of(k_lo + ahead + 1, g0), page2_b = page_of(k_lo + ahead + 1, g0 + 1);
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
           const int kn = k_lo + i + ahead;
-          int new_a = 0, new_b = 0;
-          if (i + ahead < n) new_a = row_of(kn, g0), new_b = row_of(kn, g0 + 1);
           load(p.v, now_a, now_b, k_lo + i);
+          const int new_a = row_of(page_a, kn, g0), new_b = row_of(page_b, kn, g0 + 1);
+          page_a = page2_a, page_b = page2_b;
+          page2_a = page_of(kn + 2, g0), page2_b = page_of(kn + 2, g0 + 1);
           if (i + ahead < n) load(p.k, new_a, new_b, kn);
           now_a = dual ? next_a : new_a, now_b = dual ? next_b : new_b;
           next_a = new_a, next_b = new_b;
         }
-        cp_async_wait<0>();
-        if (ok) {
-          for (int l = ld > S::kLag ? ld - S::kLag : 0; l < ld; ++l) hand_on(l);
-        } else if (lane == 0) {
+        cp_async_wait_all();
+        if (!ok && lane == 0) {
           abort_sh = 1;
           report_status(p.status, LR_ERR_TIMEOUT);
           if (warp == 8) mbar_wait(&bars.q_full, 0, nullptr);  // the copy in flight lands before the CTA ends
@@ -455,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         auto slot_wait = [&](int l) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh));
+          fence_proxy_async_smem();  // the copies wrote by the generic proxy, the products read by the async one
           tc_fence_after();
         };
         auto qk = [&](int t, int l) {
@@ -617,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   fma2(pack2(__uint_as_float(s[c * 64 + 2 * j]), __uint_as_float(s[c * 64 + 2 * j + 1])), scale2, neg2);
               float x, y;
               unpack2(e, x, y);
-              x = ex2(x);
-              y = ex2(y);
+              x = ex2_in_order(x);
+              y = ex2_in_order(y);
               part[j & 1] = add2(part[j & 1], pack2(x, y));
               // the product takes bf16: the powers round here, their sum does not
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
