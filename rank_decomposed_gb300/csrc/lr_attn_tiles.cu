@@ -10,6 +10,10 @@
 // powers are computed:
 //   warps 0-3, 4-7  softmax of ring 0 and 1, one row per thread;
 //   warps 8-11      load K and V tiles of 128 keys;
+//   warp 13         hands landed tiles on: the copies write shared memory by the
+//                   generic proxy and the products read it by the async one, and
+//                   the fence between the two takes some 400 cycles, which the
+//                   issuing warp has not;
 //   warp 12         tcgen05.mma issue: S = Q K^T (Q, K in shared memory) and
 //                   O += P V (P in TMEM, where the softmax warps put it over
 //                   S; V in shared memory as it lies in the cache, keys along
@@ -37,8 +41,8 @@
 namespace lr {
 namespace {
 
-constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, three idle
-constexpr int kMmaWarp = 12;
+constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, a relay, two idle
+constexpr int kMmaWarp = 12, kRelayWarp = 13;
 // Registers: the launch gives 128 a thread; the softmax warps hold a row of 128
 // scores and take what the others leave (256 * 200 + 256 * 56 = 512 * 128).
 constexpr int kRegsSoftmax = 200, kRegsOther = 56;
@@ -222,7 +226,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 struct Bars {
   uint64_t q_full;
-  uint64_t full[10], empty[10];
+  uint64_t landed[10], full[10], empty[10];
   uint64_t s_full[2], p_ready[2][2], o_done[2];  // P is handed on in two halves of its keys
   uint64_t drain;
 };
@@ -247,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&bars.full[s], 128);  // every producer thread's copies
+      mbar_init(&bars.landed[s], 128);  // every producer thread's copies
+      mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          cp_async_arrive(&bars.full[s]);
+          cp_async_arrive(&bars.landed[s]);
           ++ld;
         };
         // K runs `ahead` tiles before V; the pages two tiles before K.
@@ -443,6 +448,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (warp == 8) mbar_wait(&bars.q_full, 0, nullptr);  // the copy in flight lands before the CTA ends
         }
       }
+    } else if (warp == kRelayWarp) {
+      bool ok = true;
+#pragma unroll 1
+      for (int l = 0; l < 2 * n && ok; ++l) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.landed[l % kSlots], (l / kSlots) & 1, &abort_sh));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&bars.full[l % kSlots]);
+      }
+      if (!ok && lane == 0) {
+        abort_sh = 1;
+        report_status(p.status, LR_ERR_TIMEOUT);
+      }
     } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA
       // The whole warp walks the loop; one lane issues.
@@ -457,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         auto slot_wait = [&](int l) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh));
-          fence_proxy_async_smem();  // the copies wrote by the generic proxy, the products read by the async one
           tc_fence_after();
         };
         auto qk = [&](int t, int l) {
