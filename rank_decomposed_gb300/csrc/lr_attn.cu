@@ -78,17 +78,30 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>(r * HD * 2 + ((c ^ (r & 7)) << 4));
 }
 
+// One launch takes up to two parts: the prefix for all rows (where they are
+// too few for the tensor-core tiles) and the own tokens.
+struct RowsLaunch {
+  AttnPart part[2];
+  int32_t tiles[2];   // row tiles of part 0; row tiles per sequence of part 1
+  int32_t ctas0;      // CTAs of part 0 (0: only part 1)
+  int32_t beside;     // runs beside the tiles kernel that was launched before it
+};
+
 template <int HD>
-__global__ void __launch_bounds__(kRowsWarps * 32)
-    attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ AttnPart part, int tiles) {
+__device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLaunch& rl) {
   constexpr int kC16 = HD / 8;  // 16-byte columns of a row
   extern __shared__ __align__(128) uint8_t sm[];
-  pdl_launch_dependents();
-  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y;
-  const int split = blockIdx.z;
   const int G = p.group;
+  // CTA -> part, row tile, key head, key range
+  const int which = static_cast<int>(blockIdx.x) < rl.ctas0 ? 0 : 1;
+  const AttnPart part = which ? rl.part[1] : rl.part[0];
+  int idx = static_cast<int>(blockIdx.x) - (which ? rl.ctas0 : 0);
+  const int split = idx % part.slots;
+  idx /= part.slots;
+  const int kvh = idx % p.n_kv;
+  const int tile = idx / p.n_kv;
+  const int tiles = which ? rl.tiles[1] : rl.tiles[0];
 
   // This CTA's rows: r = (query row - q0) * G + head in the group.
   int q0, n_rows, row0, len, nq;
@@ -99,15 +112,15 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
     nq = p.M;
     len = prefix_view(p, tell);
     pages = p.prefix_blocks;
-    row0 = blockIdx.x * kRowsTile;
+    row0 = tile * kRowsTile;
   } else {
-    const int b = blockIdx.x / tiles;
+    const int b = tile / tiles;
     const SeqView v = seq_view(p, b, tell);
     q0 = v.q0;
     nq = v.nq;
     len = v.len;
     pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
-    row0 = (blockIdx.x % tiles) * kRowsTile;
+    row0 = (tile % tiles) * kRowsTile;
   }
   n_rows = nq * G - row0;
   if (n_rows <= 0) return;
@@ -160,7 +173,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
   auto page_of = [&](int i) {
     if ((i & 31) == 0) {
       const int c = c_lo + warp + (i + lane) * kRowsWarps;
-      ids = i + lane < mine ? pages[c * kRowsChunk / p.block_rows] : -1;
+      const int t = c * kRowsChunk;
+      ids = i + lane < mine ? pages[p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows] : -1;
       if (i + lane < mine && (ids < 0 || ids >= p.pool_blocks)) {
         report_status(p.status, LR_ERR_REMAP_RANGE);
         ids = -1;
@@ -168,23 +182,27 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
     }
     return __shfl_sync(0xffffffffu, ids, i & 31);
   };
-  const uint16_t* kh = p.k + static_cast<int64_t>(kvh) * HD;
-  const uint16_t* vh = p.v + static_cast<int64_t>(kvh) * HD;
+  // an instruction copies kRows rows
+  constexpr int kRows = 32 / kC16;
+  const int r_in = lane / kC16, col = lane % kC16;
+  const int64_t head_off = static_cast<int64_t>(kvh) * HD + col * 8;
+  const int64_t step = kRows * p.ld;
   auto issue = [&](int i) {
     if (i < mine) {
-      const int c = c_lo + warp + i * kRowsWarps;
       const int page = page_of(i);
-      const int t0 = c * kRowsChunk;
-      const int64_t row = static_cast<int64_t>(page < 0 ? 0 : page) * p.block_rows + t0 % p.block_rows;
+      const int t0 = (c_lo + warp + i * kRowsWarps) * kRowsChunk;
+      const int in_page = t0 - (p.block_shift >= 0 ? t0 >> p.block_shift << p.block_shift : t0 / p.block_rows * p.block_rows);
+      const int live = page < 0 ? 0 : kmax - t0;  // rows of the chunk that hold visible tokens
+      const int64_t off = page < 0 ? 0 : (static_cast<int64_t>(page) * p.block_rows + in_page + r_in) * p.ld + head_off;
+      const uint16_t* kp = p.k + off;
+      const uint16_t* vp = p.v + off;
       const uint32_t st = ring + (i % kRowsStages) * 2 * kTile;
 #pragma unroll
-      for (int j = 0; j < kC16 / 2; ++j) {  // 16 rows * kC16 columns by 32 lanes
-        const int idx = j * 32 + lane;
-        const int r = idx / kC16, col = idx % kC16;
-        const bool live = page >= 0 && t0 + r < kmax;
-        const int64_t off = live ? (row + r) * p.ld + col * 8 : 0;
-        cp16(st + swz<HD>(r, col), kh + off, live);
-        cp16(st + kTile + swz<HD>(r, col), vh + off, live);
+      for (int j = 0; j < kRowsChunk / kRows; ++j, kp += step, vp += step) {
+        const int r = j * kRows + r_in;
+        const bool in = r < live;
+        cp16(st + swz<HD>(r, col), in ? kp : p.k, in);
+        cp16(st + kTile + swz<HD>(r, col), in ? vp : p.v, in);
       }
     }
     cp_commit();
@@ -305,9 +323,24 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
   }
 }
 
+template <int HD>
+__global__ void __launch_bounds__(kRowsWarps * 32)
+    attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowsLaunch rl) {
+  pdl_launch_dependents();
+  // Beside the tiles kernel: all that is read here was complete before that
+  // kernel let this one start; its results are waited for at the end, so that
+  // the join, which waits for this kernel, finds both.
+  if (!rl.beside) pdl_wait();
+  attn_rows_cta<HD>(p, rl);
+  if (rl.beside) pdl_wait();
+}
+
 // --------------------------------------------------------------- join
 // One warp per (row, head): the slots' numerators with their weights.  Bound
 // by the partial results, which were written just before and lie in L2.
+constexpr int kMaxSlots = 64;  // of each part
+constexpr int kJoinSets = 2 * kMaxSlots / 32;
+
 template <int HD>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = HD / 32;  // elements per lane
@@ -327,26 +360,47 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 #pragma unroll
   for (int j = 0; j < kE; ++j) acc[j] = 0.f;
   if (m >= from && m < to) {
+    // lane i holds slots i, i + 32, ..: their weights, and the sum of all
     const int slots = p.prefix_slots + p.own_slots;
+    float2 ml[kJoinSets];
     float top = -INFINITY;
-    for (int i = 0; i < slots; ++i) top = fmaxf(top, p.pml[i * rows + r].x);
+#pragma unroll
+    for (int k = 0; k < kJoinSets; ++k) {
+      const int i = k * 32 + lane;
+      ml[k] = i < slots ? p.pml[i * rows + r] : make_float2(-INFINITY, 0.f);
+      top = fmaxf(top, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-    for (int i = 0; i < slots; ++i) {
-      const float2 ml = p.pml[i * rows + r];
-      if (ml.y == 0.f) continue;
-      const float f = exp2f(ml.x - ref);
-      l += f * ml.y;
-      const float* src = p.po + (i * rows + r) * HD + lane * kE;
-      if (kE == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] += f * x.x, acc[1] += f * x.y, acc[kE - 2] += f * x.z, acc[kE - 1] += f * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(src);
-        acc[0] += f * x.x, acc[1] += f * x.y;
+    float w[kJoinSets], l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinSets; ++k) {
+      w[k] = ml[k].y == 0.f ? 0.f : exp2f(ml[k].x - ref);  // 0: nothing was stored
+      l += w[k] * ml[k].y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
+#pragma unroll
+    for (int k = 0; k < kJoinSets; ++k) {
+      const int here = slots - k * 32 < 32 ? slots - k * 32 : 32;
+#pragma unroll 8
+      for (int i = 0; i < here; ++i) {
+        // no branch on the weight, so that several slots' loads are in flight
+        const float f = __shfl_sync(0xffffffffu, w[k], i);
+        const float* src = p.po + ((k * 32 + i) * rows + r) * HD + lane * kE;
+        if (kE == 4) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (f != 0.f) x = *reinterpret_cast<const float4*>(src);
+          acc[0] += f * x.x, acc[1] += f * x.y, acc[kE - 2] += f * x.z, acc[kE - 1] += f * x.w;
+        } else {
+          float2 x = make_float2(0.f, 0.f);
+          if (f != 0.f) x = *reinterpret_cast<const float2*>(src);
+          acc[0] += f * x.x, acc[1] += f * x.y;
+        }
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
 #pragma unroll
     for (int j = 0; j < kE; ++j) acc[j] *= inv;
   }
@@ -405,7 +459,7 @@ int slots_for(int64_t ctas, int64_t keys, int64_t want, int64_t min_keys) {
   int64_t n = ctas >= want ? 1 : want / ctas;
   const int64_t most = cdiv(keys, min_keys);
   if (n > most) n = most;
-  if (n > 64) n = 64;
+  if (n > kMaxSlots) n = kMaxSlots;
   return static_cast<int>(n);
 }
 
@@ -475,12 +529,23 @@ lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
 
 }  // namespace
 
-lr_status launch_attn_rows(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s) {
-  const int tiles = cdiv(static_cast<int64_t>(part.prefix ? p.M : p.max_q) * p.group, kRowsTile);
-  const dim3 grid(part.prefix ? tiles : tiles * p.n_seq, p.n_kv, part.slots);
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, int prefix_slots, int own_slots, bool beside,
+                           cudaStream_t s) {
+  RowsLaunch rl;
+  memset(&rl, 0, sizeof(rl));
+  rl.part[0] = AttnPart{true, false, prefix_slots, 0};
+  rl.part[1] = AttnPart{false, false, own_slots, p.prefix_slots};
+  rl.tiles[0] = cdiv(static_cast<int64_t>(p.M) * p.group, kRowsTile);
+  rl.tiles[1] = cdiv(static_cast<int64_t>(p.max_q) * p.group, kRowsTile);
+  const int64_t ctas0 = static_cast<int64_t>(rl.tiles[0]) * p.n_kv * prefix_slots;
+  const int64_t ctas = ctas0 + static_cast<int64_t>(rl.tiles[1]) * p.n_seq * p.n_kv * own_slots;
+  if (ctas > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "prefix_attention: too many rows for one launch");
+  rl.ctas0 = static_cast<int32_t>(ctas0);
+  rl.beside = beside && pdl_enabled();
+  const dim3 grid(static_cast<unsigned>(ctas));
   if (head_dim == 64)
-    return launch(attn_rows_kernel<64>, grid, dim3(kRowsWarps * 32), rows_smem<64>(), s, "attn_rows", p, part, tiles);
-  return launch(attn_rows_kernel<128>, grid, dim3(kRowsWarps * 32), rows_smem<128>(), s, "attn_rows", p, part, tiles);
+    return launch(attn_rows_kernel<64>, grid, dim3(kRowsWarps * 32), rows_smem<64>(), s, "attn_rows", p, rl);
+  return launch(attn_rows_kernel<128>, grid, dim3(kRowsWarps * 32), rows_smem<128>(), s, "attn_rows", p, rl);
 }
 
 lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s) {
@@ -573,13 +638,13 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
     st = launch_attn_tiles(p, c.head_dim, AttnPart{true, true, plan.prefix_slots > 0 ? plan.prefix_slots : 1, 0}, cs);
     if (st != LR_OK || plan.prefix_slots == 0) return st;
   } else {
-    if (p.prefix_slots > 0) {
-      const AttnPart part{true, false, p.prefix_slots, 0};
-      st = plan.tiles ? launch_attn_tiles(p, c.head_dim, part, cs) : launch_attn_rows(p, c.head_dim, part, cs);
+    if (plan.tiles && p.prefix_slots > 0) {
+      st = launch_attn_tiles(p, c.head_dim, AttnPart{true, false, p.prefix_slots, 0}, cs);
       if (st != LR_OK) return st;
     }
-    if (p.own_slots > 0) {
-      st = launch_attn_rows(p, c.head_dim, AttnPart{false, false, p.own_slots, p.prefix_slots}, cs);
+    const int row_prefix = plan.tiles ? 0 : p.prefix_slots;
+    if (row_prefix + p.own_slots > 0) {
+      st = launch_attn_rows(p, c.head_dim, row_prefix, p.own_slots, plan.tiles && p.prefix_slots > 0, cs);
       if (st != LR_OK) return st;
     }
   }

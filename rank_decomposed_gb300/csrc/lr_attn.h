@@ -52,7 +52,10 @@ struct AttnPart {
 // rows as far as whole rows do.
 inline int attn_tile_rows(int group) { return 128 / group; }
 
-lr_status launch_attn_rows(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
+// The parts that go by rows: the prefix in prefix_slots ranges (0: not here),
+// the own tokens in own_slots.  beside: right after launch_attn_tiles.
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, int prefix_slots, int own_slots, bool beside,
+                           cudaStream_t s);
 lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
 lr_status configure_attn_tiles();
 // Tensor map over query rows [M][ld]: element (c, h, m) is column h * head_dim

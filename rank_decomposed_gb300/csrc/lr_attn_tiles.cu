@@ -88,13 +88,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The same in program order with the stores to TMEM, so that the first half of
-// P is stored before the second half's powers are begun.
-__device__ __forceinline__ float ex2_in_order(float x) {
-  float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 #define LR_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
 #define LR_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
@@ -265,8 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_sh = 0;
     fence_mbar_init();
   }
-  pdl_launch_dependents();
+  // The kernel launched next may run beside this one (it takes the own tokens
+  // of the same batch and needs nothing of what is written here): it starts
+  // once every CTA is past this wait, when all earlier work is done.
   pdl_wait();
+  pdl_launch_dependents();
 
   // ---- this CTA's rows and keys
   const int kvh = blockIdx.y, split = blockIdx.z, G = p.group;
@@ -463,111 +459,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ----------------------------------------------------------- MMA
-      // The whole warp walks the loop; one lane issues.
-      if (n > 0) {
+      if (n > 0 && elect_lane()) {
         constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
         constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
-        const bool lead = elect_lane();
         const uint32_t q_lo = desc_lo(smem_u32(q_sm), 16), r_k = desc_lo(smem_u32(ring), 16);
         const uint32_t r_v = desc_lo(smem_u32(ring), S::kChunkBytes);
         const uint32_t q_step = dual ? 0 : S::kTileBytes >> 4;
-        bool ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full, 0, &abort_sh));
-        tc_fence_after();
-        auto slot_wait = [&](int l) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.full[l % kSlots], (l / kSlots) & 1, &abort_sh));
+        bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
+        // The ring's slots in the order of the loads: wait for the next one.
+        int slot = -1;
+        uint32_t phase = 0;
+        auto next_slot = [&]() {
+          if (++slot == kSlots) slot = 0, phase ^= 1;
+          if (ok) ok = mbar_wait(&bars.full[slot], phase, &abort_sh);
           tc_fence_after();
+          return slot;
         };
-        auto qk = [&](int t, int l) {
-          if (ok && lead) {
-            const uint32_t k_at = r_k + (l % kSlots) * (S::kTileBytes >> 4), q_at = q_lo + t * q_step;
+        auto qk = [&](int t, int at) {
+          if (!ok) return;
+          const uint32_t k_at = r_k + at * (S::kTileBytes >> 4), q_at = q_lo + t * q_step;
 #pragma unroll
-            for (int c = 0; c < S::kChunks; ++c)
-              mma_qk_chunk(tmem + t * kKeys, q_at + c * (S::kChunkBytes >> 4), k_at + c * (S::kChunkBytes >> 4), kIdS, c);
-            tc_commit(&bars.s_full[t]);
-          }
-          __syncwarp();
+          for (int c = 0; c < S::kChunks; ++c)
+            mma_qk_chunk(tmem + t * kKeys, q_at + c * (S::kChunkBytes >> 4), k_at + c * (S::kChunkBytes >> 4), kIdS, c);
+          tc_commit(&bars.s_full[t]);
         };
         // round r of ring t; its last one completes the ring's O
-        auto pv = [&](int t, int l, int r, bool last) {
-          const uint32_t v_at = r_v + (l % kSlots) * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t][0], r & 1, &abort_sh));
+        auto pv = [&](int t, int at, int r, bool last) {
+          const uint32_t v_at = r_v + at * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
+          if (ok) ok = mbar_wait(&bars.p_ready[t][0], r & 1, &abort_sh);
+          if (!ok) return;
           tc_fence_after();
-          if (ok && lead) mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
-          __syncwarp();
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.p_ready[t][1], r & 1, &abort_sh));
+          mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
+          ok = mbar_wait(&bars.p_ready[t][1], r & 1, &abort_sh);
+          if (!ok) return;
           tc_fence_after();
-          if (ok && lead) {
-            mma_pv_half(tmem + 256 + t * HD, p_at + 32, v_at + (64 * 128 >> 4), kIdO, 1);
-            if (last) tc_commit(&bars.o_done[t]);
-          }
-          __syncwarp();
+          mma_pv_half(tmem + 256 + t * HD, p_at + 32, v_at + (64 * 128 >> 4), kIdO, 1);
+          if (last) tc_commit(&bars.o_done[t]);
         };
-        auto release = [&](int l) {
-          if (ok && lead) tc_commit(&bars.empty[l % kSlots]);
-          __syncwarp();
+        auto release = [&](int at) {
+          if (ok) tc_commit(&bars.empty[at]);
         };
-        slot_wait(0);
-        int ld = 0;
         if (dual) {
-          qk(0, 0);
-          release(0);
-          ld = 1;
+          qk(0, next_slot());
+          release(slot);
           if (n > 1) {
-            slot_wait(1);
-            qk(1, 1);
-            release(1);
-            ld = 2;
+            qk(1, next_slot());
+            release(slot);
           }
 #pragma unroll 1
           for (int i = 0; i < n && ok; ++i) {
-            const int t = i & 1, lv = ld++;
-            slot_wait(lv);
-            pv(t, lv, i >> 1, i + 2 >= n);
-            release(lv);
+            const int t = i & 1;
+            pv(t, next_slot(), i >> 1, i + 2 >= n);
+            release(slot);
             if (i + 2 < n) {
-              const int lk = ld++;
-              slot_wait(lk);
-              qk(t, lk);
-              release(lk);
+              qk(t, next_slot());
+              release(slot);
             }
           }
         } else {
-          if (n0 > 0) qk(0, 0);
-          if (n1 > 0) qk(1, 0);
-          release(0);
-          ld = 1;
+          const int first = next_slot();
+          if (n0 > 0) qk(0, first);
+          if (n1 > 0) qk(1, first);
+          release(first);
 #pragma unroll 1
           for (int i = 0; i < n && ok; ++i) {
-            const int lv = ld++;
-            const bool more = i + 1 < n;
-            const int lk = more ? ld++ : 0;
-            slot_wait(lv);
+            const int at_v = next_slot();
+            int at_k = -1;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int mine = t ? n1 : n0;
               if (i < mine) {
-                pv(t, lv, i, i + 1 == mine);
+                pv(t, at_v, i, i + 1 == mine);
                 if (i + 1 < mine) {
-                  slot_wait(lk);
-                  qk(t, lk);
+                  if (at_k < 0) at_k = next_slot();
+                  qk(t, at_k);
                 }
               }
             }
-            release(lv);
-            if (more) release(lk);
+            release(at_v);
+            if (at_k >= 0) release(at_k);
           }
         }
-        if (lead) {
-          if (!ok) {
-            abort_sh = 1;
-            report_status(p.status, LR_ERR_TIMEOUT);
-          }
-          // every MMA issued by this thread completes before TMEM is released
-          tc_commit(&bars.drain);
-          mbar_wait(&bars.drain, 0, nullptr);
+        if (!ok) {
+          abort_sh = 1;
+          report_status(p.status, LR_ERR_TIMEOUT);
         }
-        __syncwarp();
+        // every MMA issued by this thread completes before TMEM is released
+        tc_commit(&bars.drain);
+        mbar_wait(&bars.drain, 0, nullptr);
       }
+      __syncwarp();
     }
   } else {
     regs_more<kRegsSoftmax>();
@@ -637,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   fma2(pack2(__uint_as_float(s[c * 64 + 2 * j]), __uint_as_float(s[c * 64 + 2 * j + 1])), scale2, neg2);
               float x, y;
               unpack2(e, x, y);
-              x = ex2_in_order(x);
-              y = ex2_in_order(y);
+              x = ex2(x);
+              y = ex2(y);
               part[j & 1] = add2(part[j & 1], pack2(x, y));
               // the product takes bf16: the powers round here, their sum does not
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
@@ -719,39 +700,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.pml[at] = make_float2(m, l);
         }
         const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
+        // A thread holds a row; memory wants rows side by side (16 bytes a lane
+        // of 32 rows each touch 32 lines).  The warp turns half a row at a time
+        // in its part of this ring's Q tile, which no product reads any more;
+        // 16-byte columns are permuted by the row against bank conflicts.
+        constexpr int kHalf = HD / 2, kVec = kHalf / 4, kPer = 32 / kVec;
+        float4* stage = reinterpret_cast<float4*>(q_sm + t * S::kTileBytes + (warp & 3) * (S::kTileBytes / 4));
+        const int64_t row_off = a.direct ? qrow * p.ldo + static_cast<int64_t>(head) * HD : at * HD;
+        const int left = live_rows - (warp & 3) * 32;  // rows of this warp
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t r[32];
-          float x[32];
-          tmem_ld32(o_at + c * 32, r);
-          tmem_ld_wait();
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = f0 == 0.f ? 0.f : __uint_as_float(r[j]) * f0;
-          if (both) {
+          for (int c = 0; c < kHalf / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(o_at + half * kHalf + c * 32, r);
+            tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 y = *reinterpret_cast<const float4*>(other + c * 32 + j);
-              x[j] = fmaf(y.x, f1, x[j]), x[j + 1] = fmaf(y.y, f1, x[j + 1]);
-              x[j + 2] = fmaf(y.z, f1, x[j + 2]), x[j + 3] = fmaf(y.w, f1, x[j + 3]);
+              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (f0 != 0.f)
+                x = make_float4(__uint_as_float(r[j]) * f0, __uint_as_float(r[j + 1]) * f0,
+                                __uint_as_float(r[j + 2]) * f0, __uint_as_float(r[j + 3]) * f0);
+              if (both) {
+                const float4 y = *reinterpret_cast<const float4*>(other + half * kHalf + c * 32 + j);
+                x.x = fmaf(y.x, f1, x.x), x.y = fmaf(y.y, f1, x.y);
+                x.z = fmaf(y.z, f1, x.z), x.w = fmaf(y.w, f1, x.w);
+              }
+              stage[lane * kVec + ((c * 8 + j / 4) ^ (lane & 7))] = x;
             }
           }
-          if (!live) continue;
-          if (a.direct && !p.out_f32) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + qrow * p.ldo + head * HD + c * 32);
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x[j + 2 * e + 1]), "f"(x[j + 2 * e]));
-              dst[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const int r = i * kPer + lane / kVec, c = lane % kVec;
+            const float4 x = stage[r * kVec + (c ^ (r & 7))];
+            const int64_t off = __shfl_sync(0xffffffffu, row_off, r) + half * kHalf + c * 4;
+            if (r < left) {
+              if (!a.direct) {
+                *reinterpret_cast<float4*>(p.po + off) = x;
+              } else if (p.out_f32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = x;
+              } else {
+                uint2 w;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) = w;
+              }
             }
-          } else {
-            float4* dst = a.direct ? reinterpret_cast<float4*>(static_cast<float*>(p.out) + qrow * p.ldo + head * HD + c * 32)
-                                   : reinterpret_cast<float4*>(p.po + at * HD + c * 32);
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) dst[j / 4] = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
           }
+          __syncwarp();
         }
       }
     }
