@@ -31,12 +31,11 @@ struct HeadParams {
   int64_t ld[3];
   void* dst[3];         // q_out, k_out or the K pool, the V pool
   int64_t ldo[3];
-  int32_t end[3];       // heads of q; of q and k; of q, k and v
+  int32_t heads[3];
   int32_t head_dim, lanes;
-  int32_t norm;
   float eps;
   const uint16_t* gain[2];
-  int32_t rot_dim, rot_style;
+  int32_t rot_dim;
   const float* cos_sin;
   int64_t max_pos;
   const int32_t* pos;
@@ -44,7 +43,9 @@ struct HeadParams {
   int64_t pool_rows;
   const int32_t* n_active;
   int32_t M;
-  int32_t chunk, chunks;  // heads per warp, warps per row
+  int32_t chunk;          // heads per warp
+  int32_t warp_end[2];    // a row's warps: those of q, then of k, then of v
+  int32_t row_warps;
   int32_t* status;
 };
 
@@ -81,16 +82,44 @@ __device__ __forceinline__ void unpack(const Raw<true>& r, float (&x)[8]) {
   x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
 }
 
+// The lane's partner elements: `from` holds them in the same order.
+__device__ __forceinline__ void partners(const Raw<false>& r, float (&y)[8], int from) {
+  uint4 v;
+  v.x = __shfl_sync(0xffffffffu, r.a.x, from);
+  v.y = __shfl_sync(0xffffffffu, r.a.y, from);
+  v.z = __shfl_sync(0xffffffffu, r.a.z, from);
+  v.w = __shfl_sync(0xffffffffu, r.a.w, from);
+  widen8(v, y);
+}
+__device__ __forceinline__ void partners(const Raw<true>& r, float (&y)[8], int from) {
+  float x[8];
+  unpack(r, x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], from);
+}
+
 // Heads in flight per group: their loads are issued together.
 constexpr int kFlight = 4;
+// Small CTAs: a warp of few heads that is done makes room at once.
+constexpr int kHeadWarps = 2, kHeadCtas = 12;
+constexpr int kMostRounds = 2;  // of kFlight heads, for one warp
 
-template <bool F32>
-__global__ void __launch_bounds__(256) heads_kernel(const __grid_constant__ HeadParams p) {
+enum { ROT_NONE = 0, ROT_OF_HALVES = 1, ROT_OF_PAIRS = 2 };
+
+// A head's result is inv * (x u + x' w) with x' the partner elements, u = gain
+// cos and w = -+ gain' sin (gain' the partner's gain): u and w are the lane's
+// for the whole row, so that a head costs two multiplications and an addition
+// per element beside its norm.  Lanes past rot_dim have u = gain and no x'.
+//
+// A warp's heads are all of one kind.  Its first heads are asked for before the
+// position, whose angles take two more trips to memory.
+template <bool F32, bool NORM, int ROT>
+__global__ void __launch_bounds__(kHeadWarps * 32, kHeadCtas) heads_kernel(const __grid_constant__ HeadParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t m64 = w / p.chunks;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kHeadWarps + (threadIdx.x >> 5);
+  const int64_t m64 = warp / p.row_warps;
   int n = p.M;
   if (p.n_active != nullptr) {
     const int a = *p.n_active;
@@ -98,133 +127,140 @@ __global__ void __launch_bounds__(256) heads_kernel(const __grid_constant__ Head
   }
   if (m64 >= n) return;  // whole warps
   const int m = static_cast<int>(m64);
-  const int first = static_cast<int>(w - m64 * p.chunks) * p.chunk;
+  const int part = static_cast<int>(warp - m64 * p.row_warps);
+  const int kind = part < p.warp_end[0] ? 0 : (part < p.warp_end[1] ? 1 : 2);
+  const int first = (part - (kind ? p.warp_end[kind - 1] : 0)) * p.chunk;
   const int sub = lane & (p.lanes - 1);      // lane in its group
   const int grp = lane / p.lanes, groups = 32 / p.lanes;
   const int e = sub * 8;                     // first element of this lane
   const bool lives = e < p.head_dim;         // a head of 192 leaves 8 lanes idle
+  const int last = first + p.chunk < p.heads[kind] ? first + p.chunk : p.heads[kind];
+  const int64_t src0 = m * p.ld[kind] + e;
 
+  Raw<F32> raw[kFlight];
+  auto ask = [&](int h0) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int h = h0 + f * groups + grp;
+      if (h < last && lives)
+        load_raw(raw[f], p.src[kind], src0 + h * p.head_dim);
+      else
+        memset(&raw[f], 0, sizeof(raw[f]));
+    }
+  };
+  ask(first);
+
+  // What a row's position and pool row allow: values need both, too.
   bool pos_ok = true;
-  float c[8], s[8];
-  int partner = lane;
-  float sign = 0.f;  // half style: -1 where this lane holds the pairs' a, +1 their b; 0: nothing here turns
-#pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = 1.f, s[j] = 0.f;
-  if (p.rot_dim > 0) {
-    const int64_t at = p.pos[m];
+  int64_t at = 0;
+  if (ROT != ROT_NONE) {
+    at = p.pos[m];
     pos_ok = at >= 0 && at < p.max_pos;
-    if (!pos_ok && lane == 0) report_status(p.status, LR_ERR_INDEX_RANGE);
-    if (pos_ok && e < p.rot_dim) {
-      const float* row = p.cos_sin + at * p.rot_dim;
-      const int half = p.rot_dim >> 1;
-      if (p.rot_style == LR_ROT_HALF) {
-        const int i = e < half ? e : e - half;
-        sign = e < half ? -1.f : 1.f;
-        partner = e < half ? lane + (half >> 3) : lane - (half >> 3);
+    if (!pos_ok && lane == 0 && part == 0) report_status(p.status, LR_ERR_INDEX_RANGE);
+  }
+  int64_t row = m;
+  bool store = true;
+  if (kind > 0 && p.rows != nullptr) {
+    row = p.rows[m];
+    const bool row_ok = row >= 0 && row < p.pool_rows;
+    if (!row_ok && lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
+    store = row_ok && pos_ok;
+  }
+  const bool maps = kind < 2;  // values pass through
+  const bool turns = ROT != ROT_NONE && maps && pos_ok && e < p.rot_dim;
+  int partner = lane;
+  float u[8], w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 cv = *reinterpret_cast<const float4*>(row + i + j);
-          const float4 sv = *reinterpret_cast<const float4*>(row + half + i + j);
-          c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
-          s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
-        }
-      } else {
-        const float4 cv = *reinterpret_cast<const float4*>(row + (e >> 1));
-        const float4 sv = *reinterpret_cast<const float4*>(row + half + (e >> 1));
-        sign = 1.f;
-        c[0] = c[1] = cv.x, c[2] = c[3] = cv.y, c[4] = c[5] = cv.z, c[6] = c[7] = cv.w;
-        s[0] = s[1] = sv.x, s[2] = s[3] = sv.y, s[4] = s[5] = sv.z, s[6] = s[7] = sv.w;
+  for (int j = 0; j < 8; ++j) u[j] = 1.f, w[j] = 0.f;
+  if (NORM && maps && lives && p.gain[kind] != nullptr) widen8(*reinterpret_cast<const uint4*>(p.gain[kind] + e), u);
+  if (turns) {
+    const float* ang = p.cos_sin + at * p.rot_dim;
+    const int half = p.rot_dim >> 1;
+    float c[8], s[8];
+    if (ROT == ROT_OF_HALVES) {
+      const bool a = e < half;  // this lane holds the pairs' a, else their b
+      const int i = a ? e : e - half;
+      partner = a ? lane + (half >> 3) : lane - (half >> 3);
+      if (NORM && p.gain[kind] != nullptr)
+        widen8(*reinterpret_cast<const uint4*>(p.gain[kind] + (a ? e + half : e - half)), w);
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 cv = *reinterpret_cast<const float4*>(ang + i + j);
+        const float4 sv = *reinterpret_cast<const float4*>(ang + half + i + j);
+        c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
+        s[j] = sv.x, s[j + 1] = sv.y, s[j + 2] = sv.z, s[j + 3] = sv.w;
+      }
+      const bool unit = !NORM || p.gain[kind] == nullptr;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] *= c[j];
+        w[j] = (a ? -s[j] : s[j]) * (unit ? 1.f : w[j]);
+      }
+    } else {
+      const float4 cv = *reinterpret_cast<const float4*>(ang + (e >> 1));
+      const float4 sv = *reinterpret_cast<const float4*>(ang + half + (e >> 1));
+      c[0] = c[1] = cv.x, c[2] = c[3] = cv.y, c[4] = c[5] = cv.z, c[6] = c[7] = cv.w;
+      s[0] = s[1] = sv.x, s[2] = s[3] = sv.y, s[4] = s[5] = sv.z, s[6] = s[7] = sv.w;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float g0 = u[j], g1 = u[j + 1];
+        w[j] = -g1 * s[j], w[j + 1] = g0 * s[j + 1];
+        u[j] = g0 * c[j], u[j + 1] = g1 * c[j + 1];
       }
     }
-  }
-  const bool half_style = p.rot_style == LR_ROT_HALF;
-  int64_t pool_row = m;
-  bool row_ok = true;
-  if (p.rows != nullptr) {
-    pool_row = p.rows[m];
-    row_ok = pool_row >= 0 && pool_row < p.pool_rows;
-    if (!row_ok && lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
   }
 
-  const int heads = p.end[2];
-  const int last = first + p.chunk < heads ? first + p.chunk : heads;
   const float inv_d = 1.f / static_cast<float>(p.head_dim);
-  int kind_of_gain = -1;
-  float g[8];
-  for (int h0 = first; h0 < last; h0 += kFlight * groups) {
-    Raw<F32> raw[kFlight];
+  uint16_t* dst = static_cast<uint16_t*>(p.dst[kind]) + row * p.ldo[kind] + e;
+  for (int h0 = first;;) {
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int h = h0 + u * groups + grp;
-      if (h < last && lives) {
-        const int kind = h < p.end[0] ? 0 : (h < p.end[1] ? 1 : 2);
-        const int head = h - (kind ? p.end[kind - 1] : 0);
-        load_raw(raw[u], p.src[kind], m * p.ld[kind] + static_cast<int64_t>(head) * p.head_dim + e);
-      } else {
-        memset(&raw[u], 0, sizeof(raw[u]));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      if (h0 + u * groups >= last) break;  // the whole warp is past its heads
-      const int h = h0 + u * groups + grp;
-      const int kind = h < p.end[0] ? 0 : (h < p.end[1] ? 1 : 2);
-      const int head = h - (kind ? p.end[kind - 1] : 0);
-      float x[8];
-      unpack(raw[u], x);
-      // Values pass through; q and k are normed and turned.  Both halves of a
-      // warp take part in the shuffles whatever their heads are.
-      if (p.norm) {
+    for (int f = 0; f < kFlight; ++f) {
+      if (h0 + f * groups >= last) break;  // the whole warp is past its heads
+      const int h = h0 + f * groups + grp;
+      float x[8], y[8];
+      unpack(raw[f], x);
+      // all of a warp takes part in the shuffles, heads or not
+      float inv = 1.f;
+      if (NORM) {
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
         for (int o = p.lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (kind < 2) {
-          if (kind != kind_of_gain) {
-            kind_of_gain = kind;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) g[j] = 1.f;
-            if (p.gain[kind] != nullptr && lives)
-              widen8(*reinterpret_cast<const uint4*>(p.gain[kind] + e), g);
-          }
-          const float inv = 1.f / sqrtf(ss * inv_d + p.eps);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
-        }
+        if (maps) inv = rsqrtf(fmaf(ss, inv_d, p.eps));
       }
-      if (p.rot_dim > 0) {
-        if (half_style) {
+      if (ROT == ROT_OF_HALVES) partners(raw[f], y, partner);
+      if (turns) {
+        if (ROT == ROT_OF_PAIRS) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float other = __shfl_sync(0xffffffffu, x[j], partner);
-            if (kind < 2 && sign != 0.f) x[j] = x[j] * c[j] + sign * (other * s[j]);
-          }
-        } else if (kind < 2 && sign != 0.f) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            const float a = x[j], b = x[j + 1];
-            x[j] = a * c[j] - b * s[j];
-            x[j + 1] = b * c[j] + a * s[j];
-          }
+          for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], u[j], y[j] * w[j]) * inv;
+      } else if (NORM && maps) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= u[j] * inv;
       }
-      if (h < last && lives) {
+      if (h < last && lives && store) {
         uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[j] = static_cast<uint32_t>(f32_to_bf16_rn(x[2 * j])) |
-                 (static_cast<uint32_t>(f32_to_bf16_rn(x[2 * j + 1])) << 16);
-        const bool pooled = kind > 0 && p.rows != nullptr;
-        if (!pos_ok) o[0] = o[1] = o[2] = o[3] = 0u;
-        if (!pooled || (row_ok && pos_ok)) {
-          const int64_t row = pooled ? pool_row : m;
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dst[kind]) + row * p.ldo[kind] +
-                                    static_cast<int64_t>(head) * p.head_dim + e) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+          memcpy(&o[j], &b, 4);
+          if (ROT != ROT_NONE && !pos_ok) o[j] = 0u;
         }
+        *reinterpret_cast<uint4*>(dst + h * p.head_dim) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    h0 += kFlight * groups;
+    if (h0 >= last) break;
+    ask(h0);
   }
+}
+
+template <bool F32, bool NORM>
+auto kernel_of(int rot) {
+  return rot == ROT_NONE ? heads_kernel<F32, NORM, ROT_NONE>
+                         : (rot == ROT_OF_HALVES ? heads_kernel<F32, NORM, ROT_OF_HALVES> : heads_kernel<F32, NORM, ROT_OF_PAIRS>);
 }
 
 lr_status bad(lr_status st, const char* fmt, ...) {
@@ -270,30 +306,29 @@ lr_status check_rows(const char* who, const char* name, const void* p, int64_t l
 lr_status launch_heads(HeadParams& p, const lr_head_map* hm, lr_dtype in_dtype, cudaStream_t s) {
   p.head_dim = hm->head_dim;
   p.lanes = hm->head_dim <= 64 ? 8 : (hm->head_dim <= 128 ? 16 : 32);
-  p.norm = hm->norm;
   p.eps = hm->eps;
   p.gain[0] = static_cast<const uint16_t*>(hm->q_gain);
   p.gain[1] = static_cast<const uint16_t*>(hm->k_gain);
   p.rot_dim = hm->rot_dim;
-  p.rot_style = hm->rot_style;
   p.cos_sin = hm->cos_sin;
   p.max_pos = hm->max_pos;
-  // Heads per warp: as few as one a group while the rows do not fill the GPU
-  // (16 warps an SM), then more, so that the angles are read once for them.
-  const int groups = 32 / p.lanes, heads = p.end[2];
+  // Heads per warp: one a group while the rows do not fill the GPU (16 warps an
+  // SM), then more, so that the angles are read once for them.
+  const int groups = 32 / p.lanes;
   const int64_t want = static_cast<int64_t>(num_sms()) * 16;
-  int chunk = groups;
-  while (chunk < heads && chunk < kFlight * groups * 4 &&
-         static_cast<int64_t>(p.M) * ((heads + chunk - 1) / chunk) > want)
-    chunk += groups;
-  p.chunk = chunk;
-  p.chunks = (heads + chunk - 1) / chunk;
-  const int64_t blocks = (static_cast<int64_t>(p.M) * p.chunks + 7) / 8;
+  auto warps_of = [&](int kind) { return (p.heads[kind] + p.chunk - 1) / p.chunk; };
+  for (p.chunk = groups;; p.chunk += groups) {
+    p.warp_end[0] = warps_of(0);
+    p.warp_end[1] = p.warp_end[0] + warps_of(1);
+    p.row_warps = p.warp_end[1] + warps_of(2);
+    if (p.chunk >= kFlight * groups * kMostRounds || static_cast<int64_t>(p.M) * p.row_warps <= want) break;
+  }
+  const int64_t blocks = (static_cast<int64_t>(p.M) * p.row_warps + kHeadWarps - 1) / kHeadWarps;
   if (blocks > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "heads: too many rows and heads for one launch");
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kHeadWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   if (pdl_enabled()) {
@@ -302,8 +337,10 @@ lr_status launch_heads(HeadParams& p, const lr_head_map* hm, lr_dtype in_dtype, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  cudaError_t e = in_dtype == LR_F32 ? cudaLaunchKernelEx(&cfg, heads_kernel<true>, p)
-                                     : cudaLaunchKernelEx(&cfg, heads_kernel<false>, p);
+  const int rot = hm->rot_dim == 0 ? ROT_NONE : (hm->rot_style == LR_ROT_HALF ? ROT_OF_HALVES : ROT_OF_PAIRS);
+  auto kern = in_dtype == LR_F32 ? (hm->norm ? kernel_of<true, true>(rot) : kernel_of<true, false>(rot))
+                                 : (hm->norm ? kernel_of<false, true>(rot) : kernel_of<false, false>(rot));
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return cuda_fail(e, "heads");
   return LR_OK;
 }
@@ -382,7 +419,7 @@ lr_status lr_qk_norm_rope(const void* q, int64_t ldq, int32_t n_heads, const voi
   p.ld[0] = ldq, p.ld[1] = ldk;
   p.dst[0] = q_out, p.dst[1] = k_out;
   p.ldo[0] = ldqo, p.ldo[1] = ldko;
-  p.end[0] = n_heads, p.end[1] = p.end[2] = n_heads + n_kv_heads;
+  p.heads[0] = n_heads, p.heads[1] = n_kv_heads;
   p.pos = pos;
   p.n_active = n_active;
   p.M = static_cast<int32_t>(M);
@@ -418,7 +455,7 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
   p.ld[0] = ldq, p.ld[1] = ldk, p.ld[2] = ldv;
   p.dst[0] = q_out, p.dst[1] = cache->k, p.dst[2] = cache->v;
   p.ldo[0] = ldqo, p.ldo[1] = p.ldo[2] = cache->ld;
-  p.end[0] = n_heads, p.end[1] = n_heads + cache->n_kv_heads, p.end[2] = n_heads + 2 * cache->n_kv_heads;
+  p.heads[0] = n_heads, p.heads[1] = p.heads[2] = cache->n_kv_heads;
   p.pos = pos;
   p.rows = rows;
   p.pool_rows = cache->pool_blocks * cache->block_rows;
