@@ -78,13 +78,10 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return static_cast<uint32_t>(r * HD * 2 + ((c ^ (r & 7)) << 4));
 }
 
-// One launch takes up to two parts: the prefix for all rows (where they are
-// too few for the tensor-core tiles) and the own tokens.
+// One launch takes both parts: the prefix for all rows and the own tokens.
 struct RowsLaunch {
-  AttnPart part[2];
-  int32_t tiles[2];   // row tiles of part 0; row tiles per sequence of part 1
-  int32_t ctas0;      // CTAs of part 0 (0: only part 1)
-  int32_t beside;     // runs beside the tiles kernel that was launched before it
+  int32_t tiles[2];   // row tiles of the prefix part; row tiles per sequence of the other
+  int32_t ctas0;      // CTAs of the prefix part
 };
 
 template <int HD>
@@ -95,10 +92,11 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
   const int G = p.group;
   // CTA -> part, row tile, key head, key range
   const int which = static_cast<int>(blockIdx.x) < rl.ctas0 ? 0 : 1;
-  const AttnPart part = which ? rl.part[1] : rl.part[0];
+  const bool prefix = which == 0;
+  const int slots = prefix ? p.prefix_slots : p.own_slots;
   int idx = static_cast<int>(blockIdx.x) - (which ? rl.ctas0 : 0);
-  const int split = idx % part.slots;
-  idx /= part.slots;
+  const int split = idx % slots;
+  idx /= slots;
   const int kvh = idx % p.n_kv;
   const int tile = idx / p.n_kv;
   const int tiles = which ? rl.tiles[1] : rl.tiles[0];
@@ -107,7 +105,7 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
   int q0, n_rows, row0, len, nq;
   const int32_t* pages;
   const bool tell = kvh == 0 && threadIdx.x == 0 && split == 0;
-  if (part.prefix) {
+  if (prefix) {
     q0 = 0;
     nq = p.M;
     len = prefix_view(p, tell);
@@ -133,12 +131,12 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = row0 + r_lo + 8 * i;
-    vis[i] = part.prefix ? len : len - nq + r / G + 1;
+    vis[i] = prefix ? len : len - nq + r / G + 1;
   }
-  kmax = part.prefix ? len : len - nq + (row0 + n_rows - 1) / G + 1;
+  kmax = prefix ? len : len - nq + (row0 + n_rows - 1) / G + 1;
   if (kmax < 0) kmax = 0;
   const int all_chunks = (kmax + kRowsChunk - 1) / kRowsChunk;
-  const int per = (all_chunks + part.slots - 1) / part.slots;
+  const int per = (all_chunks + slots - 1) / slots;
   const int c_lo = split * per;
   const int c_hi = c_lo + per < all_chunks ? c_lo + per : all_chunks;
 
@@ -300,7 +298,7 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
   }
   __syncthreads();
   const int64_t slot_rows = static_cast<int64_t>(p.M) * p.n_heads;
-  const int64_t base = (part.slot0 + split) * slot_rows;
+  const int64_t base = ((prefix ? 0 : p.prefix_slots) + split) * slot_rows;
   for (int idx = threadIdx.x; idx < n_rows * (HD / 4); idx += kRowsWarps * 32) {
     const int rr = idx / (HD / 4), c = idx % (HD / 4);
     float m = -INFINITY;
@@ -327,12 +325,8 @@ template <int HD>
 __global__ void __launch_bounds__(kRowsWarps * 32)
     attn_rows_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ RowsLaunch rl) {
   pdl_launch_dependents();
-  // Beside the tiles kernel: all that is read here was complete before that
-  // kernel let this one start; its results are waited for at the end, so that
-  // the join, which waits for this kernel, finds both.
-  if (!rl.beside) pdl_wait();
+  pdl_wait();
   attn_rows_cta<HD>(p, rl);
-  if (rl.beside) pdl_wait();
 }
 
 // --------------------------------------------------------------- join
@@ -465,9 +459,10 @@ int slots_for(int64_t ctas, int64_t keys, int64_t want, int64_t min_keys) {
 
 // How a call is cut, from its capacities alone (lengths are on the device).
 struct AttnPlan {
-  bool whole;         // prefix and own tokens in one tensor-core pass per sequence
-  bool tiles;         // the prefix on the tensor-core tiles
-  int32_t prefix_slots, own_slots;  // whole: prefix_slots counts the ranges, 0 when there is but one
+  bool tiles;         // on the tensor-core tiles; else by rows
+  bool whole;         // tiles: each sequence's rows by themselves
+  int32_t tile_slots;
+  int32_t prefix_slots, own_slots;  // slots of partial results (0, 0: none, results go straight to out)
   size_t ml_off, bytes;
 };
 
@@ -479,14 +474,17 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   const int64_t cap_prefix = static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows;
   const int64_t cap_own = static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows;
   const int64_t pair = 2 * attn_tile_rows(G);
-  a.whole = d->n_seq > 0 && mq * G > 64;
-  if (a.whole) {
-    const int n = slots_for(d->n_seq * cdiv(mq, pair) * kv, cap_prefix + cap_own, num_sms(), 512);
-    a.prefix_slots = n > 1 ? n : 0;
+  a.tiles = M * G > kRowsTile;
+  a.whole = a.tiles && d->n_seq > 0 && mq * G > 64;
+  if (a.tiles) {
+    // a packed tile pair has the own tokens of every sequence in it
+    const int64_t ctas = (a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
+    const int64_t seqs = a.whole ? 1 : (d->n_seq < pair ? d->n_seq : pair);
+    a.tile_slots = slots_for(ctas, cap_prefix + seqs * cap_own, num_sms(), a.whole ? 512 : 256);
+    if (a.tile_slots < 1) a.tile_slots = 1;
+    a.prefix_slots = a.tile_slots > 1 ? a.tile_slots : 0;
   } else {
-    a.tiles = M * G > kRowsTile;
-    a.prefix_slots = a.tiles ? slots_for(cdiv(M, pair) * kv, cap_prefix, num_sms(), 256)
-                             : slots_for(cdiv(M * G, kRowsTile) * kv, cap_prefix, num_sms() * 4, 128);
+    a.prefix_slots = slots_for(cdiv(M * G, kRowsTile) * kv, cap_prefix, num_sms() * 4, 128);
     a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, num_sms() * 4, 128);
   }
   const size_t rows = static_cast<size_t>(M) * d->n_heads * (a.prefix_slots + a.own_slots);
@@ -529,19 +527,15 @@ lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
 
 }  // namespace
 
-lr_status launch_attn_rows(const AttnParams& p, int head_dim, int prefix_slots, int own_slots, bool beside,
-                           cudaStream_t s) {
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, cudaStream_t s) {
   RowsLaunch rl;
-  memset(&rl, 0, sizeof(rl));
-  rl.part[0] = AttnPart{true, false, prefix_slots, 0};
-  rl.part[1] = AttnPart{false, false, own_slots, p.prefix_slots};
   rl.tiles[0] = cdiv(static_cast<int64_t>(p.M) * p.group, kRowsTile);
   rl.tiles[1] = cdiv(static_cast<int64_t>(p.max_q) * p.group, kRowsTile);
-  const int64_t ctas0 = static_cast<int64_t>(rl.tiles[0]) * p.n_kv * prefix_slots;
-  const int64_t ctas = ctas0 + static_cast<int64_t>(rl.tiles[1]) * p.n_seq * p.n_kv * own_slots;
+  const int64_t ctas0 = static_cast<int64_t>(rl.tiles[0]) * p.n_kv * p.prefix_slots;
+  const int64_t ctas = ctas0 + static_cast<int64_t>(rl.tiles[1]) * p.n_seq * p.n_kv * p.own_slots;
   if (ctas > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "prefix_attention: too many rows for one launch");
+  if (ctas == 0) return LR_OK;
   rl.ctas0 = static_cast<int32_t>(ctas0);
-  rl.beside = beside && pdl_enabled();
   const dim3 grid(static_cast<unsigned>(ctas));
   if (head_dim == 64)
     return launch(attn_rows_kernel<64>, grid, dim3(kRowsWarps * 32), rows_smem<64>(), s, "attn_rows", p, rl);
@@ -634,20 +628,13 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
   p.out_f32 = out_dtype == LR_F32;
   p.status = dev_status;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-  if (plan.whole) {
-    st = launch_attn_tiles(p, c.head_dim, AttnPart{true, true, plan.prefix_slots > 0 ? plan.prefix_slots : 1, 0}, cs);
-    if (st != LR_OK || plan.prefix_slots == 0) return st;
+  if (plan.tiles) {
+    st = launch_attn_tiles(p, c.head_dim, AttnPart{plan.whole, plan.tile_slots}, cs);
+    if (plan.tile_slots == 1) return st;
   } else {
-    if (plan.tiles && p.prefix_slots > 0) {
-      st = launch_attn_tiles(p, c.head_dim, AttnPart{true, false, p.prefix_slots, 0}, cs);
-      if (st != LR_OK) return st;
-    }
-    const int row_prefix = plan.tiles ? 0 : p.prefix_slots;
-    if (row_prefix + p.own_slots > 0) {
-      st = launch_attn_rows(p, c.head_dim, row_prefix, p.own_slots, plan.tiles && p.prefix_slots > 0, cs);
-      if (st != LR_OK) return st;
-    }
+    st = launch_attn_rows(p, c.head_dim, cs);
   }
+  if (st != LR_OK) return st;
   return launch_attn_join(p, c.head_dim, cs);
 }
 

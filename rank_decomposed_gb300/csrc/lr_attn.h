@@ -39,23 +39,19 @@ struct AttnParams {
   int32_t* status;
 };
 
-// The part of a call that one launch takes: the prefix for all rows of the
-// batch, each sequence's own tokens, or (whole) both for each sequence's rows;
-// cut along the keys into `slots` ranges, whose results are slots slot0 and on.
+// What a tensor-core launch takes, prefix and own tokens: each sequence's rows
+// by themselves (whole) or the rows of the batch packed into tiles; cut along
+// the keys into `slots` ranges.
 struct AttnPart {
-  bool prefix;
   bool whole;
-  int32_t slots, slot0;
+  int32_t slots;
 };
 
 // Query rows of a tensor-core tile: their heads of one key head fill its 128
 // rows as far as whole rows do.
 inline int attn_tile_rows(int group) { return 128 / group; }
 
-// The parts that go by rows: the prefix in prefix_slots ranges (0: not here),
-// the own tokens in own_slots.  beside: right after launch_attn_tiles.
-lr_status launch_attn_rows(const AttnParams& p, int head_dim, int prefix_slots, int own_slots, bool beside,
-                           cudaStream_t s);
+lr_status launch_attn_rows(const AttnParams& p, int head_dim, cudaStream_t s);
 lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& part, cudaStream_t s);
 lr_status configure_attn_tiles();
 // Tensor map over query rows [M][ld]: element (c, h, m) is column h * head_dim

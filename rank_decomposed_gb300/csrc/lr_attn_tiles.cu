@@ -4,12 +4,29 @@
 //
 // Rows are query rows times the G query heads of one key head: a tile is
 // floor(128 / G) query rows, so its G heads share every key that is loaded.
-// A CTA holds two row tiles against the same keys, or, when there are rows for
-// one tile only, one row tile against alternate keys twice; either way two
-// independent softmax rings keep the tensor pipe busy while the other one's
-// powers are computed:
+// A CTA holds two row tiles, or, when there are rows for one tile only, one row
+// tile against alternate keys twice; either way two independent softmax rings
+// keep the tensor pipe busy while the other one's powers are computed.  It walks
+// steps, one key tile of 128 keys a ring; the steps of a row tile pair are cut
+// into `slots` ranges, one a CTA.
+//   whole turns: the tiles are of one sequence's query rows; its prefix and own
+//     key tiles serve both rings.
+//   packed rows: the tiles are of any query rows of the batch, 16 or more
+//     sequences of one row each as a rule.  A prefix tile serves both rings; the
+//     own tokens of each sequence follow as tiles of their own, in the ring that
+//     holds its rows.  Only these rows take part: the other lanes' output is
+//     disabled in the product, so that no sequence's values, NaN or infinite as
+//     they may be, reach another's.  A tile of own tokens costs the tensor pipe
+//     as much for 8 rows as for 128 (1024 cycles), but its 64 KB take 2800 cycles
+//     of the SM's share of memory bandwidth, and the prefix's softmax, the reads
+//     of own tokens and their products overlap in one pipeline: against a second
+//     kernel for the own tokens, 64 sequences behind 8192 tokens took KXX us
+//     instead of 48.
 //   warps 0-3, 4-7  softmax of ring 0 and 1, one row per thread;
 //   warps 8-11      load K and V tiles of 128 keys;
+//   warp 14         looks the tiles' pages up, some tiles ahead of the loads: a
+//                   page's number takes a trip to memory, in which a loading
+//                   warp would load nothing;
 //   warp 13         hands landed tiles on: the copies write shared memory by the
 //                   generic proxy and the products read it by the async one, and
 //                   the fence between the two takes some 400 cycles, which the
@@ -41,11 +58,12 @@
 namespace lr {
 namespace {
 
-constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, a relay, two idle
-constexpr int kMmaWarp = 12, kRelayWarp = 13;
+constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, a relay, the pages, one idle
+constexpr int kMmaWarp = 12, kRelayWarp = 13, kPageWarp = 14;
+constexpr int kLooked = 8;           // tiles whose pages are known ahead
 // Registers: the launch gives 128 a thread; the softmax warps hold a row of 128
-// scores and take what the others leave (256 * 200 + 256 * 56 = 512 * 128).
-constexpr int kRegsSoftmax = 200, kRegsOther = 56;
+// scores and take what the others leave (256 * 208 + 128 * 40 + 128 * 56 = 512 * 128).
+constexpr int kRegsSoftmax = 208, kRegsLoad = 40, kRegsIssue = 56;
 constexpr int kKeys = 128;           // keys per tile
 constexpr int kPage = 16;            // rows of a page, at least
 constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 each), O0, O1 (head_dim each)
@@ -57,15 +75,15 @@ struct Shape {
   static constexpr int kChunkBytes = 128 * 128;        // 128 rows of 64 bf16
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kSlots = HD == 128 ? 5 : 10;    // ring of K and V tiles
-  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+  static constexpr int kTail = 3072;                   // barriers and the lists of own tokens
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + kTail;
 };
 
 struct TileParams {
   AttnParams p;
-  int32_t whole;      // one pass over prefix and own tokens of a sequence; else the prefix for all rows
   int32_t mt;         // query rows per tile
-  int32_t pairs;      // tile pairs per sequence (whole)
-  int32_t slots, slot0;
+  int32_t pairs;      // tile pairs per sequence (whole), or in all
+  int32_t slots;
   int32_t direct;     // one key range: results go straight to out
   int32_t stall;      // fault-injection hook: the producer issues nothing
 };
@@ -73,8 +91,9 @@ struct TileParams {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// Sixteen bytes, or sixteen zeros (src is not read then).
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
-  const int n = live ? 16 : 0;  // bytes read; the rest of the sixteen are zeros
+  const int n = live ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // Arrives on `bar` (which counts this thread) once its copies so far have landed.
@@ -165,6 +184,25 @@ __device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p_at, uint32_t 
       : "memory");
 }
 
+// The same with the output lanes of the set bits left alone (row r: bit r mod 32
+// of word r / 32), always added to O.
+__device__ __forceinline__ void mma_pv_half_some(uint32_t d, uint32_t p_at, uint32_t v_lo, uint32_t idesc,
+                                                 const uint32_t (&off)[4]) {
+  asm volatile(
+      "{\n\t.reg .pred t;\n\t.reg .b64 y;\n\t.reg .b32 a, b;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 y, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%5, %6, %7, %8}, t;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 y, {b, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t}" ::"r"(d),
+      "r"(p_at), "r"(v_lo), "r"(kDescHi), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
+      : "memory");
+}
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_lane() {
   uint32_t p;
@@ -217,29 +255,44 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-struct Bars {
+// What lies behind the tiles in shared memory.
+struct Tail {
   uint64_t q_full;
   uint64_t landed[10], full[10], empty[10];
   uint64_t s_full[2], p_ready[2][2], o_done[2];  // P is handed on in two halves of its keys
   uint64_t drain;
+  // Tiles in the order of their K loads: first pool row of each 16 keys (-1:
+  // none, zeros), and how many keys hold tokens.
+  uint64_t looked_up[kLooked], done_with[kLooked];
+  int rows[kLooked][8];
+  int fill[kLooked];
+  uint32_t tmem_base;
+  int abort;
+  int warp_sum[8];
+  // Packed rows, per query row of each tile: its sequence (-1: none), and the
+  // own key tiles of the sequences up to it, each sequence's counted at its last
+  // row in the tile.  Own tile o of a ring is of the first row with more than o.
+  int seq[2][128];
+  int tiles[2][128];
 };
+static_assert(sizeof(Tail) <= 3072, "the tail of shared memory");
 
-template <int HD>
+template <int HD, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ TileParams a, const __grid_constant__ CUtensorMap map_q) {
   using S = Shape<HD>;
   constexpr int kSlots = S::kSlots;
-  __shared__ __align__(8) Bars bars;
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_sh;
-  __shared__ float2 ml_sh[128];
-  extern __shared__ uint8_t dyn_smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const AttnParams& p = a.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t raw = smem_u32(dyn_smem);
-  uint8_t* smem = dyn_smem + (((raw + 1023u) & ~1023u) - raw);
   uint8_t* q_sm = smem;                            // two row tiles
   uint8_t* ring = smem + 2 * S::kTileBytes;
+  Tail& bars = *reinterpret_cast<Tail*>(ring + kSlots * S::kTileBytes);
+  int& abort_sh = bars.abort;
+  if (smem_u32(smem) & 1023u) {  // the swizzle's pattern needs it; there is no room to round up
+    if (threadIdx.x == 0) report_status(p.status, LR_ERR_UNSUPPORTED);
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(&bars.q_full, 1);
@@ -255,14 +308,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars.o_done[t], 1);
     }
     mbar_init(&bars.drain, 1);
+    for (int e = 0; e < kLooked; ++e) {
+      mbar_init(&bars.looked_up[e], 1);
+      mbar_init(&bars.done_with[e], 4);  // one arrival per producer warp
+    }
     abort_sh = 0;
     fence_mbar_init();
   }
-  // The kernel launched next may run beside this one (it takes the own tokens
-  // of the same batch and needs nothing of what is written here): it starts
-  // once every CTA is past this wait, when all earlier work is done.
-  pdl_wait();
   pdl_launch_dependents();
+  pdl_wait();
 
   // ---- this CTA's rows and keys
   const int kvh = blockIdx.y, split = blockIdx.z, G = p.group;
@@ -270,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int P = prefix_view(p, tell && blockIdx.x == 0);
   int q0 = 0, nq = p.M, own = 0, mrel;
   const int32_t* own_pages = nullptr;
-  if (a.whole) {
+  if (WHOLE) {
     const int b = blockIdx.x / a.pairs;
     const SeqView v = seq_view(p, b, tell && blockIdx.x % a.pairs == 0);
     q0 = v.q0, nq = v.nq, own = v.len;
@@ -279,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     mrel = blockIdx.x * 2 * a.mt;
   }
-  if (a.direct && kvh == 0 && threadIdx.x < 32 * 8) {  // rows of no sequence: zeros
+  if (WHOLE && a.direct && kvh == 0 && threadIdx.x < 32 * 8) {  // rows of no sequence: zeros
     const int from = p.q_start ? p.q_start[0] : 0, to = p.q_start ? p.q_start[p.n_seq] : p.n_seq;
     const int esz = p.out_f32 ? 4 : 2;
     const int vecs = p.n_heads * HD * esz / 16;
@@ -301,34 +355,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     return v < 0 ? 0 : v;
   };
   const int np = (P + kKeys - 1) / kKeys;
-  const int see0 = a.whole ? seen(mrel + rows0 - 1) : 0;
-  const int see1 = a.whole && !dual ? seen(mrel + a.mt + rows1 - 1) : 0;
-  const int see = see0 > see1 ? see0 : see1;
-  const int t_all = np + (see + kKeys - 1) / kKeys;
-  const int per = (t_all + a.slots - 1) / a.slots;
-  const int k_lo = split * per;
-  const int k_hi = k_lo + per < t_all ? k_lo + per : t_all;
-  const int n = k_hi > k_lo ? k_hi - k_lo : 0;     // key tiles of this CTA
-  int n0, n1;                                      // and of each ring
-  if (dual) {
-    n0 = (n + 1) >> 1;
-    n1 = n >> 1;
+  // own key tiles of each ring's rows
+  int own0, own1, see = 0;
+  if (WHOLE) {
+    const int see0 = seen(mrel + rows0 - 1), see1 = dual ? 0 : seen(mrel + a.mt + rows1 - 1);
+    see = see0 > see1 ? see0 : see1;
+    own0 = (see0 + kKeys - 1) / kKeys, own1 = (see1 + kKeys - 1) / kKeys;
   } else {
-    const int e0 = np + (see0 + kKeys - 1) / kKeys, e1 = np + (see1 + kKeys - 1) / kKeys;
-    n0 = (e0 < k_hi ? e0 : k_hi) - k_lo;
-    n1 = (e1 < k_hi ? e1 : k_hi) - k_lo;
-    if (n0 < 0) n0 = 0;
-    if (n1 < 0) n1 = 0;
+    if (threadIdx.x < 256) (&bars.seq[0][0])[threadIdx.x] = -1;
+    __syncthreads();
+    const int m_end = mrel + rows0 + rows1;
+    if (p.q_start == nullptr) {
+      const int m = mrel + static_cast<int>(threadIdx.x);
+      if (m < m_end && m < p.n_seq) bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = m;
+    } else {
+      for (int b = threadIdx.x; b < p.n_seq; b += kThreads) {
+        const int from = p.q_start[b], to = p.q_start[b + 1];
+        if ((from < 0 || to > p.M || to < from || to - from > p.max_q) && kvh == 0 && split == 0)
+          report_status(p.status, LR_ERR_INDEX_RANGE);
+        for (int m = from > mrel ? from : mrel; m < to && m < m_end; ++m)
+          bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = b;
+      }
+    }
+    __syncthreads();
+    int sum = 0;
+    if (threadIdx.x < 256) {
+      const int t = threadIdx.x >> 7, j = threadIdx.x & 127, rows = t ? rows1 : rows0;
+      const int b = bars.seq[t][j];
+      if (j < rows && b >= 0 && (j == rows - 1 || bars.seq[t][j + 1] != b)) {
+        const SeqView v = seq_view(p, b, kvh == 0 && split == 0);
+        int vis = v.len - v.nq + (mrel + t * a.mt + j - v.q0) + 1;
+        vis = vis > v.len ? v.len : vis;
+        if (vis > 0) sum = (vis + kKeys - 1) / kKeys;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      if (lane == 31) bars.warp_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      for (int w = warp & ~3; w < warp; ++w) sum += bars.warp_sum[w];
+      (&bars.tiles[0][0])[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    own0 = bars.tiles[0][127], own1 = bars.tiles[1][127];
   }
+  // Steps: step s is key tile s of both rings' lists (prefix tiles, then own
+  // ones), or, with one row tile, tiles 2 s and 2 s + 1 of its list.
+  const int list0 = np + own0, list1 = dual ? list0 : np + own1;
+  const int e0 = dual ? (list0 + 1) >> 1 : list0, e1 = dual ? list0 >> 1 : list1;  // steps that ring 0, 1 take
+  const int64_t steps = e0 > e1 ? e0 : e1;
+  const int s_lo = static_cast<int>(steps * split / a.slots), s_hi = static_cast<int>(steps * (split + 1) / a.slots);
+  auto of_range = [&](int e) {
+    const int c = (e < s_hi ? e : s_hi) - s_lo;
+    return c < 0 ? 0 : c;
+  };
+  const int n = s_hi - s_lo, n0 = of_range(e0), n1 = of_range(e1);  // n is the larger of the two
+  // the first n_both of them have one key tile for both rings
+  const int n_both = dual ? 0 : (WHOLE ? n : of_range(np));
+  // Own tile o of ring t's list of packed rows: the row of the tile that it is
+  // counted at, found from a row at or before it.
+  auto own_row = [&](int t, int o, int from) {
+    const int* tiles = bars.tiles[dual ? 0 : t];
+    while (from < 127 && tiles[from] <= o) ++from;
+    return from;
+  };
 
   if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_base_sh, kTmemCols);
+    tmem_alloc(&bars.tmem_base, kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tmem = bars.tmem_base;
 
   // softmax state of this thread's row
   const int ringi = warp >> 2;                     // 0, 1: softmax warps
@@ -336,11 +439,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile = dual ? 0 : (ringi & 1);
   const int live_rows = (tile ? rows1 : rows0) * G;
   const int my_n = (ringi & 1) ? n1 : n0;
+  const int my_seq = WHOLE || trow / G >= a.mt ? -1 : bars.seq[tile][trow / G];
   float mref = -INFINITY, sum = 0.f;
+  float2* hand_ml = reinterpret_cast<float2*>(ring + 128 * (HD + 4) * 4);  // behind ring 1's numerators
 
   if (warp >= 8) {
-    regs_fewer<kRegsOther>();
     if (warp < kMmaWarp) {
+      regs_fewer<kRegsLoad>();
       // ---------------------------------------------------- producers
       if (!a.stall && n > 0) {
         if (warp == 8 && lane == 0) {
@@ -365,77 +470,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = j * kRows + r_in;
           dst0[j] = smem_u32(ring) + (col >> 3) * S::kChunkBytes + (g0 * kPage + r) * 128 + (((col & 7) ^ r) << 4);
         }
-        // Page of the keys of group g of tile k, fetched some tiles ahead of its
-        // use; kNone where there are no keys.
-        constexpr int kNone = INT32_MIN;
-        auto index_of = [&](int t) { return p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows; };
-        auto page_of = [&](int k, int g) {
-          const bool pre = k < np;
-          const int t = (pre ? k : k - np) * kKeys + g * kPage;
-          if (k >= k_hi || t >= (pre ? P : see)) return kNone;
-          return (pre ? p.prefix_blocks : own_pages)[index_of(t)];
-        };
-        // Its first pool row, or -1 for none (a page outside the pool among them).
-        auto row_of = [&](int page, int k, int g) {
-          if (page == kNone) return -1;
-          if (page < 0 || page >= p.pool_blocks) {
-            if (lane == 0) report_status(p.status, LR_ERR_REMAP_RANGE);
-            return -1;
-          }
-          const int t = (k < np ? k : k - np) * kKeys + g * kPage;
-          return page * p.block_rows + (t - index_of(t) * p.block_rows);
-        };
-        int ld = 0;
+        const uint32_t dst_row = smem_u32(ring) + (col >> 3) * S::kChunkBytes + (g0 * kPage + r_in) * 128;
+        // In the order in which the products take the tiles: V of step i and K of
+        // the next, ring by ring, or once for both.  One copy of the loading code
+        // serves all (the loops stay loops): every warp role runs code of its own
+        // and all of it has to stay in the instruction caches.
+        int slot = 0, tile_no = 0;
+        int at0 = 0, at1 = 0;  // the number of each ring's tile
+        uint32_t phase = 1;
         bool ok = true;
-        auto load = [&](const uint16_t* pool, int row_a, int row_b, int k) {
-          if (!ok) return;
-          const int s = ld % kSlots;
-          ok = mbar_wait(&bars.empty[s], ((ld / kSlots) & 1) ^ 1, &abort_sh);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) return;
-          const int fill = (k < np ? P - k * kKeys : see - (k - np) * kKeys) - g0 * kPage;  // keys from the first group on
+#pragma unroll 1
+        for (int i = -1; i < n && ok; ++i) {
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            const int t = x >> 1, is_k = x & 1;
+            const int j = i + is_k;  // the step that the tile is of
+            if (j < 0 || !(j < n_both ? t == 0 : j < (t ? n1 : n0))) continue;
+            int e = t ? at1 : at0;
+            if (is_k) {
+              e = tile_no++;
+              if (t)
+                at1 = e;
+              else
+                at0 = e;
+              ok = mbar_wait(&bars.looked_up[e % kLooked], (e / kLooked) & 1, &abort_sh);
+            }
+            e %= kLooked;
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.empty[slot], phase, &abort_sh));
+            if (!ok) break;
+            const uint16_t* pool = is_k ? p.k : p.v;
+            const int fill = bars.fill[e] - g0 * kPage;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = h ? row_b : row_a;
-            const int live = row < 0 ? 0 : fill - h * kPage;
-            const uint16_t* src = pool + (row < 0 ? 0 : static_cast<int64_t>(row + r_in) * p.ld) + head_off;
-            const uint32_t at = s * S::kTileBytes + h * kPage * 128;
-            if (live >= kPage) {
+            for (int h = 0; h < 2; ++h) {
+              const int row = bars.rows[e][g0 + h];
+              const int live = row < 0 ? 0 : fill - h * kPage;
+              const uint16_t* src = pool + static_cast<int64_t>((row < 0 ? 0 : row) + r_in) * p.ld + head_off;
+              const uint32_t at = slot * S::kTileBytes + h * kPage * 128;
+              if (live >= kPage) {
 #pragma unroll
-              for (int j = 0; j < kPage / kRows; ++j, src += step)
-                cp_async16(dst0[j % kTurn] + at + j / kTurn * 1024, src);
-            } else {
-#pragma unroll
-              for (int j = 0; j < kPage / kRows; ++j, src += step) {
-                const bool in = j * kRows + r_in < live;
-                cp_async16_or_zero(dst0[j % kTurn] + at + j / kTurn * 1024, in ? src : pool, in);
+                for (int c = 0; c < kPage / kRows; ++c, src += step)
+                  cp_async16(dst0[c % kTurn] + at + c / kTurn * 1024, src);
+              } else {
+#pragma unroll 1
+                for (int c = 0; c < kPage / kRows; ++c, src += step)
+                  cp_async16_or_zero(dst_row + at + c * kRows * 128 + (((c * kRows + r_in) ^ col) & 7) * 16, src,
+                                     c * kRows + r_in < live);
               }
             }
+            cp_async_arrive(&bars.landed[slot]);
+            if (++slot == kSlots) slot = 0, phase ^= 1;
+            if (!is_k) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars.done_with[e]);
+            }
           }
-          cp_async_arrive(&bars.landed[s]);
-          ++ld;
-        };
-        // K runs `ahead` tiles before V; the pages two tiles before K.
-        const int ahead = dual ? 2 : 1;
-        int now_a = row_of(page_of(k_lo, g0), k_lo, g0), now_b = row_of(page_of(k_lo, g0 + 1), k_lo, g0 + 1);
-        int next_a = 0, next_b = 0;
-        load(p.k, now_a, now_b, k_lo);
-        if (dual && n > 1) {
-          next_a = row_of(page_of(k_lo + 1, g0), k_lo + 1, g0), next_b = row_of(page_of(k_lo + 1, g0 + 1), k_lo + 1, g0 + 1);
-          load(p.k, next_a, next_b, k_lo + 1);
-        }
-        int page_a = page_of(k_lo + ahead, g0), page_b = page_of(k_lo + ahead, g0 + 1);
-        int page2_a = page_of(k_lo + ahead + 1, g0), page2_b = page_of(k_lo + ahead + 1, g0 + 1);
-#pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
-          const int kn = k_lo + i + ahead;
-          load(p.v, now_a, now_b, k_lo + i);
-          const int new_a = row_of(page_a, kn, g0), new_b = row_of(page_b, kn, g0 + 1);
-          page_a = page2_a, page_b = page2_b;
-          page2_a = page_of(kn + 2, g0), page2_b = page_of(kn + 2, g0 + 1);
-          if (i + ahead < n) load(p.k, new_a, new_b, kn);
-          now_a = dual ? next_a : new_a, now_b = dual ? next_b : new_b;
-          next_a = new_a, next_b = new_b;
         }
         cp_async_wait_all();
         if (!ok && lane == 0) {
@@ -444,111 +532,170 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (warp == 8) mbar_wait(&bars.q_full, 0, nullptr);  // the copy in flight lands before the CTA ends
         }
       }
-    } else if (warp == kRelayWarp) {
-      bool ok = true;
+    } else {
+      regs_fewer<kRegsIssue>();
+      if (warp == kPageWarp) {
+        // ------------------------------------------------------- pages
+        bool ok = true;
+        int e = 0, at_row0 = 0, at_row1 = 0;
+        auto index_of = [&](int t) { return p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows; };
 #pragma unroll 1
-      for (int l = 0; l < 2 * n && ok; ++l) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.landed[l % kSlots], (l / kSlots) & 1, &abort_sh));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&bars.full[l % kSlots]);
-      }
-      if (!ok && lane == 0) {
-        abort_sh = 1;
-        report_status(p.status, LR_ERR_TIMEOUT);
-      }
-    } else if (warp == kMmaWarp) {
-      // ----------------------------------------------------------- MMA
-      if (n > 0 && elect_lane()) {
-        constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
-        constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
-        const uint32_t q_lo = desc_lo(smem_u32(q_sm), 16), r_k = desc_lo(smem_u32(ring), 16);
-        const uint32_t r_v = desc_lo(smem_u32(ring), S::kChunkBytes);
-        const uint32_t q_step = dual ? 0 : S::kTileBytes >> 4;
-        bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
-        // The ring's slots in the order of the loads: wait for the next one.
-        int slot = -1;
-        uint32_t phase = 0;
-        auto next_slot = [&]() {
-          if (++slot == kSlots) slot = 0, phase ^= 1;
-          if (ok) ok = mbar_wait(&bars.full[slot], phase, &abort_sh);
-          tc_fence_after();
-          return slot;
-        };
-        auto qk = [&](int t, int at) {
-          if (!ok) return;
-          const uint32_t k_at = r_k + at * (S::kTileBytes >> 4), q_at = q_lo + t * q_step;
-#pragma unroll
-          for (int c = 0; c < S::kChunks; ++c)
-            mma_qk_chunk(tmem + t * kKeys, q_at + c * (S::kChunkBytes >> 4), k_at + c * (S::kChunkBytes >> 4), kIdS, c);
-          tc_commit(&bars.s_full[t]);
-        };
-        // round r of ring t; its last one completes the ring's O
-        auto pv = [&](int t, int at, int r, bool last) {
-          const uint32_t v_at = r_v + at * (S::kTileBytes >> 4), p_at = tmem + t * kKeys;
-          if (ok) ok = mbar_wait(&bars.p_ready[t][0], r & 1, &abort_sh);
-          if (!ok) return;
-          tc_fence_after();
-          mma_pv_half(tmem + 256 + t * HD, p_at, v_at, kIdO, r);
-          ok = mbar_wait(&bars.p_ready[t][1], r & 1, &abort_sh);
-          if (!ok) return;
-          tc_fence_after();
-          mma_pv_half(tmem + 256 + t * HD, p_at + 32, v_at + (64 * 128 >> 4), kIdO, 1);
-          if (last) tc_commit(&bars.o_done[t]);
-        };
-        auto release = [&](int at) {
-          if (ok) tc_commit(&bars.empty[at]);
-        };
-        if (dual) {
-          qk(0, next_slot());
-          release(slot);
-          if (n > 1) {
-            qk(1, next_slot());
-            release(slot);
-          }
-#pragma unroll 1
-          for (int i = 0; i < n && ok; ++i) {
-            const int t = i & 1;
-            pv(t, next_slot(), i >> 1, i + 2 >= n);
-            release(slot);
-            if (i + 2 < n) {
-              qk(t, next_slot());
-              release(slot);
+        for (int x = 0; x < (a.stall ? 0 : 2 * n) && ok; ++x) {
+          const int j = x >> 1, t = x & 1;
+          if (!(j < n_both ? t == 0 : j < (t ? n1 : n0))) continue;
+          const int c = dual ? 2 * (s_lo + j) + t : s_lo + j;
+          const int32_t* pages = p.prefix_blocks;
+          int t0 = c * kKeys, limit = P;
+          if (c >= np) {
+            const int o = c - np;
+            pages = own_pages;
+            t0 = o * kKeys, limit = see;
+            if (!WHOLE) {
+              const int list = dual ? 0 : t;
+              const int r = own_row(t, o, t ? at_row1 : at_row0);
+              (t ? at_row1 : at_row0) = r;
+              const int b = bars.seq[list][r];
+              pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
+              const int len = p.lengths[b];
+              t0 = (o - (r > 0 ? bars.tiles[list][r - 1] : 0)) * kKeys;
+              limit = len < p.cap_own ? len : p.cap_own;
             }
           }
-        } else {
-          const int first = next_slot();
-          if (n0 > 0) qk(0, first);
-          if (n1 > 0) qk(1, first);
-          release(first);
-#pragma unroll 1
-          for (int i = 0; i < n && ok; ++i) {
-            const int at_v = next_slot();
-            int at_k = -1;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int mine = t ? n1 : n0;
-              if (i < mine) {
-                pv(t, at_v, i, i + 1 == mine);
-                if (i + 1 < mine) {
-                  if (at_k < 0) at_k = next_slot();
-                  qk(t, at_k);
-                }
-              }
-            }
-            release(at_v);
-            if (at_k >= 0) release(at_k);
+          const int tg = t0 + (lane & 7) * kPage;  // the first of this lane's 16 keys
+          int row = -1;
+          if (tg < limit) {
+            const int k = index_of(tg);
+            const int page = pages[k];
+            if (page < 0 || page >= p.pool_blocks)
+              report_status(p.status, LR_ERR_REMAP_RANGE);  // reads as zeros
+            else
+              row = page * p.block_rows + (tg - k * p.block_rows);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.done_with[e % kLooked], ((e / kLooked) & 1) ^ 1, &abort_sh));
+          if (ok) {
+            if (lane < 8) bars.rows[e % kLooked][lane] = row;
+            if (lane == 0) bars.fill[e % kLooked] = limit - t0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.looked_up[e % kLooked]);
+            ++e;
           }
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
           abort_sh = 1;
           report_status(p.status, LR_ERR_TIMEOUT);
         }
-        // every MMA issued by this thread completes before TMEM is released
-        tc_commit(&bars.drain);
-        mbar_wait(&bars.drain, 0, nullptr);
+      } else if (warp == kRelayWarp) {
+        bool ok = true;
+        const int loads = 2 * (n_both + (n0 > n_both ? n0 - n_both : 0) + (n1 > n_both ? n1 - n_both : 0));
+#pragma unroll 1
+        for (int l = 0; l < loads && ok; ++l) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.landed[l % kSlots], (l / kSlots) & 1, &abort_sh));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&bars.full[l % kSlots]);
+        }
+        if (!ok && lane == 0) {
+          abort_sh = 1;
+          report_status(p.status, LR_ERR_TIMEOUT);
+        }
+      } else if (warp == kMmaWarp) {
+        // ----------------------------------------------------------- MMA
+        if (n > 0 && elect_lane()) {
+          constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
+          constexpr uint32_t kIdO = idesc_bf16_f32(128, HD) | (1u << 16);  // B is MN-major
+          const uint32_t q_lo = desc_lo(smem_u32(q_sm), 16), r_k = desc_lo(smem_u32(ring), 16);
+          const uint32_t r_v = desc_lo(smem_u32(ring), S::kChunkBytes);
+          const uint32_t q_step = dual ? 0 : S::kTileBytes >> 4;
+          bool ok = mbar_wait(&bars.q_full, 0, &abort_sh);
+          // The ring's slots in the order of the loads: wait for the next one.
+          int slot = -1;
+          uint32_t phase = 0;
+          auto next_slot = [&]() {
+            if (++slot == kSlots) slot = 0, phase ^= 1;
+            if (ok) ok = mbar_wait(&bars.full[slot], phase, &abort_sh);
+            tc_fence_after();
+            return slot;
+          };
+          auto qk = [&](int t, int at) {
+            if (!ok) return;
+            const uint32_t k_at = r_k + at * (S::kTileBytes >> 4), q_at = q_lo + t * q_step;
+#pragma unroll
+            for (int c = 0; c < S::kChunks; ++c)
+              mma_qk_chunk(tmem + t * kKeys, q_at + c * (S::kChunkBytes >> 4), k_at + c * (S::kChunkBytes >> 4), kIdS, c);
+            tc_commit(&bars.s_full[t]);
+          };
+          // round r of ring t; its last one completes the ring's O
+          int at_row0 = 0, at_row1 = 0;
+          auto pv = [&](int t, int at, int r, bool last) {
+            const uint32_t v_at = r_v + at * (S::kTileBytes >> 4), p_at = tmem + t * kKeys, d = tmem + 256 + t * HD;
+            uint32_t off[4] = {0, 0, 0, 0};
+            if (!WHOLE) {  // rows of other sequences keep their O
+              const int c = dual ? 2 * (s_lo + r) + t : s_lo + r;
+              if (c >= np) {
+                const int* seq = bars.seq[dual ? 0 : t];
+                const int j = own_row(t, c - np, t ? at_row1 : at_row0);
+                (t ? at_row1 : at_row0) = j;
+                int from = j;
+                while (from > 0 && seq[from - 1] == seq[j]) --from;
+                const int lo = from * G, hi = (j + 1) * G;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const int x = lo - 32 * w, y = hi - 32 * w;
+                  const uint32_t below = x <= 0 ? 0u : (x >= 32 ? ~0u : (1u << x) - 1u);
+                  const uint32_t under = y <= 0 ? 0u : (y >= 32 ? ~0u : (1u << y) - 1u);
+                  off[w] = ~(under & ~below);
+                }
+              }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok) ok = mbar_wait(&bars.p_ready[t][half], r & 1, &abort_sh);
+              if (!ok) return;
+              tc_fence_after();
+              if (WHOLE)
+                mma_pv_half(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, r | half);
+              else
+                mma_pv_half_some(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, off);
+            }
+            if (last) tc_commit(&bars.o_done[t]);
+          };
+          auto release = [&](int at) {
+            if (ok) tc_commit(&bars.empty[at]);
+          };
+          // Step i's second products, then the next step's first ones (step -1: the
+          // first ones alone).  A tile for both rings is released after the second
+          // ring's product.
+#pragma unroll 1
+          for (int i = -1; i < n && ok; ++i) {
+            const bool both = i < n_both, both1 = i + 1 < n_both;
+            int at_v = -1, at_k = -1;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int mine = t ? n1 : n0;
+              if (i >= 0 && i < mine) {
+                if (!both || at_v < 0) at_v = next_slot();
+                pv(t, at_v, i, i + 1 == mine);
+                if (!both) release(at_v);
+              }
+              if (i + 1 < mine) {
+                if (!both1 || at_k < 0) at_k = next_slot();
+                qk(t, at_k);
+                if (!both1) release(at_k);
+              }
+            }
+            if (both && at_v >= 0) release(at_v);
+            if (both1 && at_k >= 0) release(at_k);
+          }
+          if (!ok) {
+            abort_sh = 1;
+            report_status(p.status, LR_ERR_TIMEOUT);
+          }
+          // every MMA issued by this thread completes before TMEM is released
+          tc_commit(&bars.drain);
+          mbar_wait(&bars.drain, 0, nullptr);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   } else {
     regs_more<kRegsSoftmax>();
@@ -558,8 +705,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * HD + lanes;
       // own tokens that this row sees (rows past the tile's are never stored)
-      const int m_row = mrel + tile * a.mt + trow / G;
-      const int vis = a.whole ? seen(m_row) : 0;
+      int vis = 0, at_row = 0;
+      if (WHOLE) {
+        vis = seen(mrel + tile * a.mt + trow / G);
+      } else if (my_seq >= 0) {
+        const SeqView v = seq_view(p, my_seq, false);
+        vis = v.len - v.nq + (mrel + tile * a.mt + trow / G - v.q0) + 1;
+        if (vis > v.len) vis = v.len;
+      }
+      if (!WHOLE) {  // the rows of a tile do not all take part in its first product
+        uint32_t z[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = 0;
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) tmem_st32(o_at + c * 32, z);
+        tmem_st_wait();
+      }
       const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
       bool ok = true;
       for (int i = 0; i < my_n && ok; ++i) {
@@ -567,9 +728,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (busy) {
-          const int k = k_lo + (dual ? 2 * i + t : i);
-          const int lim = k < np ? P - k * kKeys : vis - (k - np) * kKeys;
+        // keys of the tile that the row sees
+        const int c = dual ? 2 * (s_lo + i) + t : s_lo + i;
+        int lim = P - c * kKeys;
+        if (c >= np) {
+          lim = vis - (c - np) * kKeys;
+          if (!WHOLE) {
+            const int list = dual ? 0 : t;
+            at_row = own_row(t, c - np, at_row);
+            lim = bars.seq[list][at_row] == my_seq
+                      ? vis - (c - np - (at_row > 0 ? bars.tiles[list][at_row - 1] : 0)) * kKeys
+                      : 0;
+          }
+        }
+        if (busy && !__any_sync(0xffffffffu, lim > 0)) {  // none of the warp's rows: P = 0
+          uint32_t z[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = 0;
+          tmem_st32(s_at, z);
+          tmem_st32(s_at + 32, z);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.p_ready[t][0]);
+        } else if (busy) {
           uint32_t s[kKeys];
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
@@ -655,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         report_status(p.status, LR_ERR_TIMEOUT);
       }
       if (ok && dual && t == 1 && n1 > 0 && busy) {  // ring 1 hands its part to ring 0
-        ml_sh[trow] = make_float2(mref, sum);
+        hand_ml[trow] = make_float2(mref, sum);
         float* dst = reinterpret_cast<float*>(ring) + trow * (HD + 4);
 #pragma unroll
         for (int c = 0; c < HD / 32; ++c) {
@@ -681,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool both = dual && n1 > 0;
         float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
         if (both) {
-          const float2 o = ml_sh[trow];
+          const float2 o = hand_ml[trow];
           m = fmaxf(mref, o.x);
           const float ref = m == -INFINITY ? 0.f : m;
           f0 = ex2(mref - ref);
@@ -691,9 +873,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_n == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
         const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
         const int head = kvh * G + trow % G;
-        const int64_t at = (static_cast<int64_t>(a.slot0 + split) * p.M + qrow) * p.n_heads + head;
+        const int64_t at = (static_cast<int64_t>(split) * p.M + qrow) * p.n_heads + head;
         if (a.direct) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          // a packed row of no sequence comes out zero, and so does one that saw no key
+          const float inv = l == 0.f || (!WHOLE && my_seq < 0) ? 0.f : 1.f / l;
           f0 *= inv;
           f1 *= inv;
         } else if (live) {
@@ -761,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int HD>
+template <int HD, bool WHOLE>
 lr_status launch_tiles(const TileParams& a, dim3 grid, cudaStream_t s) {
   using Sh = Shape<HD>;
   CUtensorMap mq;
@@ -780,7 +963,7 @@ lr_status launch_tiles(const TileParams& a, dim3 grid, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<HD>, a, mq);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<HD, WHOLE>, a, mq);
   if (e != cudaSuccess) return cuda_fail(e, "attn_tiles");
   return LR_OK;
 }
@@ -791,22 +974,25 @@ lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& p
   TileParams a;
   memset(&a, 0, sizeof(a));
   a.p = p;
-  a.whole = part.whole;
   a.mt = attn_tile_rows(p.group);
   const int per_pair = 2 * a.mt;
   a.pairs = ((part.whole ? p.max_q : p.M) + per_pair - 1) / per_pair;
   a.slots = part.slots;
-  a.slot0 = part.slot0;
-  a.direct = part.whole && part.slots == 1;
+  a.direct = part.slots == 1;
   a.stall = test_stall_producer();
   const dim3 grid(part.whole ? a.pairs * p.n_seq : a.pairs, p.n_kv, part.slots);
-  return head_dim == 64 ? launch_tiles<64>(a, grid, s) : launch_tiles<128>(a, grid, s);
+  if (head_dim == 64) return part.whole ? launch_tiles<64, true>(a, grid, s) : launch_tiles<64, false>(a, grid, s);
+  return part.whole ? launch_tiles<128, true>(a, grid, s) : launch_tiles<128, false>(a, grid, s);
 }
 
 lr_status configure_attn_tiles() {
-  cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<64>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(attn_tiles_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<128>::kSmem);
+  auto set = [](auto kern, int smem) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  cudaError_t e = set(attn_tiles_kernel<64, true>, Shape<64>::kSmem);
+  if (e == cudaSuccess) e = set(attn_tiles_kernel<64, false>, Shape<64>::kSmem);
+  if (e == cudaSuccess) e = set(attn_tiles_kernel<128, true>, Shape<128>::kSmem);
+  if (e == cudaSuccess) e = set(attn_tiles_kernel<128, false>, Shape<128>::kSmem);
   if (e != cudaSuccess) return cuda_fail(e, "attention tiles: set smem");
   return LR_OK;
 }

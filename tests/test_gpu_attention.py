@@ -125,6 +125,40 @@ def test_ragged_rows_match_oracle(nh, nkv, hd, prefix, lens, qs, br):
     close(out, *b.want())
 
 
+FEW_ROWS = [  # some query rows a sequence, packed into tiles that cut through sequences
+    (8, 2, 64, 100, [30, 7, 64, 9, 150], [3, 1, 7, 9, 2], 16),
+    (8, 1, 128, 300, [5, 140, 2, 0, 33, 260], [5, 8, 8, 0, 0, 7], 16),       # rows before their tokens, no rows
+    (4, 4, 128, 131, [40 + i for i in range(20)], [1 + i % 9 for i in range(20)], 32),
+    (2, 2, 64, 0, [130 * (i % 3) + 1 for i in range(150)], [1 + i % 3 for i in range(150)], 16),   # two tiles, no prefix
+    (28, 4, 128, 700, [20, 300, 129], [9, 9, 9], 48),                        # seven heads a key head
+    (6, 3, 128, 0, [0] * 12, [3] * 12, 16),                                  # nothing to see at all
+]
+
+
+@pytest.mark.parametrize("nh,nkv,hd,prefix,lens,qs,br", FEW_ROWS)
+def test_few_rows_a_sequence_match_oracle(nh, nkv, hd, prefix, lens, qs, br):
+    b = Batch(22, nh, nkv, hd, prefix, lens, qs=qs, br=br)
+    out = b.run()
+    assert int(b.status.item()) == 0
+    close(out, *b.want())
+
+
+@pytest.mark.parametrize("nh,nkv,hd,n,bad", [(8, 1, 128, 40, 7), (8, 1, 128, 3, 1), (4, 4, 64, 200, 130), (64, 8, 128, 20, 0),
+                                             (16, 2, 64, 1, 0)])
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+def test_one_sequence_s_values_do_not_reach_another(nh, nkv, hd, n, bad, what):
+    """NaN or infinities among a sequence's own values show in its rows alone, though rows share their tiles."""
+    b = Batch(23, nh, nkv, hd, 260, [5 + 37 * i % 200 for i in range(n)])
+    want, mag = b.want()
+    clean = b.run()
+    b.vp[b.rows_of(b.table[bad], b.lens[bad])] = what
+    out = b.run()
+    rest = [i for i in range(n) if i != bad]
+    assert not torch.isfinite(out[bad]).any()
+    assert torch.equal(out[rest], clean[rest])
+    close(out[rest], want[rest], mag[rest])
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("nh,nkv", [(8, 2), (2, 2), (16, 1)])
 def test_rows_that_see_nothing_are_zero(hd, nh, nkv):
@@ -225,6 +259,13 @@ def test_row_offsets_that_are_wrong_are_reported():
         b.run(out=out[1:51])
         assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, starts
         assert torch.all(out[0] == 7.0) and torch.all(out[51] == 7.0)
+    for starts, max_q in (([0, 8, 4, 10], 8), ([-3, 2, 6, 10], 8), ([0, 2, 6, 1 << 30], 8), ([0, 3, 4, 10], 5)):
+        b = Batch(13, 8, 2, 64, 64, [48, 16, 200], qs=[2, 2, 6])
+        b.d.update(q_start=_i32(starts), max_q=max_q)
+        out = torch.full((12, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+        b.run(out=out[1:11])
+        assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, starts
+        assert torch.all(out[0] == 7.0) and torch.all(out[11] == 7.0)
 
 
 @pytest.mark.parametrize("n", [3, 40])
