@@ -330,60 +330,50 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
 }
 
 // --------------------------------------------------------------- join
-// One warp per (row, head): the slots' numerators with their weights.  Bound
-// by the partial results, which were written just before and lie in L2.
+// W warps per (row, head), each with every W-th slot's numerators and all
+// slots' weights.  Bound by the way to the partial results, which were written
+// just before and lie in L2: one warp for few slots (its loads of four slots are
+// in flight together), four for many (38 slots of 320 rows: 14 us with one warp).
 constexpr int kMaxSlots = 64;  // of each part
-constexpr int kJoinSets = 2 * kMaxSlots / 32;
 
-template <int HD>
+template <int HD, int W>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = HD / 32;  // elements per lane
+  constexpr int kRows = 8 / W;
+  __shared__ float parts[W > 1 ? 8 : 1][HD];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t rows = static_cast<int64_t>(p.M) * p.n_heads;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + warp / W;
   const int m = static_cast<int>(r / p.n_heads), h = static_cast<int>(r - static_cast<int64_t>(m) * p.n_heads);
   int from = 0, to = p.n_seq;
   if (p.q_start != nullptr) {
     from = p.q_start[0];
     to = p.n_seq > 0 ? p.q_start[p.n_seq] : from;
   }
-  float acc[kE];
+  float acc[kE], inv = 0.f;
 #pragma unroll
   for (int j = 0; j < kE; ++j) acc[j] = 0.f;
-  if (m >= from && m < to) {
-    // lane i holds slots i, i + 32, ..: their weights, and the sum of all
+  if (r < rows && m >= from && m < to) {
     const int slots = p.prefix_slots + p.own_slots;
-    float2 ml[kJoinSets];
     float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kJoinSets; ++k) {
-      const int i = k * 32 + lane;
-      ml[k] = i < slots ? p.pml[i * rows + r] : make_float2(-INFINITY, 0.f);
-      top = fmaxf(top, ml[k].x);
-    }
+    for (int i = lane; i < slots; i += 32) top = fmaxf(top, p.pml[i * rows + r].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
-    float w[kJoinSets], l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinSets; ++k) {
-      w[k] = ml[k].y == 0.f ? 0.f : exp2f(ml[k].x - ref);  // 0: nothing was stored
-      l += w[k] * ml[k].y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
-#pragma unroll
-    for (int k = 0; k < kJoinSets; ++k) {
-      const int here = slots - k * 32 < 32 ? slots - k * 32 : 32;
-#pragma unroll 8
-      for (int i = 0; i < here; ++i) {
+    float l = 0.f;
+    for (int i0 = 0; i0 < slots; i0 += 32) {
+      // lane i holds the weight of slot i0 + i
+      const float2 ml = i0 + lane < slots ? p.pml[(i0 + lane) * rows + r] : make_float2(-INFINITY, 0.f);
+      const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);  // 0: nothing was stored
+      l += w * ml.y;
+      const int here = slots - i0 < 32 ? slots - i0 : 32;
+#pragma unroll 4
+      for (int i = warp % W; i < here; i += W) {
         // no branch on the weight, so that several slots' loads are in flight
-        const float f = __shfl_sync(0xffffffffu, w[k], i);
-        const float* src = p.po + ((k * 32 + i) * rows + r) * HD + lane * kE;
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        const float* src = p.po + ((i0 + i) * rows + r) * HD + lane * kE;
         if (kE == 4) {
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
           if (f != 0.f) x = *reinterpret_cast<const float4*>(src);
@@ -396,8 +386,22 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       }
     }
 #pragma unroll
-    for (int j = 0; j < kE; ++j) acc[j] *= inv;
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
   }
+  if (W > 1) {
+#pragma unroll
+    for (int j = 0; j < kE; ++j) parts[warp][lane * kE + j] = acc[j];
+    __syncthreads();
+    if (warp % W) return;
+#pragma unroll
+    for (int j = 0; j < kE; ++j)
+#pragma unroll
+      for (int k = 1; k < W; ++k) acc[j] += parts[warp + k][lane * kE + j];
+  }
+  if (r >= rows) return;
+#pragma unroll
+  for (int j = 0; j < kE; ++j) acc[j] *= inv;
   const int64_t off = static_cast<int64_t>(m) * p.ldo + static_cast<int64_t>(h) * HD + lane * kE;
   if (p.out_f32) {
     float* dst = static_cast<float*>(p.out) + off;
@@ -462,6 +466,7 @@ struct AttnPlan {
   bool tiles;         // on the tensor-core tiles; else by rows
   bool whole;         // tiles: each sequence's rows by themselves
   int32_t tile_slots;
+  bool two;
   int32_t prefix_slots, own_slots;  // slots of partial results (0, 0: none, results go straight to out)
   size_t ml_off, bytes;
 };
@@ -481,8 +486,12 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
     const int64_t ctas = (a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
     const int64_t seqs = a.whole ? 1 : (d->n_seq < pair ? d->n_seq : pair);
     a.tile_slots = slots_for(ctas, cap_prefix + seqs * cap_own, num_sms(), a.whole ? 512 : 256);
+    if (a.tile_slots > kMaxSlots / 2) a.tile_slots = kMaxSlots / 2;
     if (a.tile_slots < 1) a.tile_slots = 1;
-    a.prefix_slots = a.tile_slots > 1 ? a.tile_slots : 0;
+    // a row tile alone in its CTA gives two results a range (whole turns have
+    // such tiles whatever their lengths)
+    a.two = a.tile_slots > 1 && (a.whole || cdiv(M, attn_tile_rows(G)) % 2 == 1);
+    a.prefix_slots = a.tile_slots > 1 ? a.tile_slots * (a.two ? 2 : 1) : 0;
   } else {
     a.prefix_slots = slots_for(cdiv(M * G, kRowsTile) * kv, cap_prefix, num_sms() * 4, 128);
     a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, num_sms() * 4, 128);
@@ -542,10 +551,16 @@ lr_status launch_attn_rows(const AttnParams& p, int head_dim, cudaStream_t s) {
   return launch(attn_rows_kernel<128>, grid, dim3(kRowsWarps * 32), rows_smem<128>(), s, "attn_rows", p, rl);
 }
 
+template <int HD>
+static lr_status join(const AttnParams& p, cudaStream_t s) {
+  const int64_t rows = static_cast<int64_t>(p.M) * p.n_heads;
+  if (p.prefix_slots + p.own_slots >= 16)
+    return launch(attn_join_kernel<HD, 4>, dim3(cdiv(rows, 2)), dim3(256), 0, s, "attn_join", p);
+  return launch(attn_join_kernel<HD, 1>, dim3(cdiv(rows, 8)), dim3(256), 0, s, "attn_join", p);
+}
+
 lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s) {
-  const dim3 grid(cdiv(static_cast<int64_t>(p.M) * p.n_heads, 8));
-  if (head_dim == 64) return launch(attn_join_kernel<64>, grid, dim3(256), 0, s, "attn_join", p);
-  return launch(attn_join_kernel<128>, grid, dim3(256), 0, s, "attn_join", p);
+  return head_dim == 64 ? join<64>(p, s) : join<128>(p, s);
 }
 
 lr_status configure_attn() {
@@ -629,7 +644,7 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
   p.status = dev_status;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
   if (plan.tiles) {
-    st = launch_attn_tiles(p, c.head_dim, AttnPart{plan.whole, plan.tile_slots}, cs);
+    st = launch_attn_tiles(p, c.head_dim, AttnPart{plan.whole, plan.tile_slots, plan.two}, cs);
     if (plan.tile_slots == 1) return st;
   } else {
     st = launch_attn_rows(p, c.head_dim, cs);

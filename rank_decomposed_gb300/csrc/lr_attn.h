@@ -45,6 +45,7 @@ struct AttnParams {
 struct AttnPart {
   bool whole;
   int32_t slots;
+  bool two;  // each range has two slots of results
 };
 
 // Query rows of a tensor-core tile: their heads of one key head fill its 128
@@ -89,12 +90,13 @@ __device__ __forceinline__ SeqView seq_view(const AttnParams& p, int b, bool tel
   }
   return s;
 }
-__device__ __forceinline__ int prefix_view(const AttnParams& p, bool tell) {
-  if (p.cap_prefix == 0) return 0;
-  const int len = *p.prefix_len;
+__device__ __forceinline__ int prefix_rows(const AttnParams& p, int len, bool tell) {
   const int n = len < 0 ? 0 : (len > p.cap_prefix ? p.cap_prefix : len);
   if (tell && n != len && p.status != nullptr) atomicCAS(p.status, 0, LR_ERR_INDEX_RANGE);
   return n;
+}
+__device__ __forceinline__ int prefix_view(const AttnParams& p, bool tell) {
+  return p.cap_prefix > 0 ? prefix_rows(p, *p.prefix_len, tell) : 0;
 }
 #endif
 

@@ -85,6 +85,7 @@ struct TileParams {
   int32_t pairs;      // tile pairs per sequence (whole), or in all
   int32_t slots;
   int32_t direct;     // one key range: results go straight to out
+  int32_t two;        // two slots a key range (somewhere a row tile is alone in its CTA)
   int32_t stall;      // fault-injection hook: the producer issues nothing
 };
 
@@ -126,6 +127,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
       "%29,%30,%31};" ::LR_I8(r, 0),
       LR_I8(r, 8), LR_I8(r, 16), LR_I8(r, 24), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::LR_I8(r, 0),
+      LR_I8(r, 8), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- this CTA's rows and keys
   const int kvh = blockIdx.y, split = blockIdx.z, G = p.group;
   const bool tell = threadIdx.x == 0 && kvh == 0 && split == 0;
-  const int P = prefix_view(p, tell && blockIdx.x == 0);
+  const int prefix_len = p.cap_prefix > 0 ? *p.prefix_len : 0;  // on its way while the lists are made
   int q0 = 0, nq = p.M, own = 0, mrel;
   const int32_t* own_pages = nullptr;
   if (WHOLE) {
@@ -354,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = own - nq + m + 1;
     return v < 0 ? 0 : v;
   };
-  const int np = (P + kKeys - 1) / kKeys;
   // own key tiles of each ring's rows
   int own0, own1, see = 0;
   if (WHOLE) {
@@ -403,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     own0 = bars.tiles[0][127], own1 = bars.tiles[1][127];
   }
+  const int P = prefix_rows(p, prefix_len, tell && blockIdx.x == 0);
+  const int np = (P + kKeys - 1) / kKeys;
   // Steps: step s is key tile s of both rings' lists (prefix tiles, then own
   // ones), or, with one row tile, tiles 2 s and 2 s + 1 of its list.
   const int list0 = np + own0, list1 = dual ? list0 : np + own1;
@@ -440,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int live_rows = (tile ? rows1 : rows0) * G;
   const int my_n = (ringi & 1) ? n1 : n0;
   const int my_seq = WHOLE || trow / G >= a.mt ? -1 : bars.seq[tile][trow / G];
+  // One row tile: its two rings' results are joined here, or have a slot each.
+  const bool joins = dual && a.direct;
   float mref = -INFINITY, sum = 0.f;
   float2* hand_ml = reinterpret_cast<float2*>(ring + 128 * (HD + 4) * 4);  // behind ring 1's numerators
 
@@ -714,11 +724,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (vis > v.len) vis = v.len;
       }
       if (!WHOLE) {  // the rows of a tile do not all take part in its first product
-        uint32_t z[32];
+        uint32_t z[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = 0;
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) tmem_st32(o_at + c * 32, z);
+        for (int j = 0; j < 16; ++j) z[j] = 0;
+#pragma unroll 1
+        for (int c = 0; c < HD / 16; ++c) tmem_st16(o_at + c * 16, z);
         tmem_st_wait();
       }
       const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
@@ -731,22 +741,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // keys of the tile that the row sees
         const int c = dual ? 2 * (s_lo + i) + t : s_lo + i;
         int lim = P - c * kKeys;
+        bool mine = true;  // else the output lane is disabled: the row only keeps its state
         if (c >= np) {
           lim = vis - (c - np) * kKeys;
           if (!WHOLE) {
             const int list = dual ? 0 : t;
             at_row = own_row(t, c - np, at_row);
-            lim = bars.seq[list][at_row] == my_seq
-                      ? vis - (c - np - (at_row > 0 ? bars.tiles[list][at_row - 1] : 0)) * kKeys
-                      : 0;
+            lim = vis - (c - np - (at_row > 0 ? bars.tiles[list][at_row - 1] : 0)) * kKeys;
+            mine = bars.seq[list][at_row] == my_seq;
+            if (!mine) lim = kKeys;
           }
         }
-        if (busy && !__any_sync(0xffffffffu, lim > 0)) {  // none of the warp's rows: P = 0
-          uint32_t z[32];
+        if (busy && !__any_sync(0xffffffffu, mine && lim > 0)) {  // none of the warp's rows: P = 0
+          uint32_t z[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = 0;
-          tmem_st32(s_at, z);
-          tmem_st32(s_at + 32, z);
+          for (int j = 0; j < 16; ++j) z[j] = 0;
+#pragma unroll 1
+          for (int k = 0; k < kKeys / 32; ++k) tmem_st16(s_at + k * 16, z);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -769,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + e + 4]));
           const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
-          const float now = fmaxf(mref, top * p.scale_log2);
+          const float now = mine ? fmaxf(mref, top * p.scale_log2) : mref;
           const bool move = now > mref + kSlack;  // -inf + 8 is -inf: the first key moves it
           if (__any_sync(0xffffffffu, move)) {
             const float next = move ? now : mref;
@@ -777,14 +788,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum *= f;
             mref = next;
             if (i > 0) {
-#pragma unroll
-              for (int c = 0; c < HD / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_at + c * 32, o);
+#pragma unroll 1
+              for (int c = 0; c < HD / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(o_at + c * 16, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(o_at + c * 32, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st16(o_at + c * 16, o);
               }
             }
           }
@@ -816,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float pa, pb;
           unpack2(add2(part[0], part[1]), pa, pb);
-          sum += pa + pb;
+          if (mine) sum += pa + pb;
           tmem_st_wait();
         } else if (lane == 0) {
           mbar_arrive(&bars.p_ready[t][0]);
@@ -828,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && my_n > 0) {
         ok = mbar_wait(&bars.o_done[t], 0, &abort_sh);
         // the ring is the other one's too: its products end before it is written below
-        if (ok && dual && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
+        if (ok && joins && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
         tc_fence_after();
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -836,31 +847,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         abort_sh = 1;
         report_status(p.status, LR_ERR_TIMEOUT);
       }
-      if (ok && dual && t == 1 && n1 > 0 && busy) {  // ring 1 hands its part to ring 0
+      if (ok && joins && t == 1 && n1 > 0 && busy) {  // ring 1 hands its part to ring 0
         hand_ml[trow] = make_float2(mref, sum);
         float* dst = reinterpret_cast<float*>(ring) + trow * (HD + 4);
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(o_at + c * 32, o);
+#pragma unroll 1
+        for (int c = 0; c < HD / 16; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o_at + c * 16, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4*>(dst + c * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<uint4*>(dst + c * 16 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
     }
     tc_fence_before();
-    named_bar_sync(1, 256);  // the softmax warps
+    if (joins) named_bar_sync(1, 256);  // the softmax warps
     tc_fence_after();
-    if (!(dual && ringi == 1) && *static_cast<volatile int*>(&abort_sh) == 0) {
+    if (!(joins && ringi == 1) && *static_cast<volatile int*>(&abort_sh) == 0) {
       // ------------------------------------------------- rows to memory
       const int t = ringi;
       const bool busy = (warp & 3) * 32 < live_rows;
       const bool live = trow < live_rows;
       if (busy) {
         const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const bool both = dual && n1 > 0;
+        const bool both = joins && n1 > 0;
         float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
         if (both) {
           const float2 o = hand_ml[trow];
@@ -873,7 +884,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_n == 0) f0 = 0.f;  // nothing was summed: TMEM holds no result
         const int64_t qrow = q0 + mrel + tile * a.mt + trow / G;
         const int head = kvh * G + trow % G;
-        const int64_t at = (static_cast<int64_t>(split) * p.M + qrow) * p.n_heads + head;
+        const int slot = a.two ? 2 * split + (dual ? t : 0) : split;
+        const int64_t slot_rows = static_cast<int64_t>(p.M) * p.n_heads;
+        const int64_t at = slot * slot_rows + qrow * p.n_heads + head;
         if (a.direct) {
           // a packed row of no sequence comes out zero, and so does one that saw no key
           const float inv = l == 0.f || (!WHOLE && my_seq < 0) ? 0.f : 1.f / l;
@@ -881,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f1 *= inv;
         } else if (live) {
           p.pml[at] = make_float2(m, l);
+          if (a.two && !dual) p.pml[at + slot_rows] = make_float2(-INFINITY, 0.f);
         }
         const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
         // A thread holds a row; memory wants rows side by side (16 bytes a lane
@@ -891,9 +905,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4* stage = reinterpret_cast<float4*>(q_sm + t * S::kTileBytes + (warp & 3) * (S::kTileBytes / 4));
         const int64_t row_off = a.direct ? qrow * p.ldo + static_cast<int64_t>(head) * HD : at * HD;
         const int left = live_rows - (warp & 3) * 32;  // rows of this warp
+        // (Code that runs once is short: it costs what its fetching costs.)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kHalf / 32; ++c) {
             uint32_t r[32];
             tmem_ld32(o_at + half * kHalf + c * 32, r);
@@ -913,22 +928,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          // eight stores at a time, so that their reads overlap
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32 / kPer; i0 += 8) {
+            float4 x[8];
+            int64_t off[8];
 #pragma unroll
-          for (int i = 0; i < 32 / kPer; ++i) {
-            const int r = i * kPer + lane / kVec, c = lane % kVec;
-            const float4 x = stage[r * kVec + (c ^ (r & 7))];
-            const int64_t off = __shfl_sync(0xffffffffu, row_off, r) + half * kHalf + c * 4;
-            if (r < left) {
-              if (!a.direct) {
-                *reinterpret_cast<float4*>(p.po + off) = x;
-              } else if (p.out_f32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + off) = x;
-              } else {
+            for (int i = 0; i < 8; ++i) {
+              const int r = (i0 + i) * kPer + lane / kVec, c = lane % kVec;
+              x[i] = stage[r * kVec + (c ^ (r & 7))];
+              off[i] = __shfl_sync(0xffffffffu, row_off, r) + half * kHalf + c * 4;
+            }
+            const int live_here = left - i0 * kPer - lane / kVec;
+            if (a.direct && !p.out_f32) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
                 uint2 w;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off) = w;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x[i].y), "f"(x[i].x));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x[i].w), "f"(x[i].z));
+                if (i * kPer < live_here) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + off[i]) = w;
               }
+            } else {
+              float* dst = a.direct ? static_cast<float*>(p.out) : p.po;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (i * kPer < live_here) *reinterpret_cast<float4*>(dst + off[i]) = x[i];
             }
           }
           __syncwarp();
@@ -979,6 +1003,7 @@ lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& p
   a.pairs = ((part.whole ? p.max_q : p.M) + per_pair - 1) / per_pair;
   a.slots = part.slots;
   a.direct = part.slots == 1;
+  a.two = part.two;
   a.stall = test_stall_producer();
   const dim3 grid(part.whole ? a.pairs * p.n_seq : a.pairs, p.n_kv, part.slots);
   if (head_dim == 64) return part.whole ? launch_tiles<64, true>(a, grid, s) : launch_tiles<64, false>(a, grid, s);
