@@ -483,6 +483,31 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
                               const lr_attn_desc* d, void* workspace, size_t ws_bytes, int32_t* dev_status,
                               lr_stream s);
 
+/* lr_block_forward_cached: the block of lr_block_forward with attention over a
+ * context: n1 = RMSNorm(h); q, k, v = LR(n1); the new tokens' keys and values
+ * are appended to the layer's cache (q and k normed and rotated as ctx->heads
+ * says); h += LR_o(attention of q over the context); the MLP follows.
+ *   h: device fp32 [M][d_model], row m the token at position pos[m] whose cache
+ *   row is rows[m]; ctx->attn describes the same M rows (q_start, or one row a
+ *   sequence) and its lengths count the new tokens.  The cache is this layer's;
+ *   n_heads, n_kv_heads and head_dim of ctx and block must agree, and head_dim
+ *   and block_rows are those that lr_prefix_attention takes.
+ *   Rows m >= *n_active (NULL: none) append nothing; their h is unspecified.
+ *   scratch: device, at least lr_block_cached_scratch_bytes(M, b, ctx) bytes,
+ *   256-byte aligned.  Checks, reports and capture as for the parts.  M = 0 is
+ *   a no-op. */
+typedef struct {
+  lr_attn_desc attn;
+  lr_head_map heads;
+  const int32_t* pos;
+  const int32_t* rows;
+  const int32_t* n_active;
+} lr_context;
+
+size_t lr_block_cached_scratch_bytes(int64_t M, const lr_block_desc* b, const lr_context* ctx);
+lr_status lr_block_forward_cached(float* h, int64_t M, const lr_block_desc* b, const lr_context* ctx,
+                                  void* scratch, size_t scratch_bytes, int32_t* dev_status, lr_stream s);
+
 /* ---------------------------------------------------------------------------
  * A decode step of a layer stack over fixed buffers (English page section 2.C:
  * addresses and launch parameters stay fixed while the logical batch changes):

@@ -383,6 +383,26 @@ def prefix_attention(q, k_pool, v_pool, n_heads: int, n_kv: int, head_dim: int, 
     return out, mag
 
 
+def block_forward_cached(h, factors, n_heads: int, n_kv: int, head_dim: int, k_pool, v_pool, rows, cos, sin, gains,
+                         style: str, batch, eps: float = LLAMA_RMS_EPS, head_eps: float = 1e-6):
+    """block_forward with attention over a paged context.
+
+    k_pool, v_pool (fp64 arrays) get the new tokens' rows; batch(q) is the attention of the prepared queries
+    over the pools.  gains: (q gain, k gain) or None for no norm.
+    """
+    h = np.asarray(h, dtype=np.float64)
+    n1 = rmsnorm(h, eps)
+    q, k, v = (lowrank_linear(n1, *factors[x])[1] for x in ("q", "k", "v"))
+    gq, gk = gains if gains is not None else (None, None)
+    k_pool[rows] = map_heads(k, head_dim, gk, head_eps, cos, sin, style)
+    v_pool[rows] = v
+    attn = batch(map_heads(q, head_dim, gq, head_eps, cos, sin, style))
+    h1 = h + lowrank_linear(attn, *factors["o"])[1]
+    n2 = rmsnorm(h1, eps)
+    a = silu(lowrank_linear(n2, *factors["gate"])[1]) * lowrank_linear(n2, *factors["up"])[1]
+    return h1 + lowrank_linear(a, *factors["down"])[1]
+
+
 # ------------------------------------------------------ rank-space sharding
 def shard_columns(n: int, G: int):
     """Split n columns (a multiple of 64) over G processes in whole 64-column blocks.

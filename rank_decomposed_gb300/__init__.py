@@ -83,6 +83,11 @@ class AttnDesc(ctypes.Structure):
                 ("blocks_per_seq", ctypes.c_int32), ("lengths", ctypes.c_void_p)]
 
 
+class ContextDesc(ctypes.Structure):
+    _fields_ = [("attn", AttnDesc), ("heads", HeadMapDesc), ("pos", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("n_active", ctypes.c_void_p)]
+
+
 ROT_HALF = 0
 ROT_PAIR = 1
 
@@ -122,6 +127,8 @@ def _load():
                                vp, i64, vp, vp]),
         "lr_prefix_attention_workspace_bytes": (sz, [i64, P(AttnDesc)]),
         "lr_prefix_attention": (i32, [vp, i64, vp, i64, i32, i64, P(AttnDesc), vp, sz, vp, vp]),
+        "lr_block_cached_scratch_bytes": (sz, [i64, P(BlockDesc), P(ContextDesc)]),
+        "lr_block_forward_cached": (i32, [vp, i64, P(BlockDesc), P(ContextDesc), vp, sz, vp, vp]),
         "lr_stack_forward": (i32, [P(StackDesc), vp]),
         "lr_graph_capture": (i32, [P(StackDesc), P(vp)]),
         "lr_graph_replay": (i32, [vp, vp]),
@@ -651,6 +658,44 @@ def prefix_attention(q, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len,
                                  0 if workspace is None else workspace.nbytes, _ptr(status), _stream_of(stream))
     if st != LR_OK:
         _check("lr_prefix_attention", st)
+
+
+@dataclass
+class Context:
+    """A layer's context for M new rows: its cache and head map, the rows' positions and cache rows, and the
+    batch as prefix_attention takes it (lengths count the new tokens)."""
+    cache: PagedKV
+    heads: HeadMap
+    pos: object
+    rows: object
+    prefix_blocks: object
+    prefix_len: object
+    block_table: object
+    lengths: object
+    q_start: object = None
+    max_q: int = 1
+    scale: object = None
+    n_active: object = None
+
+    def c(self, M: int, n_heads: int) -> ContextDesc:
+        attn = _attn_desc(n_heads, self.cache, self.prefix_blocks, self.prefix_len, self.block_table, self.lengths,
+                          self.q_start, self.max_q, self.scale)
+        return ContextDesc(attn, self.heads.c(), _per_row(self.pos, "pos", M), _per_row(self.rows, "rows", M),
+                           _i32(self.n_active, "n_active"))
+
+
+def block_cached_scratch_bytes(M: int, b: Block, ctx: Context) -> int:
+    return int(lib.lr_block_cached_scratch_bytes(M, ctypes.byref(b.c()), ctypes.byref(ctx.c(M, b.n_heads))))
+
+
+def block_forward_cached(h, b: Block, ctx: Context, scratch, status, stream=None):
+    """One decomposed block with attention over its cached context, applied in place to h [M][d_model] (fp32)."""
+    if h.dtype != _th().float32 or not h.is_contiguous():
+        raise TypeError("h must be a contiguous float32 tensor")
+    bc, cc = b.c(), ctx.c(h.shape[0], b.n_heads)
+    st = lib.lr_block_forward_cached(h.data_ptr(), h.shape[0], ctypes.byref(bc), ctypes.byref(cc), scratch.data_ptr(),
+                                     scratch.nbytes, _ptr(status), _stream_of(stream))
+    _check("lr_block_forward_cached", st)
 
 
 # ---------------------------------------------------------------- stack

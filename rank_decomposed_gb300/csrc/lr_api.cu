@@ -351,10 +351,19 @@ lr_status check_block(const lr_block_desc* b) {
   return LR_OK;
 }
 
+// What a block with a context has beside the others' buffers.
+struct BlockContext {
+  const lr_context* ctx;
+  void* out;       // bf16 [M][n_heads * head_dim]
+  void* ws;
+  size_t ws_bytes;
+};
+
 // One launch of a block, in stream order: a GEMM group (ops sharing M and
-// their input), an RMSNorm or a SiLU-GLU.
+// their input), an RMSNorm or a SiLU-GLU; or the append to the cache and the
+// attention over it.
 struct Step {
-  enum Kind { GEMM, RMSNORM, SILU } kind;
+  enum Kind { GEMM, RMSNORM, SILU, CONTEXT } kind;
   GemmOp ops[kMaxGroup];
   int n = 0;
   const void* src0 = nullptr;
@@ -363,6 +372,8 @@ struct Step {
   int d = 0;
   float eps = 0.f;
   int32_t* cnt = nullptr;  // GEMM: band counters for a fused prefill-size linear
+  const BlockContext* context = nullptr;
+  void* qkv[3] = {nullptr, nullptr, nullptr};
 };
 
 Step gemm_step(std::initializer_list<GemmOp> ops) {
@@ -376,7 +387,8 @@ Step gemm_step(std::initializer_list<GemmOp> ops) {
 // then up group); h += LR_o(attn(v)); n2 = RMSNorm(h);
 // h += LR_down(silu(LR_gate(n2)) * LR_up(n2)) (ReLU variant: the ReLU is
 // applied in the up projection's epilogue).
-void block_steps_of(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, std::vector<Step>& out) {
+void block_steps_of(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, const BlockContext* context,
+                    std::vector<Step>& out) {
   const BlockLayout L = block_layout(M, b);
   const int d = b->d_model, dff = b->d_ff;
   const lr_factor* f = b->f;
@@ -401,12 +413,21 @@ void block_steps_of(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, st
     dn.n = up.n = 3;
     out.push_back(dn);
     out.push_back(up);
+    if (context != nullptr) {
+      Step at;
+      at.kind = Step::CONTEXT;
+      at.context = context;
+      for (int i = 0; i < 3; ++i) at.qkv[i] = outs[i];
+      out.push_back(at);
+    }
   }
   {
     const int dq = b->n_heads * b->head_dim, dkv = b->n_kv_heads * b->head_dim;
     GemmOp od = make_op(f[LR_O].At, f[LR_O].r, dq, ws + L.v, dkv, dkv, EPI_STORE_BF16, t[LR_O],
                         f[LR_O].r);
-    if (b->n_heads != b->n_kv_heads) {
+    if (context != nullptr) {
+      od = make_op(f[LR_O].At, f[LR_O].r, dq, context->out, dq, dq, EPI_STORE_BF16, t[LR_O], f[LR_O].r);
+    } else if (b->n_heads != b->n_kv_heads) {
       od.gqa_head_dim = b->head_dim;
       od.gqa_group = b->n_heads / b->n_kv_heads;
     }
@@ -445,9 +466,10 @@ void block_steps_of(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, st
   out.push_back(gemm_step({make_op(fd.Bt, d, fd.r, t[LR_DOWN], fd.r, fd.r, EPI_ADD_F32, h, d)}));
 }
 
-void block_steps(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, std::vector<Step>& out) {
+void block_steps(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws, std::vector<Step>& out,
+                 const BlockContext* context = nullptr) {
   const size_t first = out.size();
-  block_steps_of(h, M, b, ws, out);
+  block_steps_of(h, M, b, ws, context, out);
   int32_t* cnt = reinterpret_cast<int32_t*>(ws + block_layout(M, b).cnt);
   for (size_t i = first; i < out.size(); ++i) out[i].cnt = cnt;
 }
@@ -484,6 +506,17 @@ lr_status enqueue_steps(const std::vector<Step>& steps, int64_t M, int32_t* stat
       ++i;
     } else if (st.kind == Step::GEMM) {
       r = run_ops(M, st.ops, st.n, status, s);
+    } else if (st.kind == Step::CONTEXT) {
+      const lr_context& c = *st.context->ctx;
+      const lr_attn_desc& at = c.attn;
+      const int64_t wq = static_cast<int64_t>(at.n_heads) * at.cache.head_dim;
+      const int64_t wk = static_cast<int64_t>(at.cache.n_kv_heads) * at.cache.head_dim;
+      lr_stream ls = reinterpret_cast<lr_stream>(s);
+      r = lr_kv_append(st.qkv[1], wk, st.qkv[2], wk, st.qkv[0], wq, at.n_heads, LR_BF16, M, c.pos, c.rows, c.n_active,
+                       &c.heads, &at.cache, st.qkv[0], wq, status, ls);
+      if (r == LR_OK)
+        r = lr_prefix_attention(st.qkv[0], wq, st.context->out, wq, LR_BF16, M, &at, st.context->ws,
+                                st.context->ws_bytes, status, ls);
     } else if (st.kind == Step::RMSNORM) {
       r = launch_rmsnorm(static_cast<const float*>(st.src0), st.dst, M, st.d, st.eps, s);
     } else {
@@ -499,6 +532,18 @@ lr_status enqueue_block(float* h, int64_t M, const lr_block_desc* b, uint8_t* ws
   std::vector<Step> steps;
   block_steps(h, M, b, ws, steps);
   return enqueue_steps(steps, M, status, s);
+}
+
+// The context's arguments for M rows, before anything is enqueued.  `buf`
+// stands for the block's own q, k and v, which are aligned as it is.
+lr_status check_context(int64_t M, const lr_context* c, const void* buf, const void* ws, size_t ws_bytes) {
+  const lr_attn_desc& at = c->attn;
+  const int64_t wq = static_cast<int64_t>(at.n_heads) * at.cache.head_dim;
+  const int64_t wk = static_cast<int64_t>(at.cache.n_kv_heads) * at.cache.head_dim;
+  lr_status st = check_append(buf, wk, buf, wk, buf, wq, at.n_heads, LR_BF16, M, c->pos, c->rows, &c->heads,
+                              &at.cache, buf, wq);
+  if (st != LR_OK) return st;
+  return check_attention(buf, wq, buf, wq, LR_BF16, M, &at, ws, ws_bytes);
 }
 
 int64_t block_launches(int64_t M, const lr_block_desc* b) {
@@ -672,6 +717,42 @@ lr_status lr_block_forward(float* h, int64_t M, const lr_block_desc* b, void* sc
   if (scratch_bytes < lr_block_scratch_bytes(M, b)) return invalid("block: scratch too small");
   return enqueue_block(h, M, b, static_cast<uint8_t*>(scratch), dev_status,
                        reinterpret_cast<cudaStream_t>(s));
+}
+
+size_t lr_block_cached_scratch_bytes(int64_t M, const lr_block_desc* b, const lr_context* ctx) {
+  if (b == nullptr || ctx == nullptr || M < 0) return 0;
+  const size_t out = align_up(static_cast<size_t>(M) * b->n_heads * b->head_dim * 2);
+  return block_layout(M, b).total + out + lr_prefix_attention_workspace_bytes(M, &ctx->attn);
+}
+
+lr_status lr_block_forward_cached(float* h, int64_t M, const lr_block_desc* b, const lr_context* ctx,
+                                  void* scratch, size_t scratch_bytes, int32_t* dev_status, lr_stream s) {
+  lr_status st = check_block(b);
+  if (st != LR_OK) return st;
+  if (M < 0 || M > (int64_t(1) << 31) - 1) return invalid("block: bad M");
+  if (ctx == nullptr) return invalid("block: null context");
+  const lr_attn_desc& at = ctx->attn;
+  if (at.n_heads != b->n_heads || at.cache.n_kv_heads != b->n_kv_heads || at.cache.head_dim != b->head_dim ||
+      ctx->heads.head_dim != b->head_dim)
+    return invalid("block: the context's heads are not the block's");
+  if (M == 0) return LR_OK;
+  if (h == nullptr || scratch == nullptr) return invalid("block: null pointer");
+  if (!aligned16(h) || reinterpret_cast<uintptr_t>(scratch) % kAlign)
+    return invalid("block: h must be 16-byte and scratch 256-byte aligned");
+  if (scratch_bytes < lr_block_cached_scratch_bytes(M, b, ctx)) return invalid("block: scratch too small");
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  BlockContext bc;
+  bc.ctx = ctx;
+  bc.out = ws + block_layout(M, b).total;
+  const size_t out_bytes = align_up(static_cast<size_t>(M) * b->n_heads * b->head_dim * 2);
+  bc.ws = static_cast<uint8_t*>(bc.out) + out_bytes;
+  bc.ws_bytes = lr_prefix_attention_workspace_bytes(M, &at);
+  // Both parts' arguments, before anything is enqueued.
+  st = check_context(M, ctx, bc.out, bc.ws, bc.ws_bytes);
+  if (st != LR_OK) return st;
+  std::vector<Step> steps;
+  block_steps(h, M, b, ws, steps, &bc);
+  return enqueue_steps(steps, M, dev_status, reinterpret_cast<cudaStream_t>(s));
 }
 
 lr_status remap_compact(const void* pool, int64_t pool_rows, int64_t row_bytes,

@@ -571,22 +571,8 @@ lr_status configure_attn() {
   return LR_OK;
 }
 
-}  // namespace lr
-
-using namespace lr;
-
-extern "C" {
-
-size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d) {
-  if (d == nullptr || M <= 0 || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
-      d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
-    return 0;
-  return attn_plan(M, d).bytes;
-}
-
-lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
-                              const lr_attn_desc* d, void* workspace, size_t ws_bytes, int32_t* dev_status,
-                              lr_stream s) {
+lr_status check_attention(const void* q, int64_t ldq, const void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
+                          const lr_attn_desc* d, const void* workspace, size_t ws_bytes) {
   const char* who = "prefix_attention";
   lr_status st = check_desc(who, M, d);
   if (st != LR_OK) return st;
@@ -603,6 +589,29 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
     return bad(LR_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
   if (ws_bytes < plan.bytes)
     return bad(LR_ERR_INVALID_ARG, "%s: workspace %zu < %zu bytes", who, ws_bytes, plan.bytes);
+  return LR_OK;
+}
+
+}  // namespace lr
+
+using namespace lr;
+
+extern "C" {
+
+size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d) {
+  if (d == nullptr || M <= 0 || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
+      d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
+    return 0;
+  return attn_plan(M, d).bytes;
+}
+
+lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
+                              const lr_attn_desc* d, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                              lr_stream s) {
+  lr_status st = check_attention(q, ldq, out, ldo, out_dtype, M, d, workspace, ws_bytes);
+  if (st != LR_OK || M == 0) return st;
+  const lr_kv_cache& c = d->cache;
+  const AttnPlan plan = attn_plan(M, d);
   st = ensure_configured();
   if (st != LR_OK) return st;
 

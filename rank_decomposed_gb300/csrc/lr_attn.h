@@ -61,7 +61,13 @@ lr_status encode_map_heads(CUtensorMap* map, const void* base, uint64_t head_dim
                            uint64_t ld, uint32_t box_heads, uint32_t box_rows);
 lr_status launch_attn_join(const AttnParams& p, int head_dim, cudaStream_t s);
 lr_status configure_attn();
+// The host-side argument checks of the entry points.
 lr_status check_kv_cache(const char* who, const lr_kv_cache* c);
+lr_status check_append(const void* k, int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq,
+                       int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos, const int32_t* rows,
+                       const lr_head_map* hm, const lr_kv_cache* cache, const void* q_out, int64_t ldqo);
+lr_status check_attention(const void* q, int64_t ldq, const void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,
+                          const lr_attn_desc* d, const void* workspace, size_t ws_bytes);
 
 #ifdef __CUDACC__
 // A sequence's query rows and own length, clamped to what the capacities allow.

@@ -371,6 +371,30 @@ lr_status check_kv_cache(const char* who, const lr_kv_cache* c) {
   return check_rows(who, "V pool", c->v, c->ld, width);
 }
 
+lr_status check_append(const void* k, int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq,
+                       int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos, const int32_t* rows,
+                       const lr_head_map* hm, const lr_kv_cache* cache, const void* q_out, int64_t ldqo) {
+  const char* who = "kv_append";
+  lr_status st = check_kv_cache(who, cache);
+  if (st != LR_OK) return st;
+  st = check_common(who, in_dtype, M, pos, hm, n_heads, cache->n_kv_heads);
+  if (st != LR_OK) return st;
+  if (hm->head_dim != cache->head_dim) return bad(LR_ERR_INVALID_ARG, "%s: the head map's head_dim is not the cache's", who);
+  if (M == 0) return LR_OK;
+  if (rows == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null rows", who);
+  const int64_t wk = static_cast<int64_t>(cache->n_kv_heads) * hm->head_dim;
+  if ((st = check_rows(who, "k", k, ldk, wk)) != LR_OK) return st;
+  if ((st = check_rows(who, "v", v, ldv, wk)) != LR_OK) return st;
+  if (n_heads > 0) {
+    const int64_t wq = static_cast<int64_t>(n_heads) * hm->head_dim;
+    if ((st = check_rows(who, "q", q, ldq, wq)) != LR_OK) return st;
+    if ((st = check_rows(who, "q_out", q_out, ldqo, wq)) != LR_OK) return st;
+    if (q == q_out && (in_dtype != LR_BF16 || ldq != ldqo))
+      return bad(LR_ERR_INVALID_ARG, "%s: in place needs bf16 and one leading dimension", who);
+  }
+  return LR_OK;
+}
+
 }  // namespace lr
 
 using namespace lr;
@@ -431,24 +455,8 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
                        int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
                        const int32_t* rows, const int32_t* n_active, const lr_head_map* hm,
                        const lr_kv_cache* cache, void* q_out, int64_t ldqo, int32_t* dev_status, lr_stream s) {
-  const char* who = "kv_append";
-  lr_status st = check_kv_cache(who, cache);
-  if (st != LR_OK) return st;
-  st = check_common(who, in_dtype, M, pos, hm, n_heads, cache->n_kv_heads);
-  if (st != LR_OK) return st;
-  if (hm->head_dim != cache->head_dim) return bad(LR_ERR_INVALID_ARG, "%s: the head map's head_dim is not the cache's", who);
-  if (M == 0) return LR_OK;
-  if (rows == nullptr) return bad(LR_ERR_INVALID_ARG, "%s: null rows", who);
-  const int64_t wk = static_cast<int64_t>(cache->n_kv_heads) * hm->head_dim;
-  if ((st = check_rows(who, "k", k, ldk, wk)) != LR_OK) return st;
-  if ((st = check_rows(who, "v", v, ldv, wk)) != LR_OK) return st;
-  if (n_heads > 0) {
-    const int64_t wq = static_cast<int64_t>(n_heads) * hm->head_dim;
-    if ((st = check_rows(who, "q", q, ldq, wq)) != LR_OK) return st;
-    if ((st = check_rows(who, "q_out", q_out, ldqo, wq)) != LR_OK) return st;
-    if (q == q_out && (in_dtype != LR_BF16 || ldq != ldqo))
-      return bad(LR_ERR_INVALID_ARG, "%s: in place needs bf16 and one leading dimension", who);
-  }
+  lr_status st = check_append(k, ldk, v, ldv, q, ldq, n_heads, in_dtype, M, pos, rows, hm, cache, q_out, ldqo);
+  if (st != LR_OK || M == 0) return st;
   HeadParams p;
   memset(&p, 0, sizeof(p));
   p.src[0] = q, p.src[1] = k, p.src[2] = v;

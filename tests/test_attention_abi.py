@@ -125,6 +125,41 @@ def test_workspace_covers_capacities_and_is_zero_for_nothing():
     assert f(9, cap_prefix_blocks=100) >= f(9) > 0
 
 
+def _block(**kw):
+    b = lr.BlockDesc()
+    b.d_model, b.d_ff, b.n_heads, b.n_kv_heads, b.head_dim, b.eps = 512, 1024, 8, 2, 128, 1e-6
+    io = [(512, 1024), (512, 256), (512, 256), (1024, 512), (512, 1024), (512, 1024), (1024, 512)]
+    for i, (a, o) in enumerate(io):
+        b.f[i] = lr.Factor(0x10000 * (i + 1), 0x10000 * (i + 20), a, o, 64)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return b
+
+
+def _context(attn=None, heads=None, pos=0x100, rows=0x200):
+    return lr.ContextDesc(attn or _desc(), heads or _map(), pos, rows, None)
+
+
+def test_block_forward_cached_refusals_launch_nothing():
+    def call(b=None, c=None, M=9, h=0x1000, ws=0x100000, ws_bytes=BIG):
+        b = b or _block()
+        c = _context() if c is None else c
+        return lr.lib.lr_block_forward_cached(h, M, ctypes.byref(b), ctypes.byref(c), ws, ws_bytes, None, None)
+
+    bad = lr.LR_ERR_INVALID_ARG
+    assert call(M=0) == lr.LR_OK
+    need = lr.lib.lr_block_cached_scratch_bytes(9, ctypes.byref(_block()), ctypes.byref(_context()))
+    assert need > lr.lib.lr_block_scratch_bytes(9, ctypes.byref(_block()))
+    for kw in (dict(h=None), dict(h=0x1004), dict(ws=None), dict(ws=0x100010), dict(ws_bytes=need - 1), dict(M=-1),
+               dict(c=_context(pos=None)), dict(c=_context(rows=None)), dict(c=_context(heads=_map(hd=64, rot=64))),
+               dict(c=_context(attn=_desc(n_heads=4))), dict(c=_context(attn=_desc(lengths=None))),
+               dict(c=_context(attn=_desc(scale=-1.0))), dict(c=_context(attn=_desc(cache=_cache(n_kv_heads=1)))),
+               dict(b=_block(n_kv_heads=3))):
+        assert call(**kw) == bad, kw
+    assert call(c=_context(attn=_desc(cache=_cache(block_rows=24)))) == lr.LR_ERR_UNSUPPORTED
+    assert lr.lib.lr_block_forward_cached(0x1000, 4, ctypes.byref(_block()), None, 0x100000, BIG, None, None) == bad
+
+
 def test_status_string_of_index_range():
     assert "range" in lr.status_string(lr.LR_ERR_INDEX_RANGE)
 
