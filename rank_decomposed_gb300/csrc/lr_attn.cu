@@ -471,6 +471,8 @@ struct AttnPlan {
   size_t ml_off, bytes;
 };
 
+constexpr int kMinSteps = 4;
+
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   AttnPlan a;
   memset(&a, 0, sizeof(a));
@@ -482,10 +484,12 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   a.tiles = M * G > kRowsTile;
   a.whole = a.tiles && d->n_seq > 0 && mq * G > 64;
   if (a.tiles) {
-    // a packed tile pair has the own tokens of every sequence in it
+    // Steps of a row tile pair when all is full; packed tiles have the own tokens
+    // of every sequence in them.
     const int64_t ctas = (a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
-    const int64_t seqs = a.whole ? 1 : (d->n_seq < pair ? d->n_seq : pair);
-    a.tile_slots = slots_for(ctas, cap_prefix + seqs * cap_own, num_sms(), a.whole ? 512 : 256);
+    const int64_t seqs = a.whole ? 1 : (d->n_seq < pair / 2 ? d->n_seq : pair / 2);
+    const int64_t steps = cdiv(cap_prefix, 128) + seqs * cdiv(cap_own, 128);
+    a.tile_slots = slots_for(ctas, steps, num_sms(), kMinSteps);
     if (a.tile_slots > kMaxSlots / 2) a.tile_slots = kMaxSlots / 2;
     if (a.tile_slots < 1) a.tile_slots = 1;
     // a row tile alone in its CTA gives two results a range (whole turns have
