@@ -454,7 +454,8 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   more than max_q rows (such a sequence's rows past max_q are unspecified).
  *   A listed page outside [0, pool_blocks) reads as zeros and reports
  *   LR_ERR_REMAP_RANGE.
- *   head_dim 64 or 128; block_rows a multiple of 16; n_heads a multiple of
+ *   head_dim 64 or 128; block_rows a multiple of 16; blocks_per_seq * block_rows
+ *   below 2^24; n_heads a multiple of
  *   n_kv_heads with at most 64 query heads a kv head (LR_ERR_UNSUPPORTED
  *   otherwise, LR_ERR_INVALID_ARG for a remainder); scale > 0 and finite.
  *   workspace: device, 256-byte aligned, at least

@@ -482,13 +482,14 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   const int64_t cap_own = static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows;
   const int64_t pair = 2 * attn_tile_rows(G);
   a.tiles = M * G > kRowsTile;
-  a.whole = a.tiles && d->n_seq > 0 && mq * G > 64;
+  // (the packed lists hold a sequence's number in 16 bits)
+  a.whole = a.tiles && d->n_seq > 0 && (mq * G > 64 || (d->q_start != nullptr && d->n_seq > 32767));
   if (a.tiles) {
     // Steps of a row tile pair when all is full; packed tiles have the own tokens
     // of every sequence in them.
     const int64_t ctas = (a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
     const int64_t seqs = a.whole ? 1 : (d->n_seq < pair / 2 ? d->n_seq : pair / 2);
-    const int64_t steps = cdiv(cap_prefix, 128) + seqs * cdiv(cap_own, 128);
+    const int64_t steps = cdiv(cap_prefix, 128) + cdiv(seqs * cap_own, 128);
     a.tile_slots = slots_for(ctas, steps, num_sms(), kMinSteps);
     if (a.tile_slots > kMaxSlots / 2) a.tile_slots = kMaxSlots / 2;
     if (a.tile_slots < 1) a.tile_slots = 1;
@@ -532,6 +533,9 @@ lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
     return bad(LR_ERR_INVALID_ARG, "%s: null lengths or block table", who);
   if (d->q_start == nullptr ? (d->max_q != 1 || M < d->n_seq) : (d->max_q < 1))
     return bad(LR_ERR_INVALID_ARG, "%s: max_q must be at least 1, and 1 with a row for each sequence without q_start", who);
+  // the own tokens of 128 sequences are counted in 32 bits
+  if (static_cast<int64_t>(d->blocks_per_seq) * c.block_rows > 0x7FFFFFFF / 128)
+    return bad(LR_ERR_UNSUPPORTED, "%s: an own context of more than 16 million rows", who);
   if (M * d->n_heads > 0x7FFFFFFF ||
       cdiv(most_q(M, d) * (d->n_heads / c.n_kv_heads), kRowsTile) * static_cast<int64_t>(d->n_seq) > 0x7FFFFFFF)
     return bad(LR_ERR_UNSUPPORTED, "%s: too many rows for one launch", who);

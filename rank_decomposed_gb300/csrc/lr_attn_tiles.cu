@@ -60,7 +60,7 @@ namespace {
 
 constexpr int kThreads = 512;        // 8 softmax warps, 4 producers, an MMA issuer, a relay, the pages, one idle
 constexpr int kMmaWarp = 12, kRelayWarp = 13, kPageWarp = 14;
-constexpr int kLooked = 8;           // tiles whose pages are known ahead
+constexpr int kLooked = 6;           // tiles whose pages are known, from their K load to their V product
 // Registers: the launch gives 128 a thread; the softmax warps hold a row of 128
 // scores and take what the others leave (256 * 208 + 128 * 40 + 128 * 56 = 512 * 128).
 constexpr int kRegsSoftmax = 208, kRegsLoad = 40, kRegsIssue = 56;
@@ -191,23 +191,21 @@ __device__ __forceinline__ void mma_pv_half(uint32_t d, uint32_t p_at, uint32_t 
       : "memory");
 }
 
-// The same with the output lanes of the set bits left alone (row r: bit r mod 32
-// of word r / 32), always added to O.
+// The same, always added to O, with the output lanes of others[k]'s set bits left
+// alone in the product of the k-th 16 keys.
 __device__ __forceinline__ void mma_pv_half_some(uint32_t d, uint32_t p_at, uint32_t v_lo, uint32_t idesc,
-                                                 const uint32_t (&off)[4]) {
-  asm volatile(
-      "{\n\t.reg .pred t;\n\t.reg .b64 y;\n\t.reg .b32 a, b;\n\t"
-      "setp.eq.b32 t, 0, 0;\n\t"
-      "mov.b64 y, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%5, %6, %7, %8}, t;\n\t"
-      "add.u32 a, %1, 8;\n\tadd.u32 b, %2, 128;\n\tmov.b64 y, {b, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t"
-      "add.u32 a, %1, 16;\n\tadd.u32 b, %2, 256;\n\tmov.b64 y, {b, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t"
-      "add.u32 a, %1, 24;\n\tadd.u32 b, %2, 384;\n\tmov.b64 y, {b, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, {%5, %6, %7, %8}, t;\n\t}" ::"r"(d),
-      "r"(p_at), "r"(v_lo), "r"(kDescHi), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
-      : "memory");
+                                                 const uint4* others) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4 off = others[k];
+    asm volatile(
+        "{\n\t.reg .pred t;\n\t.reg .b64 y;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%5, %6, %7, %8}, t;\n\t}" ::"r"(d),
+        "r"(p_at + k * 8), "r"(v_lo + k * 128), "r"(kDescHi), "r"(idesc), "r"(off.x), "r"(off.y), "r"(off.z), "r"(off.w)
+        : "memory");
+  }
 }
 
 // One lane of the (converged) warp.
@@ -263,24 +261,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // What lies behind the tiles in shared memory.
-struct Tail {
+struct __align__(16) Tail {
   uint64_t q_full;
   uint64_t landed[10], full[10], empty[10];
   uint64_t s_full[2], p_ready[2][2], o_done[2];  // P is handed on in two halves of its keys
   uint64_t drain;
-  // Tiles in the order of their K loads: first pool row of each 16 keys (-1:
-  // none, zeros), and how many keys hold tokens.
+  // Tiles in the order of their K loads: of each group of 16 keys the first pool
+  // row (-1: none, zeros), the keys that hold tokens, and for own tokens of packed
+  // rows the output lanes of other sequences (row r: bit r mod 32 of word r / 32).
   uint64_t looked_up[kLooked], done_with[kLooked];
+  uint4 others[kLooked][8];
   int rows[kLooked][8];
-  int fill[kLooked];
+  uint8_t live[kLooked][8];
   uint32_t tmem_base;
   int abort;
   int warp_sum[8];
-  // Packed rows, per query row of each tile: its sequence (-1: none), and the
-  // own key tiles of the sequences up to it, each sequence's counted at its last
-  // row in the tile.  Own tile o of a ring is of the first row with more than o.
-  int seq[2][128];
-  int tiles[2][128];
+  // Packed rows, per query row of each tile: its sequence (-1: none; counted from
+  // the CTA's first row without q_start), and the groups of 16 own keys of the
+  // sequences up to it, each sequence's counted at its last row in the tile.
+  int16_t seq[2][128];
+  int groups[2][128];
 };
 static_assert(sizeof(Tail) <= 3072, "the tail of shared memory");
 
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.drain, 1);
     for (int e = 0; e < kLooked; ++e) {
       mbar_init(&bars.looked_up[e], 1);
-      mbar_init(&bars.done_with[e], 4);  // one arrival per producer warp
+      mbar_init(&bars.done_with[e], WHOLE ? 4 : 5);  // the producer warps, and the issuer for the lanes
     }
     abort_sh = 0;
     fence_mbar_init();
@@ -361,7 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = own - nq + m + 1;
     return v < 0 ? 0 : v;
   };
-  // own key tiles of each ring's rows
+  // own key tiles of each ring's rows: 128 tokens of the sequence, or eight
+  // groups of 16 of the packed sequences, one after another
+  const int first_seq = p.q_start == nullptr ? mrel : 0;
   int own0, own1, see = 0;
   if (WHOLE) {
     const int see0 = seen(mrel + rows0 - 1), see1 = dual ? 0 : seen(mrel + a.mt + rows1 - 1);
@@ -373,14 +375,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int m_end = mrel + rows0 + rows1;
     if (p.q_start == nullptr) {
       const int m = mrel + static_cast<int>(threadIdx.x);
-      if (m < m_end && m < p.n_seq) bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = m;
+      if (m < m_end && m < p.n_seq) bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = static_cast<int16_t>(m - mrel);
     } else {
       for (int b = threadIdx.x; b < p.n_seq; b += kThreads) {
         const int from = p.q_start[b], to = p.q_start[b + 1];
         if ((from < 0 || to > p.M || to < from || to - from > p.max_q) && kvh == 0 && split == 0)
           report_status(p.status, LR_ERR_INDEX_RANGE);
         for (int m = from > mrel ? from : mrel; m < to && m < m_end; ++m)
-          bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = b;
+          bars.seq[m - mrel >= a.mt][(m - mrel) % a.mt] = static_cast<int16_t>(b);
       }
     }
     __syncthreads();
@@ -389,10 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = threadIdx.x >> 7, j = threadIdx.x & 127, rows = t ? rows1 : rows0;
       const int b = bars.seq[t][j];
       if (j < rows && b >= 0 && (j == rows - 1 || bars.seq[t][j + 1] != b)) {
-        const SeqView v = seq_view(p, b, kvh == 0 && split == 0);
+        const SeqView v = seq_view(p, first_seq + b, kvh == 0 && split == 0);
         int vis = v.len - v.nq + (mrel + t * a.mt + j - v.q0) + 1;
         vis = vis > v.len ? v.len : vis;
-        if (vis > 0) sum = (vis + kKeys - 1) / kKeys;
+        if (vis > 0) sum = (vis + kPage - 1) / kPage;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -404,10 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (threadIdx.x < 256) {
       for (int w = warp & ~3; w < warp; ++w) sum += bars.warp_sum[w];
-      (&bars.tiles[0][0])[threadIdx.x] = sum;
+      (&bars.groups[0][0])[threadIdx.x] = sum;
     }
     __syncthreads();
-    own0 = bars.tiles[0][127], own1 = bars.tiles[1][127];
+    own0 = (bars.groups[0][127] + 7) / 8, own1 = (bars.groups[1][127] + 7) / 8;
   }
   const int P = prefix_rows(p, prefix_len, tell && blockIdx.x == 0);
   const int np = (P + kKeys - 1) / kKeys;
@@ -424,14 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = s_hi - s_lo, n0 = of_range(e0), n1 = of_range(e1);  // n is the larger of the two
   // the first n_both of them have one key tile for both rings
   const int n_both = dual ? 0 : (WHOLE ? n : of_range(np));
-  // Own tile o of ring t's list of packed rows: the row of the tile that it is
-  // counted at, found from a row at or before it.
-  auto own_row = [&](int t, int o, int from) {
-    const int* tiles = bars.tiles[dual ? 0 : t];
-    while (from < 127 && tiles[from] <= o) ++from;
-    return from;
-  };
-
   if (warp == kMmaWarp) {
     tmem_alloc(&bars.tmem_base, kTmemCols);
     tmem_relinquish();
@@ -509,11 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars.empty[slot], phase, &abort_sh));
             if (!ok) break;
             const uint16_t* pool = is_k ? p.k : p.v;
-            const int fill = bars.fill[e] - g0 * kPage;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int row = bars.rows[e][g0 + h];
-              const int live = row < 0 ? 0 : fill - h * kPage;
+              const int live = bars.live[e][g0 + h];
               const uint16_t* src = pool + static_cast<int64_t>((row < 0 ? 0 : row) + r_in) * p.ld + head_off;
               const uint32_t at = slot * S::kTileBytes + h * kPage * 128;
               if (live >= kPage) {
@@ -546,48 +539,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       regs_fewer<kRegsIssue>();
       if (warp == kPageWarp) {
         // ------------------------------------------------------- pages
+        // Lane g (mod 8) looks group g of the tile up.
         bool ok = true;
         int e = 0, at_row0 = 0, at_row1 = 0;
+        uint32_t phase = 0;  // of the entries
         auto index_of = [&](int t) { return p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows; };
 #pragma unroll 1
         for (int x = 0; x < (a.stall ? 0 : 2 * n) && ok; ++x) {
-          const int j = x >> 1, t = x & 1;
+          const int j = x >> 1, t = x & 1, g = lane & 7;
           if (!(j < n_both ? t == 0 : j < (t ? n1 : n0))) continue;
           const int c = dual ? 2 * (s_lo + j) + t : s_lo + j;
           const int32_t* pages = p.prefix_blocks;
-          int t0 = c * kKeys, limit = P;
-          if (c >= np) {
-            const int o = c - np;
+          int t0 = c * kKeys + g * kPage, limit = P;
+          uint4 others = make_uint4(0, 0, 0, 0);
+          if (WHOLE && c >= np) {
             pages = own_pages;
-            t0 = o * kKeys, limit = see;
-            if (!WHOLE) {
-              const int list = dual ? 0 : t;
-              const int r = own_row(t, o, t ? at_row1 : at_row0);
-              (t ? at_row1 : at_row0) = r;
-              const int b = bars.seq[list][r];
+            t0 -= np * kKeys, limit = see;
+          }
+          if (!WHOLE && c >= np) {
+            const int list = dual ? 0 : t;
+            const int* groups = bars.groups[list];
+            const int16_t* seq = bars.seq[list];
+            const int group = (c - np) * 8 + g;
+            int r = t ? at_row1 : at_row0;
+            while (r < 127 && groups[r] <= group) ++r;
+            (t ? at_row1 : at_row0) = __shfl_sync(0xffffffffu, r, 0);
+            limit = 0;
+            if (group < groups[127]) {
+              const int b = first_seq + seq[r];
               pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
               const int len = p.lengths[b];
-              t0 = (o - (r > 0 ? bars.tiles[list][r - 1] : 0)) * kKeys;
               limit = len < p.cap_own ? len : p.cap_own;
+              t0 = (group - (r > 0 ? groups[r - 1] : 0)) * kPage;
+              int from = r;
+              while (from > 0 && seq[from - 1] == seq[r]) --from;
+              uint32_t off[4];
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const int lo = from * G - 32 * w, hi = (r + 1) * G - 32 * w;
+                const uint32_t below = lo <= 0 ? 0u : (lo >= 32 ? ~0u : (1u << lo) - 1u);
+                const uint32_t under = hi <= 0 ? 0u : (hi >= 32 ? ~0u : (1u << hi) - 1u);
+                off[w] = ~(under & ~below);
+              }
+              others = make_uint4(off[0], off[1], off[2], off[3]);
+            } else {
+              others = make_uint4(~0u, ~0u, ~0u, ~0u);
             }
           }
-          const int tg = t0 + (lane & 7) * kPage;  // the first of this lane's 16 keys
-          int row = -1;
-          if (tg < limit) {
-            const int k = index_of(tg);
+          int row = -1, live = limit - t0;
+          live = live < 0 ? 0 : (live > kPage ? kPage : live);
+          if (live > 0) {
+            const int k = index_of(t0);
             const int page = pages[k];
-            if (page < 0 || page >= p.pool_blocks)
-              report_status(p.status, LR_ERR_REMAP_RANGE);  // reads as zeros
-            else
-              row = page * p.block_rows + (tg - k * p.block_rows);
+            if (page < 0 || page >= p.pool_blocks) {  // reads as zeros
+              report_status(p.status, LR_ERR_REMAP_RANGE);
+              live = 0;
+            } else {
+              row = page * p.block_rows + (t0 - k * p.block_rows);
+            }
           }
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars.done_with[e % kLooked], ((e / kLooked) & 1) ^ 1, &abort_sh));
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.done_with[e], phase ^ 1u, &abort_sh));
           if (ok) {
-            if (lane < 8) bars.rows[e % kLooked][lane] = row;
-            if (lane == 0) bars.fill[e % kLooked] = limit - t0;
+            if (lane < 8) {
+              bars.rows[e][lane] = row;
+              bars.live[e][lane] = static_cast<uint8_t>(live);
+              if (!WHOLE) bars.others[e][lane] = others;
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.looked_up[e % kLooked]);
-            ++e;
+            if (lane == 0) mbar_arrive(&bars.looked_up[e]);
+            if (++e == kLooked) e = 0, phase ^= 1u;
           }
         }
         if (!ok && lane == 0) {
@@ -635,37 +655,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&bars.s_full[t]);
           };
           // round r of ring t; its last one completes the ring's O
-          int at_row0 = 0, at_row1 = 0;
-          auto pv = [&](int t, int at, int r, bool last) {
+          auto pv = [&](int t, int at, int r, int e, bool last) {
             const uint32_t v_at = r_v + at * (S::kTileBytes >> 4), p_at = tmem + t * kKeys, d = tmem + 256 + t * HD;
-            uint32_t off[4] = {0, 0, 0, 0};
-            if (!WHOLE) {  // rows of other sequences keep their O
-              const int c = dual ? 2 * (s_lo + r) + t : s_lo + r;
-              if (c >= np) {
-                const int* seq = bars.seq[dual ? 0 : t];
-                const int j = own_row(t, c - np, t ? at_row1 : at_row0);
-                (t ? at_row1 : at_row0) = j;
-                int from = j;
-                while (from > 0 && seq[from - 1] == seq[j]) --from;
-                const int lo = from * G, hi = (j + 1) * G;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const int x = lo - 32 * w, y = hi - 32 * w;
-                  const uint32_t below = x <= 0 ? 0u : (x >= 32 ? ~0u : (1u << x) - 1u);
-                  const uint32_t under = y <= 0 ? 0u : (y >= 32 ? ~0u : (1u << y) - 1u);
-                  off[w] = ~(under & ~below);
-                }
-              }
-            }
+            const bool some = !WHOLE && (dual ? 2 * (s_lo + r) + t : s_lo + r) >= np;
+            if (some && ok) ok = mbar_wait(&bars.looked_up[e & 15], e >> 4, &abort_sh);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               if (ok) ok = mbar_wait(&bars.p_ready[t][half], r & 1, &abort_sh);
               if (!ok) return;
               tc_fence_after();
-              if (WHOLE)
-                mma_pv_half(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, r | half);
+              // packed rows start from a cleared O
+              if (some)
+                mma_pv_half_some(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, &bars.others[e & 15][half * 4]);
               else
-                mma_pv_half_some(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, off);
+                mma_pv_half(d, p_at + half * 32, v_at + half * (64 * 128 >> 4), kIdO, WHOLE ? r | half : 1);
             }
             if (last) tc_commit(&bars.o_done[t]);
           };
@@ -675,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Step i's second products, then the next step's first ones (step -1: the
           // first ones alone).  A tile for both rings is released after the second
           // ring's product.
+          int looked = 0, e0 = 0, e1 = 0, n0_e = 0, next_e = 0;  // the entries of the rings' tiles: number, and turn in bit 4
 #pragma unroll 1
           for (int i = -1; i < n && ok; ++i) {
             const bool both = i < n_both, both1 = i + 1 < n_both;
@@ -684,15 +688,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int mine = t ? n1 : n0;
               if (i >= 0 && i < mine) {
                 if (!both || at_v < 0) at_v = next_slot();
-                pv(t, at_v, i, i + 1 == mine);
+                const int e = both ? e0 : (t ? e1 : e0);
+                pv(t, at_v, i, e, i + 1 == mine);
                 if (!both) release(at_v);
+                if (!WHOLE && ok && (!both || t == 1)) mbar_arrive(&bars.done_with[e & 15]);
               }
               if (i + 1 < mine) {
-                if (!both1 || at_k < 0) at_k = next_slot();
+                if (!both1 || at_k < 0) {
+                  at_k = next_slot();
+                  next_e = looked;
+                  if ((++looked & 15) == kLooked) looked = (looked >> 4 ^ 1) << 4;
+                }
                 qk(t, at_k);
                 if (!both1) release(at_k);
+                if (t)
+                  e1 = next_e;
+                else
+                  n0_e = next_e;
               }
             }
+            e0 = n0_e;
             if (both && at_v >= 0) release(at_v);
             if (both1 && at_k >= 0) release(at_k);
           }
@@ -714,14 +729,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = ringi;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 256 + t * HD + lanes;
-      // own tokens that this row sees (rows past the tile's are never stored)
-      int vis = 0, at_row = 0;
+      // own tokens that this row sees (rows past the tile's are never stored), and
+      // where its sequence's lie in the list of packed tiles
+      int vis = 0, list_lo = 0, list_hi = 0;
       if (WHOLE) {
         vis = seen(mrel + tile * a.mt + trow / G);
       } else if (my_seq >= 0) {
-        const SeqView v = seq_view(p, my_seq, false);
+        const SeqView v = seq_view(p, first_seq + my_seq, false);
         vis = v.len - v.nq + (mrel + tile * a.mt + trow / G - v.q0) + 1;
-        if (vis > v.len) vis = v.len;
+        vis = vis > v.len ? v.len : (vis < 0 ? 0 : vis);
+        int r = trow / G;
+        while (r < (tile ? rows1 : rows0) - 1 && bars.seq[tile][r + 1] == my_seq) ++r;
+        list_lo = r > 0 ? bars.groups[tile][r - 1] * kPage : 0;
+        list_hi = bars.groups[tile][r] * kPage;
       }
       if (!WHOLE) {  // the rows of a tile do not all take part in its first product
         uint32_t z[16];
@@ -738,21 +758,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // keys of the tile that the row sees
+        // The row sees the tile's keys from lo to below hi.  Of a packed tile of own
+        // tokens, a row whose sequence is not in it only keeps its state: its output
+        // lane is off.
         const int c = dual ? 2 * (s_lo + i) + t : s_lo + i;
-        int lim = P - c * kKeys;
-        bool mine = true;  // else the output lane is disabled: the row only keeps its state
+        int lo = 0, hi = P - c * kKeys;
+        bool mine = true;
         if (c >= np) {
-          lim = vis - (c - np) * kKeys;
+          const int first = (c - np) * kKeys;
+          hi = vis - first;
           if (!WHOLE) {
-            const int list = dual ? 0 : t;
-            at_row = own_row(t, c - np, at_row);
-            lim = vis - (c - np - (at_row > 0 ? bars.tiles[list][at_row - 1] : 0)) * kKeys;
-            mine = bars.seq[list][at_row] == my_seq;
-            if (!mine) lim = kKeys;
+            mine = list_lo < first + kKeys && list_hi > first;
+            lo = mine ? list_lo - first : 0;
+            hi = mine ? lo + vis : kKeys;
           }
         }
-        if (busy && !__any_sync(0xffffffffu, mine && lim > 0)) {  // none of the warp's rows: P = 0
+        if (WHOLE && busy && !__any_sync(0xffffffffu, hi > 0)) {  // none of the warp's rows: P = 0
           uint32_t z[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) z[j] = 0;
@@ -762,15 +783,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.p_ready[t][0]);
-        } else if (busy) {
+        } else if (busy && (WHOLE || __any_sync(0xffffffffu, mine))) {
           uint32_t s[kKeys];
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
           tmem_ld_wait();
-          if (__any_sync(0xffffffffu, lim < kKeys)) {
+          if (__any_sync(0xffffffffu, hi < kKeys || lo > 0)) {
+            if (WHOLE) {
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if (j >= lim) s[j] = 0xFF800000u;  // -inf
+              for (int j = 0; j < kKeys; ++j)
+                if (j >= hi) s[j] = 0xFF800000u;  // -inf
+            } else {
+              const uint32_t width = hi > lo ? hi - lo : 0;
+#pragma unroll
+              for (int j = 0; j < kKeys; ++j)
+                if (static_cast<uint32_t>(j - lo) >= width) s[j] = 0xFF800000u;
+            }
           }
           float tops[4];
 #pragma unroll
