@@ -537,22 +537,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       regs_fewer<kRegsIssue>();
+      // K and V tiles of this CTA
+      const int loads = 2 * (n_both + (n0 > n_both ? n0 - n_both : 0) + (n1 > n_both ? n1 - n_both : 0));
       if (warp == kPageWarp) {
         // ------------------------------------------------------- pages
-        // Lane g (mod 8) looks group g of the tile up.
+        // Four tiles at a time, a lane for each group: a page's number takes a trip
+        // to memory, and one for four tiles is soon enough.
         bool ok = true;
-        int e = 0, at_row0 = 0, at_row1 = 0;
+        int e = 0;
         uint32_t phase = 0;  // of the entries
+        const int pairs = (n0 < n1 ? n0 : n1) - n_both;
         auto index_of = [&](int t) { return p.block_shift >= 0 ? t >> p.block_shift : t / p.block_rows; };
 #pragma unroll 1
-        for (int x = 0; x < (a.stall ? 0 : 2 * n) && ok; ++x) {
-          const int j = x >> 1, t = x & 1, g = lane & 7;
-          if (!(j < n_both ? t == 0 : j < (t ? n1 : n0))) continue;
+        for (int k0 = 0; k0 < (a.stall ? 0 : loads / 2) && ok; k0 += 4) {
+          // the tiles in the order of their loads: those for both rings, then each
+          // ring's in turn, then what one ring has more than the other
+          const int k = k0 + (lane >> 3), g = lane & 7;
+          int j = k, t = 0;
+          if (k >= n_both) {
+            const int x = k - n_both;
+            j = n_both + (x < 2 * pairs ? x >> 1 : x - pairs);
+            t = x < 2 * pairs ? x & 1 : n1 > n0;
+          }
           const int c = dual ? 2 * (s_lo + j) + t : s_lo + j;
           const int32_t* pages = p.prefix_blocks;
-          int t0 = c * kKeys + g * kPage, limit = P;
+          int t0 = c * kKeys + g * kPage, limit = k < loads / 2 ? P : 0;
+          int row = -1, live = 0;
           uint4 others = make_uint4(0, 0, 0, 0);
-          if (WHOLE && c >= np) {
+          if (WHOLE && c >= np && k < loads / 2) {
             pages = own_pages;
             t0 -= np * kKeys, limit = see;
           }
@@ -561,15 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int* groups = bars.groups[list];
             const int16_t* seq = bars.seq[list];
             const int group = (c - np) * 8 + g;
-            int r = t ? at_row1 : at_row0;
-            while (r < 127 && groups[r] <= group) ++r;
-            (t ? at_row1 : at_row0) = __shfl_sync(0xffffffffu, r, 0);
             limit = 0;
+            others = make_uint4(~0u, ~0u, ~0u, ~0u);
             if (group < groups[127]) {
+              int r = 0;  // the first row with more than `group` groups
+#pragma unroll 1
+              for (int half = 64; half > 0; half >>= 1)
+                if (groups[r + half - 1] <= group) r += half;
               const int b = first_seq + seq[r];
               pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
-              const int len = p.lengths[b];
-              limit = len < p.cap_own ? len : p.cap_own;
+              limit = p.lengths[b];
               t0 = (group - (r > 0 ? groups[r - 1] : 0)) * kPage;
               int from = r;
               while (from > 0 && seq[from - 1] == seq[r]) --from;
@@ -582,28 +595,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 off[w] = ~(under & ~below);
               }
               others = make_uint4(off[0], off[1], off[2], off[3]);
-            } else {
-              others = make_uint4(~0u, ~0u, ~0u, ~0u);
             }
           }
-          int row = -1, live = limit - t0;
-          live = live < 0 ? 0 : (live > kPage ? kPage : live);
-          if (live > 0) {
-            const int k = index_of(t0);
-            const int page = pages[k];
+          // A group in a list of packed rows holds a token: its page is asked for
+          // beside the sequence's length.
+          if (!WHOLE && c >= np ? others.x != ~0u || others.y != ~0u || others.z != ~0u || others.w != ~0u : t0 < limit) {
+            const int x = index_of(t0);
+            const int page = pages[x];
+            live = limit < p.cap_own || c < np ? limit - t0 : p.cap_own - t0;
+            live = live > kPage ? kPage : live;
             if (page < 0 || page >= p.pool_blocks) {  // reads as zeros
               report_status(p.status, LR_ERR_REMAP_RANGE);
               live = 0;
             } else {
-              row = page * p.block_rows + (t0 - k * p.block_rows);
+              row = page * p.block_rows + (t0 - x * p.block_rows);
             }
           }
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars.done_with[e], phase ^ 1u, &abort_sh));
-          if (ok) {
-            if (lane < 8) {
-              bars.rows[e][lane] = row;
-              bars.live[e][lane] = static_cast<uint8_t>(live);
-              if (!WHOLE) bars.others[e][lane] = others;
+#pragma unroll 1
+          for (int q = 0; q < 4 && k0 + q < loads / 2; ++q) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.done_with[e], phase ^ 1u, &abort_sh));
+            if (!ok) break;
+            if (lane >> 3 == q) {
+              bars.rows[e][g] = row;
+              bars.live[e][g] = static_cast<uint8_t>(live);
+              if (!WHOLE) bars.others[e][g] = others;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.looked_up[e]);
@@ -616,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else if (warp == kRelayWarp) {
         bool ok = true;
-        const int loads = 2 * (n_both + (n0 > n_both ? n0 - n_both : 0) + (n1 > n_both ? n1 - n_both : 0));
 #pragma unroll 1
         for (int l = 0; l < loads && ok; ++l) {
           ok = __all_sync(0xffffffffu, mbar_wait(&bars.landed[l % kSlots], (l / kSlots) & 1, &abort_sh));
@@ -758,21 +772,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // The row sees the tile's keys from lo to below hi.  Of a packed tile of own
-        // tokens, a row whose sequence is not in it only keeps its state: its output
-        // lane is off.
+        // Of the tile's eight groups of 16 keys the row takes those in `use`, and of
+        // these the keys below hi.  The others are keys of other sequences: the
+        // row's output lane is off in their products, so that they only have to
+        // stay out of its maximum and sum, and that goes by whole groups.
         const int c = dual ? 2 * (s_lo + i) + t : s_lo + i;
-        int lo = 0, hi = P - c * kKeys;
-        bool mine = true;
+        int hi = P - c * kKeys, end = kKeys;
+        uint32_t use = 0xFFu;
         if (c >= np) {
           const int first = (c - np) * kKeys;
           hi = vis - first;
           if (!WHOLE) {
-            mine = list_lo < first + kKeys && list_hi > first;
-            lo = mine ? list_lo - first : 0;
-            hi = mine ? lo + vis : kKeys;
+            const int from = list_lo - first > 0 ? list_lo - first : 0;
+            end = list_hi - first < kKeys ? list_hi - first : kKeys;
+            use = end > from ? (0xFFu >> (8 - end / kPage)) & (0xFFu << (from / kPage)) : 0u;
+            hi = use ? list_lo - first + vis : kKeys;
           }
         }
+        const bool mine = use != 0;
         if (WHOLE && busy && !__any_sync(0xffffffffu, hi > 0)) {  // none of the warp's rows: P = 0
           uint32_t z[16];
 #pragma unroll
@@ -788,26 +805,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
           tmem_ld_wait();
-          if (__any_sync(0xffffffffu, hi < kKeys || lo > 0)) {
-            if (WHOLE) {
+          // groups that some row of the warp sees a part of
+          const uint32_t beyond = hi >= end ? 0u : (hi <= 0 ? use : use & (0xFFu << (hi / kPage)));
+          const uint32_t cut = __reduce_or_sync(0xffffffffu, beyond);
+          if (cut != 0) {
 #pragma unroll
-              for (int j = 0; j < kKeys; ++j)
-                if (j >= hi) s[j] = 0xFF800000u;  // -inf
-            } else {
-              const uint32_t width = hi > lo ? hi - lo : 0;
+            for (int g = 0; g < 8; ++g)
+              if (cut >> g & 1u) {
+                const int left = use >> g & 1u ? hi - g * kPage : kPage;
 #pragma unroll
-              for (int j = 0; j < kKeys; ++j)
-                if (static_cast<uint32_t>(j - lo) >= width) s[j] = 0xFF800000u;
-            }
+                for (int j = 0; j < kPage; ++j)
+                  if (j >= left) s[g * kPage + j] = 0xFF800000u;  // -inf
+              }
           }
-          float tops[4];
+          const bool full = WHOLE || __all_sync(0xffffffffu, use == 0xFFu);
+          float tops[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tops[j] = fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 4]));
+          for (int g = 0; g < 8; ++g) {
+            const uint32_t* x = s + g * kPage;
+            float m = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
 #pragma unroll
-          for (int j = 8; j < kKeys; j += 8)
+            for (int j = 3; j < 15; j += 2) m = max3(m, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+            tops[g] = fmaxf(m, __uint_as_float(x[15]));
+          }
+          if (!full) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + e + 4]));
-          const float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+            for (int g = 0; g < 8; ++g)
+              if ((use >> g & 1u) == 0) tops[g] = -INFINITY;
+          }
+          const float top = fmaxf(max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[4]), max3(tops[5], tops[6], tops[7]));
           const float now = mine ? fmaxf(mref, top * p.scale_log2) : mref;
           const bool move = now > mref + kSlack;  // -inf + 8 is -inf: the first key moves it
           if (__any_sync(0xffffffffu, move)) {
@@ -829,19 +855,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float neg = mref == -INFINITY ? 0.f : -mref;
           const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2), neg2 = pack2(neg, neg);
-          uint64_t part[2] = {0, 0};
+          uint64_t part[8];  // of each group
 #pragma unroll
           for (int c = 0; c < kKeys / 64; ++c) {
             uint32_t w[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const uint64_t e =
-                  fma2(pack2(__uint_as_float(s[c * 64 + 2 * j]), __uint_as_float(s[c * 64 + 2 * j + 1])), scale2, neg2);
+              const int at = c * 64 + 2 * j, g = at / kPage;
               float x, y;
-              unpack2(e, x, y);
+              unpack2(fma2(pack2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), scale2, neg2), x, y);
               x = ex2(x);
               y = ex2(y);
-              part[j & 1] = add2(part[j & 1], pack2(x, y));
+              part[g] = at % kPage == 0 ? pack2(x, y) : add2(part[g], pack2(x, y));
               // the product takes bf16: the powers round here, their sum does not
               asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
             }
@@ -853,8 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) mbar_arrive(&bars.p_ready[t][0]);
             }
           }
+          if (!full) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              if ((use >> g & 1u) == 0) part[g] = 0;
+          }
           float pa, pb;
-          unpack2(add2(part[0], part[1]), pa, pb);
+          unpack2(add2(add2(add2(part[0], part[1]), add2(part[2], part[3])),
+                       add2(add2(part[4], part[5]), add2(part[6], part[7]))), pa, pb);
           if (mine) sum += pa + pb;
           tmem_st_wait();
         } else if (lane == 0) {
