@@ -451,10 +451,11 @@ int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 int64_t most_q(int64_t M, const lr_attn_desc* d) { return d->max_q < M ? d->max_q : (M < 1 ? 1 : M); }
 
 // Key ranges for `ctas` row tiles: as many as fill `want` CTAs, none shorter
-// than min_keys.
+// than min_keys.  (The workspace rule comes here with sizes that the call itself
+// refuses: a count that wrapped gets one range.)
 int slots_for(int64_t ctas, int64_t keys, int64_t want, int64_t min_keys) {
   if (keys <= 0) return 0;
-  int64_t n = ctas >= want ? 1 : want / ctas;
+  int64_t n = ctas >= want || ctas < 1 ? 1 : want / ctas;
   const int64_t most = cdiv(keys, min_keys);
   if (n > most) n = most;
   if (n > kMaxSlots) n = kMaxSlots;
@@ -472,6 +473,7 @@ struct AttnPlan {
 };
 
 constexpr int kMinSteps = 4;
+constexpr int kMostHeads = 64;  // query heads a key head: a tile has two query rows at least
 
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   AttnPlan a;
@@ -518,7 +520,7 @@ lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
   if (c.head_dim != 64 && c.head_dim != 128)
     return bad(LR_ERR_UNSUPPORTED, "%s: head_dim %d is neither 64 nor 128", who, c.head_dim);
   if (c.block_rows % 16) return bad(LR_ERR_UNSUPPORTED, "%s: block_rows %d is not a multiple of 16", who, c.block_rows);
-  if (d->n_heads / c.n_kv_heads > 64)
+  if (d->n_heads / c.n_kv_heads > kMostHeads)
     return bad(LR_ERR_UNSUPPORTED, "%s: more than 64 query heads a key head", who);
   if (c.n_kv_heads > 65535) return bad(LR_ERR_UNSUPPORTED, "%s: more than 65535 key heads", who);
   if (!(d->scale > 0.f) || std::isinf(d->scale)) return bad(LR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
@@ -607,8 +609,8 @@ using namespace lr;
 extern "C" {
 
 size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d) {
-  if (d == nullptr || M <= 0 || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
-      d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
+  if (d == nullptr || M <= 0 || M > 0x7FFFFFFF || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
+      d->n_heads / d->cache.n_kv_heads > kMostHeads || d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
     return 0;
   return attn_plan(M, d).bytes;
 }

@@ -101,10 +101,12 @@ def _attn(d=None, M=9, q=0x10000, ldq=1024, out=0x20000, ldo=1024, dt=lr.LR_BF16
 def test_prefix_attention_refusals_launch_nothing():
     assert _attn(M=0) == lr.LR_OK
     bad, no = lr.LR_ERR_INVALID_ARG, lr.LR_ERR_UNSUPPORTED
-    need = lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(_desc()))
+    long = _desc(cap_prefix_blocks=100)   # several key ranges, whose results meet in the workspace
+    need = lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(long))
     assert need > 0
-    for kw in (dict(q=None), dict(out=None), dict(q=0x10002), dict(ldq=1000), dict(ldo=1028), dict(dt=3), dict(M=-1),
-               dict(ws=None), dict(ws=0x30010), dict(ws_bytes=need - 1)):
+    for kw in (dict(ws=None), dict(ws=0x30010), dict(ws_bytes=need - 1)):
+        assert _attn(d=long, **kw) == bad, kw
+    for kw in (dict(q=None), dict(out=None), dict(q=0x10002), dict(ldq=1000), dict(ldo=1028), dict(dt=3), dict(M=-1)):
         assert _attn(**kw) == bad, kw
     for kw in (dict(n_heads=7), dict(n_heads=0), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(prefix_blocks=None), dict(prefix_len=None), dict(cap_prefix_blocks=-1), dict(n_seq=-1),
@@ -122,7 +124,26 @@ def test_workspace_covers_capacities_and_is_zero_for_nothing():
     f = lambda M, **kw: lr.lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(_desc(**kw)))
     assert f(0) == 0 and f(-3) == 0
     assert lr.lib.lr_prefix_attention_workspace_bytes(9, None) == 0
-    assert f(9, cap_prefix_blocks=100) >= f(9) > 0
+    assert f(9, cap_prefix_blocks=200) >= f(9, cap_prefix_blocks=100) > 0
+    assert f(9) == 0   # one key range: nothing to join
+
+
+def test_workspace_of_refused_head_groups_is_zero():
+    """More query heads a key head than a tile has rows: refused by the call, and no division by zero before it."""
+    for nh in (130, 256, 260, 1 << 20):
+        d = _desc(n_heads=nh)
+        assert lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(d)) == 0
+        assert _attn(d=d, ldq=1 << 28, ldo=1 << 28) == lr.LR_ERR_UNSUPPORTED
+    f = lambda M, **kw: lr.lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(_desc(**kw)))
+    assert f(1 << 39) == 0 and f(1 << 62) == 0
+    f((1 << 31) - 1, n_seq=1 << 30, cache=_cache(n_kv_heads=1 << 14), n_heads=1 << 14, max_q=1 << 25)  # counts that wrap
+    many = _desc(n_heads=512, cache=_cache(n_kv_heads=1))
+    b = _block(n_heads=512, n_kv_heads=1)
+    b.f[0], b.f[3] = lr.Factor(0x10000, 0x20000, 512, 65536, 64), lr.Factor(0x30000, 0x40000, 65536, 512, 64)
+    for i in (1, 2):
+        b.f[i] = lr.Factor(0x50000, 0x60000, 512, 128, 64)
+    assert lr.lib.lr_block_forward_cached(0x1000, 9, ctypes.byref(b), ctypes.byref(_context(attn=many)), 0x100000, BIG,
+                                          None, None) == lr.LR_ERR_UNSUPPORTED
 
 
 def _block(**kw):
