@@ -436,7 +436,9 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  * n_kv_heads)).  A row that sees no token comes out zero, and so does a row of
  * q that belongs to no sequence.  Pool rows that hold no token of the batch
  * (the ends of last pages among them) do not reach the result, whatever they
- * hold.
+ * hold, nor does a sequence's own token reach another sequence's rows.  Within
+ * a sequence of several query rows a token that a row does not see has the
+ * weight 0 there, which leaves a NaN or infinity among its values a NaN.
  *   q: device bf16 [M][ldq]; out: device [M][ldo] of out_dtype (LR_BF16 or
  *   LR_F32); M < 2^31; 16-byte aligned, ldq and ldo multiples of 8 and >=
  *   n_heads * head_dim.
@@ -450,14 +452,13 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   Lengths, pages and row offsets are read on the device: a captured call
  *   serves every batch within the capacities.  A length outside its capacity
  *   (block_rows times the pages it may use) is clamped and reported as
- *   LR_ERR_INDEX_RANGE, as is a q_start outside [0, M], one that decreases, or
+ *   LR_ERR_INDEX_RANGE (an own length where its sequence has query rows), as is a q_start outside [0, M], one that decreases, or
  *   more than max_q rows (such a sequence's rows past max_q are unspecified).
  *   A listed page outside [0, pool_blocks) reads as zeros and reports
  *   LR_ERR_REMAP_RANGE.
  *   head_dim 64 or 128; block_rows a multiple of 16; blocks_per_seq * block_rows
- *   below 2^24; n_heads a multiple of
- *   n_kv_heads with at most 64 query heads a kv head (LR_ERR_UNSUPPORTED
- *   otherwise, LR_ERR_INVALID_ARG for a remainder); scale > 0 and finite.
+ *   below 2^24; n_heads a multiple of n_kv_heads with at most 64 query heads a
+ *   kv head (LR_ERR_UNSUPPORTED otherwise, LR_ERR_INVALID_ARG for a remainder); scale > 0 and finite.
  *   workspace: device, 256-byte aligned, at least
  *   lr_prefix_attention_workspace_bytes(M, d); contents on entry do not
  *   matter; calls that share it must be ordered on one stream.
@@ -567,8 +568,8 @@ const char* lr_last_error(void);
 
 /* ---------------------------------------------------------------------------
  * Testing hook (no counterpart on the pages).  lr_test_stall_producer(1) makes
- * the TMA producers of every decode-size GEMM and every SM-pair prefill GEMM
- * launched afterwards issue no copy, so the bounded wait of the thread that
+ * the producers of every decode-size GEMM, every SM-pair prefill GEMM and every
+ * attention launch on tensor-core tiles afterwards issue no copy, so the bounded wait of the thread that
  * consumes the copies runs out:
  * the launch reports LR_ERR_TIMEOUT through dev_status (after about two
  * seconds), releases its resources and returns, and the context stays usable.
@@ -589,6 +590,14 @@ void lr_test_stall_producer(int32_t on);
  * the up projection wait and vary the order of the tiles; results do not
  * depend on it.  Nothing else sets it, and no environment variable does. */
 void lr_test_prefill_schedule(int32_t lag, int32_t group);
+
+/* Testing hook (no counterpart on the pages).  lr_prefix_attention has a kernel
+ * for few query rows and one on tensor-core tiles and chooses by the call's
+ * sizes.  lr_test_attention_kernel(1) makes every later call take the first,
+ * 2 the second, 0 restores the choice; the workspace rule follows.  It exists
+ * so that tests can run both on one problem.  Nothing else sets it, and no
+ * environment variable does. */
+void lr_test_attention_kernel(int32_t which);
 
 
 #ifdef __cplusplus

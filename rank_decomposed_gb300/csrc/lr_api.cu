@@ -52,6 +52,8 @@ int num_sms() {
 
 static std::atomic<int> g_stall_producer{0};
 
+static std::atomic<int> g_attention_kernel{0};
+int test_attention_kernel() { return g_attention_kernel.load(std::memory_order_relaxed); }
 bool test_stall_producer() { return g_stall_producer.load(std::memory_order_relaxed) != 0; }
 
 bool pdl_enabled() {
@@ -648,6 +650,8 @@ const char* lr_status_string(lr_status st) {
 const char* lr_last_error(void) { return g_err; }
 
 void lr_test_stall_producer(int32_t on) { g_stall_producer.store(on != 0 ? 1 : 0); }
+
+void lr_test_attention_kernel(int32_t which) { g_attention_kernel.store(which); }
 
 void lr_test_prefill_schedule(int32_t lag, int32_t group) {
   g_prefill_lag.store(lag > 0 ? lag : (lag < 0 ? -1 : 0));

@@ -472,8 +472,34 @@ struct AttnPlan {
   size_t ml_off, bytes;
 };
 
+// Key ranges of the tensor-core tiles are no shorter than this.  256 sequences
+// with heads of 64 behind 1500 tokens: 27, 26, 25, 29, 38 us with 1, 2, 4, 8, 16;
+// long contexts fill the GPU with longer ranges and do not depend on it.
 constexpr int kMinSteps = 4;
 constexpr int kMostHeads = 64;  // query heads a key head: a tile has two query rows at least
+
+// Rows or tiles.  A call on the tiles starts 8 to 10 us later (its CTAs take a
+// whole SM each, set up TMEM and a pipeline of five roles, and end through
+// TMEM), and after that it is the faster one wherever a tile's 128 rows are used.
+// The rows kernel takes 3.7 us for each wave of CTAs (two an SM with heads of 128,
+// four with 64) and reads the keys once for every 16 rows, 512 bytes for a key of
+// 128 elements, from L2 at 8 TB/s (16e3 keys a us).  It is taken when that comes
+// to 12 us at most, and always when all rows fit one tile of it.  Measured
+// (rows, tiles), all of 64 heads over 8: 4 rows behind 200 tokens 13, 22 us; 8
+// behind 2000 23, 25; 15 behind 1300 22, 25; 8 behind 16000 45, 32; 94 behind 119
+// 28, 26; 1 behind 128000 93, 102.  100 calls of other shapes agree within 2 us but
+// for one (96 rows in 3 sequences of 32 heads: tiles 30, rows 26).
+bool by_rows(int64_t M, int64_t mq, int G, const lr_attn_desc* d, int64_t cap_prefix, int64_t cap_own) {
+  const int forced = test_attention_kernel();
+  if (forced != 0) return forced == 1;
+  if (M * G <= kRowsTile) return true;
+  const double kv = d->cache.n_kv_heads;
+  const double shared = kv * static_cast<double>(cdiv(M * G, kRowsTile));
+  const double own = kv * static_cast<double>(cdiv(mq * G, kRowsTile)) * static_cast<double>(d->n_seq);
+  const double wide = d->cache.head_dim / 128.0;
+  const double keys = (shared * static_cast<double>(cap_prefix) + own * static_cast<double>(cap_own)) * wide;
+  return 3.7 * wide * (shared + own) / (2.0 * num_sms()) + keys / 16e3 <= 12.0;
+}
 
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   AttnPlan a;
@@ -483,7 +509,7 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   const int64_t cap_prefix = static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows;
   const int64_t cap_own = static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows;
   const int64_t pair = 2 * attn_tile_rows(G);
-  a.tiles = M * G > kRowsTile;
+  a.tiles = !by_rows(M, mq, G, d, cap_prefix, cap_own);
   // (the packed lists hold a sequence's number in 16 bits)
   a.whole = a.tiles && d->n_seq > 0 && (mq * G > 64 || (d->q_start != nullptr && d->n_seq > 32767));
   if (a.tiles) {
@@ -500,8 +526,11 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
     a.two = a.tile_slots > 1 && (a.whole || cdiv(M, attn_tile_rows(G)) % 2 == 1);
     a.prefix_slots = a.tile_slots > 1 ? a.tile_slots * (a.two ? 2 : 1) : 0;
   } else {
-    a.prefix_slots = slots_for(cdiv(M * G, kRowsTile) * kv, cap_prefix, num_sms() * 4, 128);
-    a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, num_sms() * 4, 128);
+    // One wave: a row of 64 heads over 8 behind 16000 tokens takes 24, 26, 32 us
+    // with 1, 2, 4 CTAs an SM, one of 32 over 32 behind 60000 167, 156, 155.
+    const int64_t want = num_sms() * 2;
+    a.prefix_slots = slots_for(static_cast<int64_t>(cdiv(M * G, kRowsTile)) * kv, cap_prefix, want, 128);
+    a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, want, 128);
   }
   const size_t rows = static_cast<size_t>(M) * d->n_heads * (a.prefix_slots + a.own_slots);
   a.ml_off = (rows * d->cache.head_dim * 4 + 255) / 256 * 256;

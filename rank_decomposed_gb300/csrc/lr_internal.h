@@ -214,5 +214,7 @@ bool pdl_enabled();
 // Fault-injection hook of the bounded-wait tests (lr_test_stall_producer):
 // while set, the decode kernels' weight producers issue no copy.
 bool test_stall_producer();
+// Kernel of the attention fixed by lr_test_attention_kernel (0: by the rule).
+int test_attention_kernel();
 
 }  // namespace lr

@@ -101,12 +101,10 @@ def _attn(d=None, M=9, q=0x10000, ldq=1024, out=0x20000, ldo=1024, dt=lr.LR_BF16
 def test_prefix_attention_refusals_launch_nothing():
     assert _attn(M=0) == lr.LR_OK
     bad, no = lr.LR_ERR_INVALID_ARG, lr.LR_ERR_UNSUPPORTED
-    long = _desc(cap_prefix_blocks=100)   # several key ranges, whose results meet in the workspace
-    need = lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(long))
+    need = lr.lib.lr_prefix_attention_workspace_bytes(9, ctypes.byref(_desc()))
     assert need > 0
-    for kw in (dict(ws=None), dict(ws=0x30010), dict(ws_bytes=need - 1)):
-        assert _attn(d=long, **kw) == bad, kw
-    for kw in (dict(q=None), dict(out=None), dict(q=0x10002), dict(ldq=1000), dict(ldo=1028), dict(dt=3), dict(M=-1)):
+    for kw in (dict(q=None), dict(out=None), dict(q=0x10002), dict(ldq=1000), dict(ldo=1028), dict(dt=3), dict(M=-1),
+               dict(ws=None), dict(ws=0x30010), dict(ws_bytes=need - 1)):
         assert _attn(**kw) == bad, kw
     for kw in (dict(n_heads=7), dict(n_heads=0), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
                dict(prefix_blocks=None), dict(prefix_len=None), dict(cap_prefix_blocks=-1), dict(n_seq=-1),
@@ -124,8 +122,7 @@ def test_workspace_covers_capacities_and_is_zero_for_nothing():
     f = lambda M, **kw: lr.lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(_desc(**kw)))
     assert f(0) == 0 and f(-3) == 0
     assert lr.lib.lr_prefix_attention_workspace_bytes(9, None) == 0
-    assert f(9, cap_prefix_blocks=200) >= f(9, cap_prefix_blocks=100) > 0
-    assert f(9) == 0   # one key range: nothing to join
+    assert f(9, cap_prefix_blocks=100) >= f(9) > 0
 
 
 def test_workspace_of_refused_head_groups_is_zero():
