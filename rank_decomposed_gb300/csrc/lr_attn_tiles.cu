@@ -2,31 +2,38 @@
 // prefix against all rows of the batch, and whole ragged turns (prefix and own
 // tokens in one pass).
 //
+//   S = Q K^T;  P = 2^(scale log2(e) S - m);  O = sum P V;  l = sum P;  out = O / l
+// in one walk over the keys, with the running maximum m of each row.
+//
 // Rows are query rows times the G query heads of one key head: a tile is
 // floor(128 / G) query rows, so its G heads share every key that is loaded.
 // A CTA holds two row tiles, or, when there are rows for one tile only, one row
 // tile against alternate keys twice; either way two independent softmax rings
 // keep the tensor pipe busy while the other one's powers are computed.  It walks
 // steps, one key tile of 128 keys a ring; the steps of a row tile pair are cut
-// into `slots` ranges, one a CTA.
+// into `slots` ranges, one a CTA, and a second kernel joins their results.
 //   whole turns: the tiles are of one sequence's query rows; its prefix and own
 //     key tiles serve both rings.
 //   packed rows: the tiles are of any query rows of the batch, 16 or more
 //     sequences of one row each as a rule.  A prefix tile serves both rings; the
-//     own tokens of each sequence follow as tiles of their own, in the ring that
-//     holds its rows.  Only these rows take part: the other lanes' output is
-//     disabled in the product, so that no sequence's values, NaN or infinite as
-//     they may be, reach another's.  A tile of own tokens costs the tensor pipe
-//     as much for 8 rows as for 128 (1024 cycles), but its 64 KB take 2800 cycles
-//     of the SM's share of memory bandwidth, and the prefix's softmax, the reads
-//     of own tokens and their products overlap in one pipeline: against a second
-//     kernel for the own tokens, 64 sequences behind 8192 tokens took KXX us
-//     instead of 48.
+//     own tokens of the sequences follow in tiles of the ring that holds their
+//     rows, each sequence's in groups of 16 keys one after another, so that a
+//     tile holds up to eight sequences.  The product of a group's 16 keys has the
+//     output lanes of all other sequences' rows disabled: no sequence's values,
+//     NaN or infinite as they may be, reach another's.  (A tile for each
+//     sequence's last tokens instead: 100 sequences of 56 heads with up to 50 own
+//     tokens 110 us, so 41.  The own tokens in a second kernel beside this one:
+//     64 sequences behind 8192 tokens 62 us, then, in one pass, 48.)
+// A sequence is taken whole when its rows times G may pass 64: 40 turns of 4, 8,
+// 16, 32 rows and G = 8 behind 2000 tokens take 75, 75, 77, 111 us whole and 40,
+// 50, 87, 128 us packed; 20 of 16, 40, 64, 100 rows and G = 1 120, 121, 122, 127
+// whole and 52, 63, 103, 116 packed.
 //   warps 0-3, 4-7  softmax of ring 0 and 1, one row per thread;
-//   warps 8-11      load K and V tiles of 128 keys;
-//   warp 14         looks the tiles' pages up, some tiles ahead of the loads: a
-//                   page's number takes a trip to memory, in which a loading
-//                   warp would load nothing;
+//   warps 8-11      load K and V tiles of 128 keys (three warps: 250 us for
+//                   ragged turns of 33 to 300 rows behind 4096 tokens, four 237);
+//   warp 14         looks the tiles' pages up, four tiles in one trip to memory
+//                   and some tiles ahead of the loads: a loading warp that waited
+//                   for a page's number would load nothing;
 //   warp 13         hands landed tiles on: the copies write shared memory by the
 //                   generic proxy and the products read it by the async one, and
 //                   the fence between the two takes some 400 cycles, which the
@@ -34,7 +41,10 @@
 //   warp 12         tcgen05.mma issue: S = Q K^T (Q, K in shared memory) and
 //                   O += P V (P in TMEM, where the softmax warps put it over
 //                   S; V in shared memory as it lies in the cache, keys along
-//                   the reduction, which is the operand's MN-major form).
+//                   the reduction, which is the operand's MN-major form).  A
+//                   second issuing warp, one a ring, took 320 us for the ragged
+//                   turns instead of 243: each more warp role costs the others
+//                   issue slots and instruction cache.
 // The tiles come by 16-byte asynchronous copies into the layout of the 128-byte
 // swizzle.  A page may be 16 rows long and a TMA box cannot cross one: sixteen
 // boxes a tile took 1340 cycles from L2, where one 128-row box takes 630, and
@@ -48,6 +58,16 @@
 // The running maximum moves only when it would grow by more than 2^8 in the
 // powers: until then powers up to 256 are summed against the older maximum
 // (exact in fp32 and in bf16's range), and O in TMEM needs no rescaling.
+//
+// Bound: a step's four products of 128 x 128 x 128 are 2048 cycles of the tensor
+// pipe (heads of 128), and a step takes some 2900: its two softmaxes are 942
+// cycles each for a warp alone on its scheduler and 1410 with two, plus the
+// hand-overs from product to softmax and back.  A CTA's first score comes some 5
+// us after its start (lengths, pages, keys: three trips to memory one after
+// another) and its results take 4 us more after its last product.  Measured, with
+// heads of 128 and 64 over 8: 12 ragged turns 247 us (tensor floor 143), 64
+// sequences behind 8192 tokens 46 us with the join (bytes 15), 5 behind 131000 92
+// us (bytes 80: 87 % of the copy rate).
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -75,7 +95,7 @@ struct Shape {
   static constexpr int kChunkBytes = 128 * 128;        // 128 rows of 64 bf16
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kSlots = HD == 128 ? 5 : 10;    // ring of K and V tiles
-  static constexpr int kTail = 3072;                   // barriers and the lists of own tokens
+  static constexpr int kTail = 3 * 1024;                  // barriers and the lists of own tokens
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + kTail;
 };
 
@@ -282,7 +302,7 @@ struct __align__(16) Tail {
   int16_t seq[2][128];
   int groups[2][128];
 };
-static_assert(sizeof(Tail) <= 3072, "the tail of shared memory");
+static_assert(sizeof(Tail) <= Shape<64>::kTail, "the tail of shared memory");
 
 template <int HD, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -418,7 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int list0 = np + own0, list1 = dual ? list0 : np + own1;
   const int e0 = dual ? (list0 + 1) >> 1 : list0, e1 = dual ? list0 >> 1 : list1;  // steps that ring 0, 1 take
   const int64_t steps = e0 > e1 ? e0 : e1;
-  const int s_lo = static_cast<int>(steps * split / a.slots), s_hi = static_cast<int>(steps * (split + 1) / a.slots);
+  // The ranges are equal in time: a step of packed own tokens loads a tile for
+  // each ring and takes 5/4 of the time of a prefix step (64 sequences of up to 512
+  // own tokens behind 8192 shared: 57, 52, 48, 48, 50 us with 3, 4, 5, 6, 8 quarters;
+  // 200 of 300 behind 1000: 63, 59, 59, 56, 61; MHA of 1000 behind 4099: 73, 71, 71, 73, 77).
+  const int64_t shared_steps = dual ? (np + 1) >> 1 : np;
+  auto cut = [&](int i) {
+    if (WHOLE) return static_cast<int>(steps * i / a.slots);
+    const int at = static_cast<int>((4 * shared_steps + 5 * (steps - shared_steps)) * i / a.slots);  // quarters of a prefix step
+    const int more = at - 4 * static_cast<int>(shared_steps);
+    return more <= 0 ? at / 4 : static_cast<int>(shared_steps) + more / 5;
+  };
+  const int s_lo = cut(split), s_hi = cut(split + 1);
   auto of_range = [&](int e) {
     const int c = (e < s_hi ? e : s_hi) - s_lo;
     return c < 0 ? 0 : c;

@@ -14,6 +14,13 @@
 // and the gains of its lanes in registers and walks several heads of one row
 // with them: read per head, the angles (64 bytes a lane) would be four times
 // the head's own bytes.
+// Measured: 8191 rows of 64 + 8 heads of 128 in 63 us (302 MB and the angles: 4.9
+// TB/s; a plain copy of the same bytes between two fresh buffers takes 50), an
+// append of 4099 rows of 32 + 32 heads 24 us (134 MB, 5.6 TB/s), 64 rows of a
+// decode step 6 us, one token 5 us, of which 3 are the launch and two trips to
+// memory (positions, then angles) the rest.  Streaming hints on loads and stores
+// changed nothing, the next heads asked for before the present ones are worked on
+// took 64 us for the first and 25 to 31 for the second.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -102,7 +109,9 @@ __device__ __forceinline__ void partners(const Raw<true>& r, float (&y)[8], int 
 constexpr int kFlight = 4;
 // Small CTAs: a warp of few heads that is done makes room at once.
 constexpr int kHeadWarps = 2, kHeadCtas = 12;
-constexpr int kMostRounds = 2;  // of kFlight heads, for one warp
+// Rounds of kFlight heads for one warp, at most.  1, 2, 4, 8: 8191 rows 71, 67, 68,
+// 90 us cold, the append of 4099 rows 28, 25, 24, 24, 2000 rows 24, 23, 26, 30.
+constexpr int kMostRounds = 2;
 
 enum { ROT_NONE = 0, ROT_OF_HALVES = 1, ROT_OF_PAIRS = 2 };
 
@@ -313,7 +322,8 @@ lr_status launch_heads(HeadParams& p, const lr_head_map* hm, lr_dtype in_dtype, 
   p.cos_sin = hm->cos_sin;
   p.max_pos = hm->max_pos;
   // Heads per warp: one a group while the rows do not fill the GPU (16 warps an
-  // SM), then more, so that the angles are read once for them.
+  // SM), then more, so that the angles are read once for them.  (4, 16 or 64 warps:
+  // 256 fp32 rows of 64 heads 11, 10, 14 us, 500 rows 13, 12, 13.)
   const int groups = 32 / p.lanes;
   const int64_t want = static_cast<int64_t>(num_sms()) * 16;
   auto warps_of = [&](int kind) { return (p.heads[kind] + p.chunk - 1) / p.chunk; };
