@@ -11,6 +11,7 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "lr_attn.h"
@@ -754,9 +755,14 @@ lr_status lr_block_forward_cached(float* h, int64_t M, const lr_block_desc* b, c
   // Both parts' arguments, before anything is enqueued.
   st = check_context(M, ctx, bc.out, bc.ws, bc.ws_bytes);
   if (st != LR_OK) return st;
-  std::vector<Step> steps;
-  block_steps(h, M, b, ws, steps, &bc);
-  return enqueue_steps(steps, M, dev_status, reinterpret_cast<cudaStream_t>(s));
+  try {
+    std::vector<Step> steps;
+    block_steps(h, M, b, ws, steps, &bc);
+    return enqueue_steps(steps, M, dev_status, reinterpret_cast<cudaStream_t>(s));
+  } catch (const std::bad_alloc&) {
+    set_error("block: out of host memory");
+    return LR_ERR_STATE;
+  }
 }
 
 lr_status remap_compact(const void* pool, int64_t pool_rows, int64_t row_bytes,
