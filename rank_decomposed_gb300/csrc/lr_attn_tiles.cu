@@ -51,6 +51,9 @@
 // the products of two rings take 2048 for two tiles.  The copies also fill with
 // zeros where no token lies, so that whatever a last page holds behind its
 // tokens stays out (0 * NaN would be NaN).
+// P is handed on in halves of its keys (in one piece: ragged turns 267 us, 253),
+// and the products themselves release the tiles (the softmax warps instead, once
+// they see the next scores: 259).
 // The order of the products is  S0 S1 | PV0 S0' PV1 S1' | ...: S0' needs
 // softmax 0 to be through with S0 (its P has been consumed by PV0, issued just
 // before), and runs while softmax 1 works.
@@ -60,9 +63,13 @@
 // (exact in fp32 and in bf16's range), and O in TMEM needs no rescaling.
 //
 // Bound: a step's four products of 128 x 128 x 128 are 2048 cycles of the tensor
-// pipe (heads of 128), and a step takes some 2900: its two softmaxes are 942
-// cycles each for a warp alone on its scheduler and 1410 with two, plus the
-// hand-overs from product to softmax and back.  A CTA's first score comes some 5
+// pipe (heads of 128), and a step takes some 2900.  Shared memory is as busy: S
+// reads Q and K, 8 KB in the 64 cycles of a product, which is all of its 128
+// bytes a cycle, and with V and the tiles coming in that makes 2048 cycles, too,
+// so that copies delay products.  The two softmaxes are 942 cycles each for a
+// warp alone on its scheduler and 1410 with two, 512 of them the exponentials,
+// and the issuing warp, which shares its scheduler with two of them, takes 50 to
+// 100 cycles for each of its six waits.  A CTA's first score comes some 5
 // us after its start (lengths, pages, keys: three trips to memory one after
 // another) and its results take 4 us more after its last product.  Measured, with
 // heads of 128 and 64 over 8: 12 ragged turns 247 us (tensor floor 143), 64
