@@ -43,8 +43,8 @@
 //                   S; V in shared memory as it lies in the cache, keys along
 //                   the reduction, which is the operand's MN-major form).  A
 //                   second issuing warp, one a ring, took 320 us for the ragged
-//                   turns instead of 243: each more warp role costs the others
-//                   issue slots and instruction cache.
+//                   turns instead of 243, and 275 instead of 251 with the turns
+//                   handed from one to the other.
 // The tiles come by 16-byte asynchronous copies into the layout of the 128-byte
 // swizzle.  A page may be 16 rows long and a TMA box cannot cross one: sixteen
 // boxes a tile took 1340 cycles from L2, where one 128-row box takes 630, and
@@ -63,13 +63,14 @@
 // (exact in fp32 and in bf16's range), and O in TMEM needs no rescaling.
 //
 // Bound: a step's four products of 128 x 128 x 128 are 2048 cycles of the tensor
-// pipe (heads of 128), and a step takes some 2900.  Shared memory is as busy: S
-// reads Q and K, 8 KB in the 64 cycles of a product, which is all of its 128
-// bytes a cycle, and with V and the tiles coming in that makes 2048 cycles, too,
-// so that copies delay products.  The two softmaxes are 942 cycles each for a
-// warp alone on its scheduler and 1410 with two, 512 of them the exponentials,
-// and the issuing warp, which shares its scheduler with two of them, takes 50 to
-// 100 cycles for each of its six waits.  A CTA's first score comes some 5
+// pipe (heads of 128), and a step takes some 2950, by latency: a ring's scores are
+// seen 250 cycles after their last product, loaded 200 later, their maximum known
+// after 400 more and the first half of P after another 400 (512 cycles of each
+// softmax are the exponentials, and two warps share a scheduler), and every wait
+// of the issuing warp queues behind the products that it issued.  No resource is
+// full by itself: the ragged turns take 250 us, and in copies made for timing 248
+// with an eighth of the loads, 242 without the exponentials, 234 with half of the
+// products of S.  A CTA's first score comes some 5
 // us after its start (lengths, pages, keys: three trips to memory one after
 // another) and its results take 4 us more after its last product.  Measured, with
 // heads of 128 and 64 over 8: 12 ragged turns 247 us (tensor floor 143), 64
