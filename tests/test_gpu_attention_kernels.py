@@ -32,6 +32,23 @@ def test_more_shapes(nh, nkv, hd, prefix, lens, qs):
     close(out, *b.want())
 
 
+@pytest.mark.parametrize("qs", [[0, 30, 200], [0, 1, 2]])
+def test_a_prefix_length_is_reported_when_the_first_sequence_has_no_rows(qs):
+    b = Batch(33, 8, 2, 64, 64, [5, 40, 208], qs=qs, pcap=4)
+    b.d["prefix_len"].fill_(65)
+    close(b.run(), *b.want())
+    assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE
+
+
+@pytest.mark.parametrize("nh,nkv,hd,n", [(8, 1, 128, 700), (4, 4, 64, 513)])
+def test_a_prompt_alone(nh, nkv, hd, n):
+    """Many row tiles of one sequence, the last of them first: every row sees itself and what is before it."""
+    b = Batch(34, nh, nkv, hd, 0, [n], qs=[n])
+    out = b.run()
+    assert int(b.status.item()) == 0
+    close(out, *b.want())
+
+
 def test_a_stalled_load_is_reported_and_the_next_call_is_right(kernel):
     """The producers of the tiles issue nothing: every wait of the launch runs out, and it returns."""
     for qs in (None, [30, 1, 200]):
