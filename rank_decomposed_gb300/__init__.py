@@ -149,6 +149,7 @@ def _load():
 
 
 lib = _load()
+from . import _calls  # noqa: E402  (built beside liblr.so)
 
 
 def status_string(st: int) -> str:
@@ -443,64 +444,37 @@ def kv_reconstruct_paged(latent_pool, blocks, n_blocks, Bt, out, status, stream=
 
 
 # ------------------------------------------------- attention over a context
-# These calls sit in a decode step whose kernels take a few microseconds, so
-# their checks read each tensor's properties once.
-_torch = None
-_raw_stream = None
+# These calls sit in a decode step whose kernels take a few microseconds: their
+# arguments are checked and put together in C (csrc/lr_calls.c).
+_ready = False
 
 
-def _th():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
+def _first_use():
+    global _ready
+    import torch
+    f = [ctypes.cast(x, ctypes.c_void_p).value for x in (lib.lr_qk_norm_rope, lib.lr_kv_append, lib.lr_prefix_attention)]
+    _calls.init(torch.bfloat16, torch.float32, torch.int32, *f)
+    _ready = True
 
 
-def _stream_of(stream):
-    """The raw handle of `stream`, or of the current stream of the current device."""
-    global _raw_stream
-    if stream is not None:
-        return getattr(stream, "cuda_stream", stream)
-    if _raw_stream is None:
-        c = _th()._C
-        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
-            _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
-        else:
-            _raw_stream = lambda: _torch.cuda.current_stream().cuda_stream  # noqa: E731
-        _torch.cuda.init()
-    return _raw_stream()
+def _current_stream():
+    """The raw handle of the current stream of the current device; its first call finds the quickest way to it."""
+    global _current_stream
+    import torch
+    torch.cuda.init()
+    c = torch._C
+    if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+        _current_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
 
 
-def _i32(t, name, dims=1):
-    if t is None:
-        return None
-    if t.dtype != _th().int32 or t.dim() != dims or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous %d-D int32 tensor" % (name, dims))
-    return t.data_ptr()
-
-
-def _per_row(t, name, m):
-    if t is None:
-        return None
-    if t.dtype != _th().int32 or t.shape != (m,) or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous int32 tensor with one entry a row" % name)
-    return t.data_ptr()
-
-
-def _mat(t, name, dtype, rows=None, cols=None):
-    """(pointer, row stride, rows, columns) of a row-major matrix of `dtype`."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
-        raise ValueError("%s must be a row-major 2-D tensor" % name)
-    n, w = shape
-    if (rows is not None and n != rows) or (cols is not None and w != cols):
-        raise ValueError("%s must be [%s][%s]" % (name, rows, cols))
-    # one row's stride says nothing: it counts as at least the row's width
-    ld = strides[0] if n > 1 or strides[0] >= w else (w + 7) // 8 * 8
-    return t.data_ptr(), ld, n, w
+def _call(stream):
+    """Before a call of _calls: the raw handle of its stream."""
+    if not _ready:
+        _first_use()
+    return _current_stream() if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0):
@@ -524,23 +498,9 @@ class HeadMap:
     rot_style: int = ROT_HALF
     cos_sin: object = None   # device fp32 [max_pos][rot_dim], see rope_table
 
-    def _gain(self, g, name):
-        if g is None:
-            return None
-        if g.dtype != _th().bfloat16 or g.shape != (self.head_dim,) or not g.is_contiguous():
-            raise TypeError("%s must be a contiguous bfloat16 [head_dim] tensor" % name)
-        return g.data_ptr()
-
     def c(self) -> HeadMapDesc:
-        table, n = None, 0
-        if self.rot_dim > 0 and self.cos_sin is not None:
-            t = self.cos_sin
-            n = t.shape[0]
-            if t.dtype != _th().float32 or t.shape != (n, self.rot_dim) or not t.is_contiguous():
-                raise TypeError("cos_sin must be a contiguous float32 [max_pos][rot_dim] tensor")
-            table = t.data_ptr()
-        return HeadMapDesc(self.head_dim, 1 if self.norm else 0, self.eps, self._gain(self.q_gain, "q_gain"),
-                           self._gain(self.k_gain, "k_gain"), self.rot_dim, self.rot_style, table, n)
+        _call(0)
+        return HeadMapDesc.from_buffer_copy(_calls.head_map(self))
 
 
 @dataclass
@@ -553,29 +513,8 @@ class PagedKV:
     block_rows: int = 16
 
     def c(self) -> KvCache:
-        bf16 = _th().bfloat16
-        kp, ld, n, w = _mat(self.k_pool, "k_pool", bf16)
-        vp, ldv, _, _ = _mat(self.v_pool, "v_pool", bf16, n, w)
-        if ldv != ld:
-            raise ValueError("k_pool and v_pool must have one row stride")
-        if w < self.n_kv_heads * self.head_dim:
-            raise ValueError("the pools' rows are narrower than n_kv_heads * head_dim")
-        br = self.block_rows
-        if br <= 0 or n % br:
-            raise ValueError("the pools' rows must be whole pages of block_rows")
-        return KvCache(kp, vp, ld, n // br, br, self.n_kv_heads, self.head_dim)
-
-
-def _dtype_code(t):
-    torch = _th()
-    if t.dtype == torch.bfloat16:
-        return LR_BF16
-    if t.dtype == torch.float32:
-        return LR_F32
-    raise TypeError("a tensor of heads must be bfloat16 or float32")
-
-
-_NONE = (None, 0, None, 0)
+        _call(0)
+        return KvCache.from_buffer_copy(_calls.kv_cache(self))
 
 
 def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None, stream=None):
@@ -583,24 +522,8 @@ def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None,
 
     In place (q_out is q, k_out is k) is allowed for bf16 inputs.
     """
-    hd = heads.head_dim
-    first = q if q is not None else k
-    if first is None or hd <= 0:
-        raise ValueError("qk_norm_rope: q or k and a positive head_dim are needed")
-    code, dt, bf16, m = _dtype_code(first), first.dtype, _torch.bfloat16, None
-    (qp, ldq, wq, _), (qo, ldqo), (kp, ldk, wk, _), (ko, ldko) = _NONE, (None, 0), _NONE, (None, 0)
-    wq = wk = 0
-    if q is not None:
-        qp, ldq, m, wq = _mat(q, "q", dt)
-        qo, ldqo, _, _ = _mat(q_out, "q_out", bf16, m, wq)
-    if k is not None:
-        kp, ldk, m, wk = _mat(k, "k", dt, m)
-        ko, ldko, _, _ = _mat(k_out, "k_out", bf16, m, wk)
-    if wq % hd or wk % hd:
-        raise ValueError("qk_norm_rope: a width is not whole heads of head_dim")
-    st = lib.lr_qk_norm_rope(qp, ldq, wq // hd, kp, ldk, wk // hd, code, m, _per_row(pos, "pos", m),
-                             _i32(n_active, "n_active"), ctypes.byref(heads.c()), qo, ldqo, ko, ldko, _ptr(status),
-                             _stream_of(stream))
+    s = _call(stream)
+    st = _calls.qk_norm_rope(q, k, pos, heads, q_out, k_out, status, n_active, s)
     if st != LR_OK:
         _check("lr_qk_norm_rope", st)
 
@@ -608,39 +531,17 @@ def qk_norm_rope(q, k, pos, heads: HeadMap, q_out, k_out, status, n_active=None,
 def kv_append(k, v, pos, rows, heads: HeadMap, cache: PagedKV, status, q=None, q_out=None, n_active=None,
               stream=None):
     """cache rows rows[m] = (norm and rotation of k[m], v[m]); with q also q_out as qk_norm_rope. One launch."""
-    hd = heads.head_dim
-    code, dt = _dtype_code(k), k.dtype
-    kp, ldk, m, w = _mat(k, "k", dt, None, cache.n_kv_heads * cache.head_dim)
-    vp, ldv, _, _ = _mat(v, "v", dt, m, w)
-    qp, ldq, wq, qo, ldqo = None, 0, 0, None, 0
-    if q is not None:
-        qp, ldq, _, wq = _mat(q, "q", dt, m)
-        qo, ldqo, _, _ = _mat(q_out, "q_out", _torch.bfloat16, m, wq)
-        if hd <= 0 or wq % hd:
-            raise ValueError("kv_append: q's width is not whole heads of head_dim")
-        wq //= hd
-    st = lib.lr_kv_append(kp, ldk, vp, ldv, qp, ldq, wq, code, m, _per_row(pos, "pos", m), _per_row(rows, "rows", m),
-                          _i32(n_active, "n_active"), ctypes.byref(heads.c()), ctypes.byref(cache.c()), qo, ldqo,
-                          _ptr(status), _stream_of(stream))
+    s = _call(stream)
+    st = _calls.kv_append(k, v, pos, rows, heads, cache, status, q, q_out, n_active, s)
     if st != LR_OK:
         _check("lr_kv_append", st)
 
 
-def _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale):
-    n_seq = lengths.shape[0]
-    if block_table.shape[0] != n_seq:
-        raise ValueError("block_table must be [n_seq][blocks_per_seq]")
-    if q_start is not None and q_start.shape[0] != n_seq + 1:
-        raise ValueError("q_start must have n_seq + 1 entries")
-    return AttnDesc(cache.c(), n_heads, cache.head_dim ** -0.5 if scale is None else scale,
-                    _i32(prefix_blocks, "prefix_blocks"), 0 if prefix_blocks is None else prefix_blocks.shape[0],
-                    _i32(prefix_len, "prefix_len"), n_seq, _i32(q_start, "q_start"), max_q,
-                    _i32(block_table, "block_table", 2), block_table.shape[1], _i32(lengths, "lengths"))
-
-
 def prefix_attention_workspace_bytes(M: int, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len, block_table,
                                      lengths, q_start=None, max_q: int = 1) -> int:
-    d = _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, None)
+    _call(0)
+    d = AttnDesc.from_buffer_copy(_calls.attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths,
+                                                   q_start, max_q, None))
     return int(lib.lr_prefix_attention_workspace_bytes(M, ctypes.byref(d)))
 
 
@@ -651,12 +552,9 @@ def prefix_attention(q, n_heads: int, cache: PagedKV, prefix_blocks, prefix_len,
     q: bf16 [M][n_heads * head_dim]; out: bf16 or fp32, the same shape.  Sequence b's rows are
     q_start[b]..q_start[b + 1] - 1 (row b without q_start), its last own tokens.
     """
-    odt = _dtype_code(out)
-    qp, ldq, m, w = _mat(q, "q", _torch.bfloat16, None, n_heads * cache.head_dim)
-    op, ldo, _, _ = _mat(out, "out", out.dtype, m, w)
-    d = _attn_desc(n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, q_start, max_q, scale)
-    st = lib.lr_prefix_attention(qp, ldq, op, ldo, odt, m, ctypes.byref(d), _ptr(workspace),
-                                 0 if workspace is None else workspace.nbytes, _ptr(status), _stream_of(stream))
+    s = _call(stream)
+    st = _calls.prefix_attention(q, n_heads, cache, prefix_blocks, prefix_len, block_table, lengths, out, workspace,
+                                 status, q_start, max_q, scale, s)
     if st != LR_OK:
         _check("lr_prefix_attention", st)
 
@@ -679,10 +577,8 @@ class Context:
     n_active: object = None
 
     def c(self, M: int, n_heads: int) -> ContextDesc:
-        attn = _attn_desc(n_heads, self.cache, self.prefix_blocks, self.prefix_len, self.block_table, self.lengths,
-                          self.q_start, self.max_q, self.scale)
-        return ContextDesc(attn, self.heads.c(), _per_row(self.pos, "pos", M), _per_row(self.rows, "rows", M),
-                           _i32(self.n_active, "n_active"))
+        _call(0)
+        return ContextDesc.from_buffer_copy(_calls.context(self, M, n_heads))
 
 
 def block_cached_scratch_bytes(M: int, b: Block, ctx: Context) -> int:
@@ -691,11 +587,12 @@ def block_cached_scratch_bytes(M: int, b: Block, ctx: Context) -> int:
 
 def block_forward_cached(h, b: Block, ctx: Context, scratch, status, stream=None):
     """One decomposed block with attention over its cached context, applied in place to h [M][d_model] (fp32)."""
-    if h.dtype != _th().float32 or not h.is_contiguous():
+    import torch
+    if h.dtype != torch.float32 or not h.is_contiguous():
         raise TypeError("h must be a contiguous float32 tensor")
     bc, cc = b.c(), ctx.c(h.shape[0], b.n_heads)
     st = lib.lr_block_forward_cached(h.data_ptr(), h.shape[0], ctypes.byref(bc), ctypes.byref(cc), scratch.data_ptr(),
-                                     scratch.nbytes, _ptr(status), _stream_of(stream))
+                                     scratch.nbytes, _ptr(status), _stream(stream))
     _check("lr_block_forward_cached", st)
 
 

@@ -1,7 +1,8 @@
-"""Build liblr.so (the CUDA path) and libsynth.so (the GPU input generator).
+"""Build liblr.so (the CUDA path), _calls.so (argument marshalling of small
+calls) and libsynth.so (the GPU input generator).
 
-Both are compiled in-tree for sm_103a only, with nvcc, one translation unit
-per process so a build takes well under a minute.
+All are compiled in-tree, the CUDA code for sm_103a only, with nvcc, one
+translation unit per process so a build takes well under a minute.
 """
 
 from __future__ import annotations
@@ -10,12 +11,15 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblr.so")
+CALLS_SRC = os.path.join(CSRC, "lr_calls.c")
+CALLS_LIB = os.path.join(PKG, "_calls.so")
 SYNTH_SRC = os.path.join(ROOT, "synth", "synth_gen.cu")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 SYNTH_HOST_SRC = os.path.join(ROOT, "synth", "synth_host.c")
@@ -56,11 +60,14 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                  SYNTH_SRC, "-o", SYNTH_LIB]
     host_cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c99", "-fopenmp", "-fPIC", "-shared",
                 SYNTH_HOST_SRC, "-o", SYNTH_HOST_LIB]
+    calls_cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-I",
+                 sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), CALLS_SRC, "-o", CALLS_LIB]
     logs = []
     with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
         futs = [ex.submit(_run, cmd) for cmd, _ in jobs]
         futs.append(ex.submit(_run, synth_cmd))
         futs.append(ex.submit(_run, host_cmd))
+        futs.append(ex.submit(_run, calls_cmd))
         for f in futs:
             logs.append(f.result())
     _run([exe, *ARCH, "-shared", "-o", LIB, *[o for _, o in jobs], "-lcudart_static"])

@@ -182,6 +182,72 @@ def test_status_string_of_index_range():
     assert "range" in lr.status_string(lr.LR_ERR_INDEX_RANGE)
 
 
+# ---------------------------------------------------------------- binding
+def test_binding_refuses_wrong_tensors():
+    """Types, shapes and strides that the calls cannot take; no call reaches a GPU (streams are numbers here)."""
+    torch = pytest.importorskip("torch")
+    b16 = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    hm = lambda **kw: lr.HeadMap(**dict(dict(head_dim=64, norm=True, q_gain=b16(64), rot_dim=64,  # noqa: E731
+                                             cos_sin=torch.zeros(8, 64)), **kw))
+    m, st = 0, i32(1)
+
+    def rope(q=b16(m, 128), k=b16(m, 64), pos=i32(m), heads=None, qo=b16(m, 128), ko=b16(m, 64), n=None):
+        lr.qk_norm_rope(q, k, pos, heads or hm(), qo, ko, st, n_active=n, stream=1)
+
+    rope()                                              # no rows: nothing to do
+    rope(q=None, qo=None)
+    for kw in (dict(q=torch.zeros(m, 128).half(), k=None), dict(qo=torch.zeros(m, 128)), dict(k=torch.zeros(m, 64)),
+               dict(pos=torch.zeros(m, dtype=torch.int64)), dict(heads=hm(q_gain=torch.zeros(64))),
+               dict(heads=hm(k_gain=b16(128)[::2])), dict(heads=hm(cos_sin=b16(8, 64))), dict(n=i32(1, 1)),
+               dict(pos=i32(m, 1))):
+        with pytest.raises(TypeError):
+            rope(**kw)
+    for kw in (dict(q=None, k=None), dict(q=b16(m, 100), qo=b16(m, 100)), dict(qo=b16(m, 64)), dict(qo=b16(2, 128)),
+               dict(q=b16(128)), dict(q=b16(128, 3).t()), dict(pos=i32(3)), dict(heads=hm(cos_sin=torch.zeros(8, 32))),
+               dict(heads=hm(q_gain=b16(32))), dict(heads=hm(head_dim=0, q_gain=None))):
+        with pytest.raises(ValueError):
+            rope(**kw)
+    with pytest.raises(OverflowError):
+        rope(heads=hm(rot_style=1 << 40))
+    with pytest.raises(AttributeError):
+        rope(heads=7)
+    with pytest.raises(lr.LrError):
+        rope(heads=hm(eps=-1.0))
+
+    pools = b16(64, 192)
+    cache = lambda **kw: lr.PagedKV(**dict(dict(k_pool=pools[:, :128], v_pool=pools[:, 64:], n_kv_heads=2,  # noqa: E731
+                                                head_dim=64), **kw))
+
+    def append(k=b16(m, 128), v=b16(m, 128), pos=i32(m), rows=i32(m), c=None, q=None, qo=None):
+        lr.kv_append(k, v, pos, rows, hm(), c or cache(), st, q=q, q_out=qo, stream=1)
+
+    append()
+    append(q=b16(m, 256), qo=b16(m, 256))
+    assert cache().c().ld == 192 and cache().c().pool_blocks == 4
+    for kw in (dict(k=b16(m, 64)), dict(v=b16(m, 64)), dict(rows=i32(2)), dict(q=b16(m, 100), qo=b16(m, 100)),
+               dict(c=cache(v_pool=b16(64, 128))), dict(c=cache(block_rows=48)), dict(c=cache(block_rows=0)),
+               dict(c=cache(n_kv_heads=3)), dict(c=cache(k_pool=pools[:32, :128]))):
+        with pytest.raises(ValueError):
+            append(**kw)
+    with pytest.raises(TypeError):
+        append(v=torch.zeros(m, 128))
+
+    def attend(q=b16(m, 256), out=b16(m, 256), pages=i32(3), n=i32(1), table=i32(2, 4), lens=i32(2), start=i32(3)):
+        lr.prefix_attention(q, 4, cache(), pages, n, table, lens, out=out, workspace=None, status=st, q_start=start,
+                            max_q=5, stream=1)
+
+    attend()
+    attend(out=torch.zeros(m, 256), pages=None, n=None)
+    for kw in (dict(q=b16(m, 128)), dict(out=b16(m, 128)), dict(table=i32(3, 4)), dict(start=i32(4))):
+        with pytest.raises(ValueError):
+            attend(**kw)
+    for kw in (dict(q=torch.zeros(m, 256)), dict(lens=None), dict(table=i32(4)), dict(table=i32(4, 2).t()),
+               dict(pages=torch.zeros(3)), dict(out=torch.zeros(m, 256).double())):
+        with pytest.raises(TypeError):
+            attend(**kw)
+
+
 # ------------------------------------------------------------ oracle pins
 def test_oracle_rotation_keeps_pair_norms_and_adds_angles():
     rng = np.random.default_rng(0)
