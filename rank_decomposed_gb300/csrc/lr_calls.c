@@ -1,10 +1,10 @@
 /* Argument marshalling of the calls over a context, as a CPython extension.
  *
  * These calls sit in a decode step whose kernels take a few microseconds, and
- * reading thirty properties of ten tensors from Python took more than the rest
- * of a call (one token's rotation: 9.6 us of the call, 3.4 of them the
- * library's).  Here each property is read once, checked, and put into the
- * structures of lr.h.  Tensors are read by their Python attributes alone, so the
+ * reading thirty properties of ten tensors from Python and converting them by
+ * ctypes took most of a call (one token's rotation: 9.6 us, 3.4 of them the
+ * library's launch; from here 4.9).  Each property is read once, checked, and
+ * put into the structures of lr.h.  Tensors are read by their Python attributes alone, so the
  * extension knows no version of torch.  It holds no state but the functions and
  * types given to init().
  */
