@@ -944,6 +944,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the ring is the other one's too: its products end before it is written below
         if (ok && joins && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
         tc_fence_after();
+      } else if (ok) {
+        // a ring without keys waited for nothing: its Q tile, where the rows are turned
+        // below, may still be on its way here
+        ok = mbar_wait(&bars.q_full, 0, &abort_sh);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) {
