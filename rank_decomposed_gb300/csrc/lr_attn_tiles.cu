@@ -971,7 +971,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     if (joins) named_bar_sync(1, 256);  // the softmax warps
     tc_fence_after();
-    if (!(joins && ringi == 1) && *static_cast<volatile int*>(&abort_sh) == 0) {
+    // (one answer for the warp: another warp may give up just now, and a part of a
+    // warp must not go where its lanes wait for each other)
+    const bool gave_up = __any_sync(0xffffffffu, *static_cast<volatile int*>(&abort_sh) != 0);
+    if (!(joins && ringi == 1) && !gave_up) {
       // ------------------------------------------------- rows to memory
       const int t = ringi;
       const bool busy = (warp & 3) * 32 < live_rows;

@@ -43,3 +43,24 @@ def test_a_row_tile_without_keys_beside_one_with_keys(nh, nkv, hd, lens, qs, bps
         assert int(b.status.item()) == 0
         close(out, want, mag)
         assert not out[torch.from_numpy(~sees).cuda()].any()
+
+
+@pytest.mark.parametrize("nh,nkv,hd,prefix,lens,qs,bps", [
+    (2, 2, 64, 0, [40], [200], 3),                     # one key range, two row tiles, one of them without keys
+    (8, 8, 128, 40, [40], [100], 3),                   # one key range, one row tile on both rings
+    (8, 1, 128, 3000, [90] * 40, None, 8),             # packed rows, several key ranges
+])
+def test_every_warp_gives_up_together(kernel, nh, nkv, hd, prefix, lens, qs, bps):
+    """Loads that never come: the launch reports it and ends whichever of its warps notices first."""
+    if kernel == 1:
+        pytest.skip("the kernel by rows waits for its own copies alone")
+    b = Batch(47, nh, nkv, hd, prefix, lens, qs=qs, bps=bps)
+    lr.lib.lr_test_stall_producer(1)
+    try:
+        b.run()
+    finally:
+        lr.lib.lr_test_stall_producer(0)
+    assert int(b.status.item()) == lr.LR_ERR_TIMEOUT
+    b.status.zero_()
+    close(b.run(), *b.want())
+    assert int(b.status.item()) == 0
