@@ -443,7 +443,8 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   LR_F32); M < 2^31; 16-byte aligned, ldq and ldo multiples of 8 and >=
  *   n_heads * head_dim.
  *   prefix_blocks: device int32 [cap_prefix_blocks]; prefix_len: device int32
- *   (both may be NULL when cap_prefix_blocks is 0: no shared part).
+ *   (both may be NULL when cap_prefix_blocks is 0: no shared part; a prefix_len
+ *   that is given then has the capacity 0).
  *   q_start: device int32 [n_seq + 1], not decreasing, within [0, M]; NULL
  *   when every sequence has one row (M = n_seq then; M > n_seq leaves zero
  *   rows).  max_q: the most rows that a sequence may have (1 for NULL).

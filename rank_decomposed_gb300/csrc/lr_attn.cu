@@ -361,6 +361,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     from = p.q_start[0];
     to = p.n_seq > 0 ? p.q_start[p.n_seq] : from;
   }
+  // A part without pages has no CTA of the rows kernel: what it holds is looked at here.
+  if (p.cap_own == 0)
+    for (int64_t b = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; b < p.n_seq; b += static_cast<int64_t>(gridDim.x) * 256)
+      seq_view(p, static_cast<int>(b), true);
+  if (p.cap_prefix == 0 && p.prefix_len != nullptr && blockIdx.x == 0 && threadIdx.x == 0) prefix_rows(p, *p.prefix_len, true);
   float acc[kE], inv = 0.f;
 #pragma unroll
   for (int j = 0; j < kE; ++j) acc[j] = 0.f;

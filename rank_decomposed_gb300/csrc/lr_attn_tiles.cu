@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int seq_of = WHOLE ? item % p.n_seq : 0;
   const int pair = WHOLE ? a.pairs - 1 - item / p.n_seq : item;
   const bool tell = threadIdx.x == 0 && kvh == 0 && split == 0;
-  const int prefix_len = p.cap_prefix > 0 ? *p.prefix_len : 0;  // on its way while the lists are made
+  const int prefix_len = p.prefix_len != nullptr ? *p.prefix_len : 0;  // on its way while the lists are made
   int q0 = 0, nq = p.M, own = 0, mrel;
   const int32_t* own_pages = nullptr;
   if (WHOLE) {

@@ -6,7 +6,7 @@ import pytest
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import rank_decomposed_gb300 as lr  # noqa: E402
-from test_gpu_attention import Batch, close  # noqa: E402
+from test_gpu_attention import Batch, _i32, close  # noqa: E402
 
 
 @pytest.fixture(autouse=True, params=[1, 2], ids=["rows", "tiles"])
@@ -64,3 +64,43 @@ def test_every_warp_gives_up_together(kernel, nh, nkv, hd, prefix, lens, qs, bps
     b.status.zero_()
     close(b.run(), *b.want())
     assert int(b.status.item()) == 0
+
+
+@pytest.mark.parametrize("prefix,qs", [(64, None), (0, None), (64, [40, 1, 20]), (0, [40, 1, 20]), (64, [2, 1, 3]), (700, None)])
+def test_lengths_and_row_offsets_are_reported_where_there_are_no_pages(prefix, qs):
+    b = Batch(42, 8, 2, 64, prefix, [0, 0, 0], qs=qs)
+    b.d["block_table"] = torch.empty(3, 0, dtype=torch.int32, device="cuda")
+    want = b.want()
+    close(b.run(), *want)
+    assert int(b.status.item()) == 0
+    for bad in (1, -1, 1 << 30):
+        b.status.zero_()
+        b.d["lengths"][1] = bad
+        close(b.run(), *want)
+        assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, bad
+    b.d["lengths"][1] = 0
+    if qs is not None:
+        for i, bad in ((1, b.starts[2] + 1), (2, b.m + 1), (0, -1)):
+            b.status.zero_()
+            b.d["q_start"][i] = bad
+            b.run()
+            assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, (i, bad)
+            b.d["q_start"][i] = b.starts[i]
+        b.status.zero_()
+        b.d["max_q"] -= 1
+        b.run()
+        assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE
+
+
+@pytest.mark.parametrize("lens", [[30, 7, 1], [0, 0, 0]])
+def test_a_prefix_length_is_reported_where_there_are_no_prefix_pages(lens):
+    b = Batch(43, 8, 2, 64, 0, lens)
+    b.d.update(prefix_blocks=torch.empty(0, dtype=torch.int32, device="cuda"), prefix_len=_i32([0]))
+    want = b.want()
+    close(b.run(), *want)
+    assert int(b.status.item()) == 0
+    for bad in (1, -1):
+        b.status.zero_()
+        b.d["prefix_len"].fill_(bad)
+        close(b.run(), *want)
+        assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, bad
