@@ -453,8 +453,9 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   Lengths, pages and row offsets are read on the device: a captured call
  *   serves every batch within the capacities.  A length outside its capacity
  *   (block_rows times the pages it may use) is clamped and reported as
- *   LR_ERR_INDEX_RANGE (an own length where its sequence has query rows), as is a q_start outside [0, M], one that decreases, or
- *   more than max_q rows (such a sequence's rows past max_q are unspecified).
+ *   LR_ERR_INDEX_RANGE (an own length only where its sequence has query rows),
+ *   as is a q_start outside [0, M], one that decreases, or more than max_q rows
+ *   (such a sequence's rows past max_q are unspecified).
  *   A listed page outside [0, pool_blocks) reads as zeros and reports
  *   LR_ERR_REMAP_RANGE.
  *   head_dim 64 or 128; block_rows a multiple of 16; blocks_per_seq * block_rows

@@ -90,7 +90,7 @@ __device__ __forceinline__ SeqView seq_view(const AttnParams& p, int b, bool tel
   }
   const int len = p.lengths[b];
   s.len = len < 0 ? 0 : (len > p.cap_own ? p.cap_own : len);
-  if (tell && (bad || s.len != len)) {
+  if (tell && (bad || (s.len != len && s.nq > 0))) {  // a place without rows may hold any length
     int32_t* st = p.status;
     if (st != nullptr) atomicCAS(st, 0, LR_ERR_INDEX_RANGE);
   }

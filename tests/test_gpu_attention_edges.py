@@ -104,3 +104,13 @@ def test_a_prefix_length_is_reported_where_there_are_no_prefix_pages(lens):
         b.d["prefix_len"].fill_(bad)
         close(b.run(), *want)
         assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, bad
+
+
+@pytest.mark.parametrize("qs", [[3, 0, 5], [70, 0, 5]])
+@pytest.mark.parametrize("stale", [-7, 1 << 30])
+def test_the_length_of_a_sequence_without_rows_is_not_reported(qs, stale):
+    """A place of the batch that is empty may hold any length, whichever kernel runs."""
+    b = Batch(44, 8, 2, 64, 100, [80, 0, 33], qs=qs)
+    b.d["lengths"][1] = stale
+    close(b.run(), *b.want())
+    assert int(b.status.item()) == 0
