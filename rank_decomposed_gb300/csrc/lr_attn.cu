@@ -108,12 +108,12 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
   const int tiles = which ? rl.tiles[1] : rl.tiles[0];
 
   // This CTA's rows: r = (query row - q0) * G + head in the group.
-  int q0, n_rows, row0, len, nq;
+  int q0, n_rows, row0, len, nq, n;
   const int32_t* pages;
   const bool tell = kvh == 0 && threadIdx.x == 0 && split == 0;
   if (prefix) {
     q0 = 0;
-    nq = p.M;
+    n = nq = p.M;
     len = prefix_view(p, tell);
     pages = p.prefix_blocks;
     row0 = tile * kRowsTile;
@@ -122,6 +122,7 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
     const SeqView v = seq_view(p, b, tell);
     q0 = v.q0;
     nq = v.nq;
+    n = v.n;
     len = v.len;
     pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
     row0 = (tile % tiles) * kRowsTile;
@@ -137,9 +138,9 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = row0 + r_lo + 8 * i;
-    vis[i] = prefix ? len : len - nq + r / G + 1;
+    vis[i] = prefix ? len : len - n + r / G + 1;
   }
-  kmax = prefix ? len : len - nq + (row0 + n_rows - 1) / G + 1;
+  kmax = prefix ? len : len - n + (row0 + n_rows - 1) / G + 1;
   if (kmax < 0) kmax = 0;
   const int all_chunks = (kmax + kRowsChunk - 1) / kRowsChunk;
   const int per = (all_chunks + slots - 1) / slots;

@@ -71,8 +71,10 @@ lr_status check_attention(const void* q, int64_t ldq, const void* out, int64_t l
 
 #ifdef __CUDACC__
 // A sequence's query rows and own length, clamped to what the capacities allow.
+// Row j sees the own tokens up to len - n + j: of n rows that are more than
+// max_q, the first nq = max_q still see what they would.
 struct SeqView {
-  int32_t q0, nq, len;
+  int32_t q0, nq, n, len;
 };
 __device__ __forceinline__ SeqView seq_view(const AttnParams& p, int b, bool tell) {
   SeqView s;
@@ -83,10 +85,11 @@ __device__ __forceinline__ SeqView seq_view(const AttnParams& p, int b, bool tel
     const int end = e < 0 ? 0 : (e > p.M ? p.M : e);
     s.nq = end > s.q0 ? end - s.q0 : 0;
     bad = a < 0 || e > p.M || e < a || s.nq > p.max_q;
+    s.n = s.nq;
     if (s.nq > p.max_q) s.nq = p.max_q;
   } else {
     s.q0 = b;
-    s.nq = b < p.M ? 1 : 0;
+    s.n = s.nq = b < p.M ? 1 : 0;
   }
   const int len = p.lengths[b];
   s.len = len < 0 ? 0 : (len > p.cap_own ? p.cap_own : len);

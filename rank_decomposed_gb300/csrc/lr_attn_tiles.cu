@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair = WHOLE ? a.pairs - 1 - item / p.n_seq : item;
   const bool tell = threadIdx.x == 0 && kvh == 0 && split == 0;
   const int prefix_len = p.prefix_len != nullptr ? *p.prefix_len : 0;  // on its way while the lists are made
-  int q0 = 0, nq = p.M, own = 0, mrel;
+  int q0 = 0, nq = p.M, n_seen = 0, own = 0, mrel;
   const int32_t* own_pages = nullptr;
   if (WHOLE) {
     const int b = seq_of;
     const SeqView v = seq_view(p, b, tell && pair == 0);
-    q0 = v.q0, nq = v.nq, own = v.len;
+    q0 = v.q0, nq = v.nq, n_seen = v.n, own = v.len;
     own_pages = p.block_table + static_cast<int64_t>(b) * p.blocks_per_seq;
   }
   mrel = pair * 2 * a.mt;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool dual = rows1 == 0;  // one row tile, both rings
   // own tokens that a tile's last row sees
   auto seen = [&](int m) {
-    const int v = own - nq + m + 1;
+    const int v = own - n_seen + m + 1;
     return v < 0 ? 0 : v;
   };
   // own key tiles of each ring's rows: 128 tokens of the sequence, or eight
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = bars.seq[t][j];
       if (j < rows && b >= 0 && (j == rows - 1 || bars.seq[t][j + 1] != b)) {
         const SeqView v = seq_view(p, first_seq + b, kvh == 0 && split == 0);
-        int vis = v.len - v.nq + (mrel + t * a.mt + j - v.q0) + 1;
+        int vis = v.len - v.n + (mrel + t * a.mt + j - v.q0) + 1;
         vis = vis > v.len ? v.len : vis;
         if (vis > 0) sum = (vis + kPage - 1) / kPage;
       }
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         vis = seen(mrel + tile * a.mt + trow / G);
       } else if (my_seq >= 0) {
         const SeqView v = seq_view(p, first_seq + my_seq, false);
-        vis = v.len - v.nq + (mrel + tile * a.mt + trow / G - v.q0) + 1;
+        vis = v.len - v.n + (mrel + tile * a.mt + trow / G - v.q0) + 1;
         vis = vis > v.len ? v.len : (vis < 0 ? 0 : vis);
         int r = trow / G;
         while (r < (tile ? rows1 : rows0) - 1 && bars.seq[tile][r + 1] == my_seq) ++r;

@@ -114,3 +114,14 @@ def test_the_length_of_a_sequence_without_rows_is_not_reported(qs, stale):
     b.d["lengths"][1] = stale
     close(b.run(), *b.want())
     assert int(b.status.item()) == 0
+
+
+@pytest.mark.parametrize("qs,max_q", [([10, 30, 5], 29), ([10, 30, 5], 12), ([2, 7, 3], 5), ([70, 300, 20], 260)])
+def test_rows_up_to_max_q_of_a_sequence_with_more_are_right(qs, max_q):
+    b = Batch(45, 8, 2, 64, 100, [40, 310, 33], qs=qs)
+    b.d["max_q"] = max_q
+    out = b.run()
+    assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE
+    want, mag = b.want()
+    keep = [r for i, (s, n) in enumerate(zip(b.starts, qs)) for r in range(s, s + min(n, max_q))]
+    close(out[keep], want[keep], mag[keep])
