@@ -434,7 +434,8 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   out = sum_t softmax_t(scale q . k_t) v_t
  * for each of n_heads heads (query head h reads kv head h / (n_heads /
  * n_kv_heads)).  A row that sees no token comes out zero, and so does a row of
- * q that belongs to no sequence.  Pool rows that hold no token of the batch
+ * q that belongs to no sequence; one whose tokens all have the score minus
+ * infinity is NaN, as the formula is.  Pool rows that hold no token of the batch
  * (the ends of last pages among them) do not reach the result, whatever they
  * hold, nor does a sequence's own token reach another sequence's rows.  Within
  * a sequence of several query rows a token that a row does not see has the

@@ -346,6 +346,25 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
 // 59, 68; 100 of 56 heads behind 300 (2 slots) 40, 44.
 constexpr int kMaxSlots = 64;  // of each part
 
+// Whether row m, of some sequence, sees a token: asked where all weights are zero.
+// Then none was summed, or all scores are minus infinity, whose softmax is 0 / 0.
+__device__ __noinline__ bool row_sees(const AttnParams& p, int m) {
+  if (prefix_view(p, false) > 0) return true;
+  int b = m;
+  if (p.q_start != nullptr) {  // the last sequence that starts at or before m
+    int end = p.n_seq;
+    for (b = 0; end - b > 1;) {
+      const int mid = b + (end - b) / 2;
+      if (p.q_start[mid] <= m)
+        b = mid;
+      else
+        end = mid;
+    }
+  }
+  const SeqView v = seq_view(p, b, false);
+  return v.len - v.n + (m - v.q0) + 1 > 0;
+}
+
 template <int HD, int W>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = HD / 32;  // elements per lane
@@ -402,7 +421,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
+    inv = l != 0.f ? 1.f / l : (row_sees(p, m) ? NAN : 0.f);  // no visible key: zeros
   }
   if (W > 1) {
 #pragma unroll

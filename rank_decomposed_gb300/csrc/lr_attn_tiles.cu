@@ -78,6 +78,7 @@
 // us (bytes 80: 87 % of the copy rate).
 #include <cuda_bf16.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "lr_attn.h"
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // One row tile: its two rings' results are joined here, or have a slot each.
   const bool joins = dual && a.direct;
   float mref = -INFINITY, sum = 0.f;
+  bool sees = false;  // a token at all
   float2* hand_ml = reinterpret_cast<float2*>(ring + 128 * (HD + 4) * 4);  // behind ring 1's numerators
 
   if (warp >= 8) {
@@ -801,6 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         list_lo = r > 0 ? bars.groups[tile][r - 1] * kPage : 0;
         list_hi = bars.groups[tile][r] * kPage;
       }
+      sees = P > 0 || vis > 0;
       if (!WHOLE) {  // the rows of a tile do not all take part in its first product
         uint32_t z[16];
 #pragma unroll
@@ -998,8 +1001,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t slot_rows = static_cast<int64_t>(p.M) * p.n_heads;
         const int64_t at = slot * slot_rows + qrow * p.n_heads + head;
         if (a.direct) {
-          // a packed row of no sequence comes out zero, and so does one that saw no key
-          const float inv = l == 0.f || (!WHOLE && my_seq < 0) ? 0.f : 1.f / l;
+          // a packed row of no sequence comes out zero, and so does one that sees no key;
+          // one that sees keys of score minus infinity alone is 0 / 0
+          const float inv = !WHOLE && my_seq < 0 ? 0.f : (l != 0.f ? 1.f / l : (sees ? NAN : 0.f));
           f0 *= inv;
           f1 *= inv;
         } else if (live) {

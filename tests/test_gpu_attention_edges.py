@@ -5,8 +5,9 @@ import pytest
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
+import oracle  # noqa: E402
 import rank_decomposed_gb300 as lr  # noqa: E402
-from test_gpu_attention import Batch, _i32, close  # noqa: E402
+from test_gpu_attention import Batch, _f64, _i32, close  # noqa: E402
 
 
 @pytest.fixture(autouse=True, params=[1, 2], ids=["rows", "tiles"])
@@ -125,3 +126,31 @@ def test_rows_up_to_max_q_of_a_sequence_with_more_are_right(qs, max_q):
     want, mag = b.want()
     keep = [r for i, (s, n) in enumerate(zip(b.starts, qs)) for r in range(s, s + min(n, max_q))]
     close(out[keep], want[keep], mag[keep])
+
+
+@pytest.mark.parametrize("nh,nkv,hd,n,bps", [(8, 1, 128, 3, 4), (4, 4, 64, 5, 4), (8, 1, 128, 60, 4), (4, 4, 128, 200, 4),
+                                             (80, 80, 64, 3, 1), (8, 2, 64, 9, 300)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_scores_of_minus_infinity(nh, nkv, hd, n, bps, ragged):
+    """Such a key has no weight beside others; a row whose tokens all have that score is NaN, as its softmax is."""
+    qs = [1 + i % 2 for i in range(n)] if ragged else None
+    for prefix in (0, 70):
+        lens = [i % 3 * 7 for i in range(n)]            # sequences 0, 3, .. see the prefix alone
+        b = Batch(46, nh, nkv, hd, prefix, lens, qs=qs, bps=bps)
+        b.q.view(b.m, nh, hd)[:, :, 0] = 1.0
+        low = b.rows_of(b.prefix_blocks, prefix)        # all of the prefix, all of some sequences, a part of others
+        for i in range(n):
+            rows = b.rows_of(b.table[i], lens[i])
+            low += rows if i % 2 else rows[: len(rows) // 2]
+        b.kp.view(-1, nkv, hd)[low, :, 0] = float("-inf")
+        with np.errstate(invalid="ignore"):
+            kp, vp = (np.where(np.isnan(x), 0.0, x) for x in (_f64(b.kp), _f64(b.vp)))
+            want, mag = oracle.prefix_attention(_f64(b.q), kp, vp, nh, nkv, hd, b.br, b.prefix_blocks.numpy(), prefix,
+                                                b.table.numpy(), b.lens, b.starts, hd ** -0.5)
+        out = b.run()
+        assert int(b.status.item()) == 0
+        nan = np.isnan(want)
+        assert nan.any() and not nan.all()
+        assert np.array_equal(np.isnan(_f64(out)), nan)
+        ok = ~nan.any(1)
+        close(out[torch.from_numpy(ok).cuda()], want[ok], mag[ok])
