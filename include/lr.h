@@ -462,9 +462,14 @@ lr_status lr_kv_append(const void* k, int64_t ldk, const void* v, int64_t ldv, c
  *   head_dim 64 or 128; block_rows a multiple of 16; blocks_per_seq * block_rows
  *   below 2^24; n_heads a multiple of n_kv_heads with at most 64 query heads a
  *   kv head (LR_ERR_UNSUPPORTED otherwise, LR_ERR_INVALID_ARG for a remainder); scale > 0 and finite.
- *   workspace: device, 256-byte aligned, at least
- *   lr_prefix_attention_workspace_bytes(M, d); contents on entry do not
- *   matter; calls that share it must be ordered on one stream.
+ *   workspace: device, 256-byte aligned, of
+ *   lr_prefix_attention_workspace_bytes(M, d) bytes (a call that needs less
+ *   takes less); contents on entry do not matter; calls that share it must be
+ *   ordered on one stream.  That size does not fall as M, n_seq or the numbers
+ *   of pages grow, and max_q and q_start do not enter it: a workspace for a
+ *   program's largest sizes serves all its calls with the same heads and page
+ *   rows.  It is 512 rows of results an SM (40 MB for heads of 128) at most,
+ *   unless n_kv_heads alone gives more.
  *   Scores, softmax statistics and sums are fp32; probabilities are rounded to
  *   bf16 for the second product.  The result is deterministic.  M = 0 or
  *   n_seq = 0 with M = 0 is a no-op. */
@@ -498,8 +503,9 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
  *   n_heads, n_kv_heads and head_dim of ctx and block must agree, and head_dim
  *   and block_rows are those that lr_prefix_attention takes.
  *   Rows m >= *n_active (NULL: none) append nothing; their h is unspecified.
- *   scratch: device, at least lr_block_cached_scratch_bytes(M, b, ctx) bytes,
- *   256-byte aligned.  Checks, reports and capture as for the parts.  M = 0 is
+ *   scratch: device, lr_block_cached_scratch_bytes(M, b, ctx) bytes, which
+ *   grows with M and the context's capacities as its parts do, 256-byte
+ *   aligned.  Checks, reports and capture as for the parts.  M = 0 is
  *   a no-op. */
 typedef struct {
   lr_attn_desc attn;

@@ -744,14 +744,15 @@ lr_status lr_block_forward_cached(float* h, int64_t M, const lr_block_desc* b, c
   if (h == nullptr || scratch == nullptr) return invalid("block: null pointer");
   if (!aligned16(h) || reinterpret_cast<uintptr_t>(scratch) % kAlign)
     return invalid("block: h must be 16-byte and scratch 256-byte aligned");
-  if (scratch_bytes < lr_block_cached_scratch_bytes(M, b, ctx)) return invalid("block: scratch too small");
+  const size_t out_bytes = align_up(static_cast<size_t>(M) * b->n_heads * b->head_dim * 2);
+  const size_t own_bytes = block_layout(M, b).total + out_bytes;
+  if (scratch_bytes < own_bytes) return invalid("block: scratch too small");
   uint8_t* ws = static_cast<uint8_t*>(scratch);
   BlockContext bc;
   bc.ctx = ctx;
   bc.out = ws + block_layout(M, b).total;
-  const size_t out_bytes = align_up(static_cast<size_t>(M) * b->n_heads * b->head_dim * 2);
   bc.ws = static_cast<uint8_t*>(bc.out) + out_bytes;
-  bc.ws_bytes = lr_prefix_attention_workspace_bytes(M, &at);
+  bc.ws_bytes = scratch_bytes - own_bytes;
   // Both parts' arguments, before anything is enqueued.
   st = check_context(M, ctx, bc.out, bc.ws, bc.ws_bytes);
   if (st != LR_OK) return st;

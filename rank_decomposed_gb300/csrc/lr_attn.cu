@@ -480,13 +480,14 @@ lr_status bad(lr_status st, const char* fmt, ...) {
 }
 
 int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+int64_t smaller(int64_t a, int64_t b) { return a < b ? a : b; }
 
 // No sequence has more rows than the call.
 int64_t most_q(int64_t M, const lr_attn_desc* d) { return d->max_q < M ? d->max_q : (M < 1 ? 1 : M); }
 
 // Key ranges for `ctas` row tiles: as many as fill `want` CTAs, none shorter
-// than min_keys.  (The workspace rule comes here with sizes that the call itself
-// refuses: a count that wrapped gets one range.)
+// than min_keys.
 int slots_for(int64_t ctas, int64_t keys, int64_t want, int64_t min_keys) {
   if (keys <= 0) return 0;
   int64_t n = ctas >= want || ctas < 1 ? 1 : want / ctas;
@@ -535,6 +536,8 @@ bool by_rows(int64_t M, int64_t mq, int G, const lr_attn_desc* d, int64_t cap_pr
   return 3.7 * wide * (shared + own) / (2.0 * num_sms()) + keys / 16e3 <= 12.0;
 }
 
+size_t result_bytes(int64_t rows, int64_t each) { return static_cast<size_t>(rows * each + 255) / 256 * 256; }
+
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   AttnPlan a;
   memset(&a, 0, sizeof(a));
@@ -549,7 +552,7 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
   if (a.tiles) {
     // Steps of a row tile pair when all is full; packed tiles have the own tokens
     // of every sequence in them.
-    const int64_t ctas = (a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
+    const int64_t ctas = (a.whole ? larger(d->n_seq * cdiv(mq, pair), cdiv(M, pair)) : cdiv(M, pair)) * kv;
     const int64_t seqs = a.whole ? 1 : (d->n_seq < pair / 2 ? d->n_seq : pair / 2);
     const int64_t steps = cdiv(cap_prefix, 128) + cdiv(seqs * cap_own, 128);
     a.tile_slots = slots_for(ctas, steps, num_sms(), kMinSteps);
@@ -564,12 +567,39 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
     // with 1, 2, 4 CTAs an SM, one of 32 over 32 behind 60000 167, 156, 155.
     const int64_t want = num_sms() * 2;
     a.prefix_slots = slots_for(static_cast<int64_t>(cdiv(M * G, kRowsTile)) * kv, cap_prefix, want, 128);
-    a.own_slots = d->n_seq == 0 ? 0 : slots_for(d->n_seq * cdiv(mq * G, kRowsTile) * kv, cap_own, want, 128);
+    a.own_slots = d->n_seq == 0 ? 0 : slots_for(larger(d->n_seq * cdiv(mq * G, kRowsTile), cdiv(M * G, kRowsTile)) * kv, cap_own, want, 128);
   }
-  const size_t rows = static_cast<size_t>(M) * d->n_heads * (a.prefix_slots + a.own_slots);
-  a.ml_off = (rows * d->cache.head_dim * 4 + 255) / 256 * 256;
-  a.bytes = a.ml_off + (rows * 8 + 255) / 256 * 256;
+  const int64_t rows = M * d->n_heads * (a.prefix_slots + a.own_slots);
+  a.ml_off = result_bytes(rows, d->cache.head_dim * 4);
+  a.bytes = a.ml_off + result_bytes(rows, 8);
   return a;
+}
+
+// Workspace for every call of up to M rows with up to d's sequences and pages.
+// What a call itself needs goes up and down with its sizes, as the kernels and
+// key ranges change (64 heads over 8 behind 8192 tokens: 18 MB for 64 rows, 16 for
+// 256, none for 512), and a program that allocates once for its largest batch must
+// serve the smaller ones.  R = M * n_heads rows have R times the most key ranges of
+// results; and no call has more than
+//   on tiles    ranges * row tile pairs <= SMs, 256 rows a pair, two results a range:
+//               512 SMs;
+//   by rows     of each part, either ranges * CTAs <= 2 SMs, with 16 rows a CTA, or one
+//               range, R <= 104 SMs * 128 / head_dim by the limit of by_rows: 416 SMs at
+//               most; or no more than one row tile a key head: 2 * 16 n_kv.
+size_t attn_workspace(int64_t M, const lr_attn_desc* d) {
+  // (zero for sizes that the call refuses, those that would overflow below among them)
+  const int64_t cap_prefix = static_cast<int64_t>(d->cap_prefix_blocks) * d->cache.block_rows;
+  const int64_t cap_own = d->n_seq > 0 ? static_cast<int64_t>(d->blocks_per_seq) * d->cache.block_rows : 0;
+  if (M * d->n_heads > 0x7FFFFFFF || cap_prefix > 0x7FFFFFFF || cap_own > 0x7FFFFFFF) return 0;
+  const int64_t R = M * d->n_heads;
+  const int64_t pair = 2 * attn_tile_rows(d->n_heads / d->cache.n_kv_heads);
+  const int64_t by_rows = smaller((cap_prefix + 127) / 128, kMaxSlots) + smaller((cap_own + 127) / 128, kMaxSlots);
+  const int64_t steps = (cap_prefix + 127) / 128 + (smaller(d->n_seq, pair / 2) * cap_own + 127) / 128;
+  const int64_t on_tiles = smaller((steps + kMinSteps - 1) / kMinSteps, kMaxSlots / 2);
+  int64_t most = larger(512 * static_cast<int64_t>(num_sms()), 2 * smaller(R, static_cast<int64_t>(kRowsTile) * d->cache.n_kv_heads));
+  if (test_attention_kernel() == 1) most = larger(most, 2 * R);
+  const int64_t rows = smaller(R * larger(by_rows, on_tiles > 1 ? 2 * on_tiles : 0), most);
+  return result_bytes(rows, d->cache.head_dim * 4) + result_bytes(rows, 8);
 }
 
 lr_status check_desc(const char* who, int64_t M, const lr_attn_desc* d) {
@@ -673,9 +703,10 @@ extern "C" {
 
 size_t lr_prefix_attention_workspace_bytes(int64_t M, const lr_attn_desc* d) {
   if (d == nullptr || M <= 0 || M > 0x7FFFFFFF || d->cache.n_kv_heads <= 0 || d->n_heads < d->cache.n_kv_heads || d->max_q < 1 ||
-      d->n_heads / d->cache.n_kv_heads > kMostHeads || d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0)
+      d->n_heads / d->cache.n_kv_heads > kMostHeads || d->cap_prefix_blocks < 0 || d->blocks_per_seq < 0 || d->n_seq < 0 ||
+      d->cache.block_rows <= 0 || d->cache.head_dim <= 0 || d->cache.head_dim > 128)
     return 0;
-  return attn_plan(M, d).bytes;
+  return attn_workspace(M, d);
 }
 
 lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo, lr_dtype out_dtype, int64_t M,

@@ -154,3 +154,17 @@ def test_scores_of_minus_infinity(nh, nkv, hd, n, bps, ragged):
         assert np.array_equal(np.isnan(_f64(out)), nan)
         ok = ~nan.any(1)
         close(out[torch.from_numpy(ok).cuda()], want[ok], mag[ok])
+
+
+def test_a_workspace_for_the_largest_batch_serves_smaller_ones(kernel):
+    """Sized once, by the rule, for 300 sequences; the calls need more of it, less of it or nothing as sizes change."""
+    lr.lib.lr_test_attention_kernel(0)                 # the kernel that the sizes choose
+    full = Batch(48, 16, 2, 128, 700, [1 + i % 40 for i in range(300)])
+    ws = full.workspace()
+    for n in (1, 2, 9, 40, 130, 300):
+        b = Batch(49, 16, 2, 128, 700, [1 + i % 40 for i in range(n)])
+        assert lr.prefix_attention_workspace_bytes(n, 16, b.cache(), **b.d) <= ws.numel()
+        ws.fill_(0xFF)
+        out = b.run(ws=ws)
+        assert int(b.status.item()) == 0
+        close(out, *b.want())
