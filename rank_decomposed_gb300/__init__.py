@@ -576,9 +576,10 @@ class Context:
     scale: object = None
     n_active: object = None
 
-    def c(self, M: int, n_heads: int) -> ContextDesc:
+    def c(self, M: int, n_heads: int, launch: bool = False) -> ContextDesc:
+        """The C structure; with launch, every tensor has to be on the GPU."""
         _call(0)
-        return ContextDesc.from_buffer_copy(_calls.context(self, M, n_heads))
+        return ContextDesc.from_buffer_copy(_calls.context(self, M, n_heads, launch))
 
 
 def block_cached_scratch_bytes(M: int, b: Block, ctx: Context) -> int:
@@ -590,7 +591,14 @@ def block_forward_cached(h, b: Block, ctx: Context, scratch, status, stream=None
     import torch
     if h.dtype != torch.float32 or not h.is_contiguous():
         raise TypeError("h must be a contiguous float32 tensor")
-    bc, cc = b.c(), ctx.c(h.shape[0], b.n_heads)
+    if h.dim() != 2 or h.shape[1] != b.d_model:
+        raise ValueError("h must be [M][d_model]")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise TypeError("status must be an int32 tensor with an element")
+    for name, t in (("h", h), ("scratch", scratch), ("status", status)):
+        if t is not None and h.shape[0] > 0 and not t.is_cuda:
+            raise TypeError("%s must be on the GPU" % name)
+    bc, cc = b.c(), ctx.c(h.shape[0], b.n_heads, launch=True)
     st = lib.lr_block_forward_cached(h.data_ptr(), h.shape[0], ctypes.byref(bc), ctypes.byref(cc), scratch.data_ptr(),
                                      scratch.nbytes, _ptr(status), _stream(stream))
     _check("lr_block_forward_cached", st)

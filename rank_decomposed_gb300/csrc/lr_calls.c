@@ -4,9 +4,9 @@
  * reading thirty properties of ten tensors from Python and converting them by
  * ctypes took most of a call (one token's rotation: 9.6 us, 3.4 of them the
  * library's launch; from here 4.9).  Each property is read once, checked, and
- * put into the structures of lr.h.  Tensors are read by their Python attributes alone, so the
- * extension knows no version of torch.  It holds no state but the functions and
- * types given to init().
+ * put into the structures of lr.h.  Tensors are read by their Python attributes
+ * alone, so the extension knows no version of torch.  It holds no state but the
+ * functions and types given to init().
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -35,7 +35,7 @@ static PyObject *t_bf16, *t_f32, *t_i32; /* torch's dtypes */
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_is_contiguous, *s_nbytes, *s_head_dim, *s_norm, *s_eps,
     *s_q_gain, *s_k_gain, *s_rot_dim, *s_rot_style, *s_cos_sin, *s_k_pool, *s_v_pool, *s_n_kv_heads, *s_block_rows,
     *s_cache, *s_heads, *s_pos, *s_rows, *s_prefix_blocks, *s_prefix_len, *s_block_table, *s_lengths, *s_q_start,
-    *s_max_q, *s_scale, *s_n_active;
+    *s_max_q, *s_scale, *s_n_active, *s_is_cuda;
 
 typedef struct {
   void* p;
@@ -72,10 +72,24 @@ static int arg_i64(PyObject* v, int64_t* out) {
   return *out == -1 && PyErr_Occurred() ? -1 : 0;
 }
 
+/* The first tensor of the present call that is not on the GPU.  Calls without
+ * rows touch no tensor, and the structures' sizes can be asked for without a
+ * GPU; a launch refuses it, since the kernels would follow a host address. */
+static _Thread_local const char* host_tensor;
+
+static int on_gpu(int64_t rows) {
+  if (rows <= 0 || host_tensor == NULL) return 0;
+  return fail(PyExc_TypeError, "%s must be on the GPU", host_tensor);
+}
+
 /* Address of a tensor; None is NULL. */
-static int address(PyObject* t, void** out) {
+static int address(PyObject* t, const char* name, void** out) {
   *out = NULL;
   if (t == Py_None) return 0;
+  PyObject* dev = PyObject_GetAttr(t, s_is_cuda);
+  if (dev == NULL) return -1;
+  Py_DECREF(dev); /* a truth value */
+  if (dev != Py_True && host_tensor == NULL) host_tensor = name;
   PyObject* v = PyObject_CallMethodNoArgs(t, s_data_ptr);
   if (v == NULL) return -1;
   const unsigned long long a = PyLong_AsUnsignedLongLong(v);
@@ -140,7 +154,7 @@ static int matrix(PyObject* t, const char* name, PyObject* type, int64_t rows, i
   m->cols = shape[1];
   /* one row's stride says nothing: it counts as at least the row's width */
   m->ld = shape[0] > 1 || stride[0] >= shape[1] ? stride[0] : (shape[1] + 7) / 8 * 8;
-  return address(t, &m->p);
+  return address(t, name, &m->p);
 }
 
 /* A contiguous tensor of `dims` (1 or 2) dimensions; None is NULL with sizes 0.  n < 0: any first size. */
@@ -163,7 +177,7 @@ static int table(PyObject* t, const char* name, PyObject* type, int dims, int64_
     return -1;
   }
   if (n >= 0 && shape[0] != n) return fail(PyExc_ValueError, "%s has another number of entries than the call needs", name);
-  return address(t, p);
+  return address(t, name, p);
 }
 
 static int vector_i32(PyObject* t, const char* name, int64_t n, const int32_t** p) {
@@ -172,6 +186,26 @@ static int vector_i32(PyObject* t, const char* name, int64_t n, const int32_t** 
   if (table(t, name, t_i32, 1, n, &a, shape) < 0) return -1;
   *p = (const int32_t*)a;
   return 0;
+}
+
+/* One int32 on the device, the first of a vector; None is NULL. */
+static int word_i32(PyObject* t, const char* name, const int32_t** p) {
+  int64_t shape[2];
+  void* a;
+  if (table(t, name, t_i32, 1, -1, &a, shape) < 0) return -1;
+  if (t != Py_None && shape[0] < 1) return fail(PyExc_ValueError, "%s is empty", name);
+  *p = (const int32_t*)a;
+  return 0;
+}
+
+/* The status word: any int32 tensor with an element; None is NULL. */
+static int status_word(PyObject* t, void** p) {
+  int64_t bytes;
+  *p = NULL;
+  if (t == Py_None) return 0;
+  if (has_dtype(t, "status", t_i32) < 0 || attr_i64(t, s_nbytes, &bytes) < 0) return -1;
+  if (bytes < 4) return fail(PyExc_ValueError, "%s is empty", "status");
+  return address(t, "status", p);
 }
 
 static int attr_table(PyObject* o, PyObject* attr, PyObject* type, int dims, int64_t n, void** p, int64_t* shape) {
@@ -264,7 +298,7 @@ static int attn_desc(int64_t n_heads, PyObject* cache, PyObject* prefix_blocks, 
   if (table(prefix_blocks, "prefix_blocks", t_i32, 1, -1, &p, shape) < 0) return -1;
   d->prefix_blocks = (const int32_t*)p;
   if (to_i32(shape[0], "the number of prefix pages", &d->cap_prefix_blocks) < 0) return -1;
-  if (vector_i32(prefix_len, "prefix_len", -1, &d->prefix_len) < 0) return -1;
+  if (word_i32(prefix_len, "prefix_len", &d->prefix_len) < 0) return -1;
   return vector_i32(q_start, "q_start", n + 1, &d->q_start);
 }
 
@@ -276,6 +310,7 @@ static int stream_of(PyObject* v, lr_stream* s) {
 }
 
 static int n_args(const char* name, Py_ssize_t got, Py_ssize_t want) {
+  host_tensor = NULL;
   if (got == want && g_rope != NULL) return 0;
   PyErr_Format(PyExc_TypeError, "%s: %zd arguments after init(), not %zd", name, want, got);
   return -1;
@@ -311,8 +346,8 @@ static PyObject* py_qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t 
     PyErr_SetString(PyExc_ValueError, "qk_norm_rope: a width is not whole heads of head_dim");
     return NULL;
   }
-  if (vector_i32(a[2], "pos", rows, &pos) < 0 || vector_i32(a[7], "n_active", -1, &active) < 0 ||
-      address(a[6], &status) < 0 || stream_of(a[8], &s) < 0)
+  if (vector_i32(a[2], "pos", rows, &pos) < 0 || word_i32(a[7], "n_active", &active) < 0 ||
+      status_word(a[6], &status) < 0 || stream_of(a[8], &s) < 0 || on_gpu(rows) < 0)
     return NULL;
   lr_status st;
   Py_BEGIN_ALLOW_THREADS
@@ -346,7 +381,8 @@ static PyObject* py_kv_append(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     }
   }
   if (vector_i32(a[2], "pos", k.rows, &pos) < 0 || vector_i32(a[3], "rows", k.rows, &rows) < 0 ||
-      vector_i32(a[9], "n_active", -1, &active) < 0 || address(a[6], &status) < 0 || stream_of(a[10], &s) < 0)
+      word_i32(a[9], "n_active", &active) < 0 || status_word(a[6], &status) < 0 || stream_of(a[10], &s) < 0 ||
+      on_gpu(k.rows) < 0)
     return NULL;
   lr_status st;
   Py_BEGIN_ALLOW_THREADS
@@ -374,8 +410,8 @@ static PyObject* py_prefix_attention(PyObject* self, PyObject* const* a, Py_ssiz
   if (matrix(a[0], "q", t_bf16, -1, (int64_t)d.n_heads * d.cache.head_dim, &q) < 0 ||
       matrix(a[7], "out", type, q.rows, q.cols, &out) < 0)
     return NULL;
-  if (address(a[8], &ws) < 0 || (a[8] != Py_None && attr_i64(a[8], s_nbytes, &bytes) < 0) ||
-      address(a[9], &status) < 0 || stream_of(a[13], &s) < 0)
+  if (address(a[8], "workspace", &ws) < 0 || (a[8] != Py_None && attr_i64(a[8], s_nbytes, &bytes) < 0) ||
+      status_word(a[9], &status) < 0 || stream_of(a[13], &s) < 0 || on_gpu(q.rows) < 0)
     return NULL;
   lr_status st;
   Py_BEGIN_ALLOW_THREADS
@@ -405,7 +441,7 @@ static PyObject* py_attn_desc(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     return NULL;
   return PyBytes_FromStringAndSize((const char*)&d, sizeof(d));
 }
-/* (context, M, n_heads) */
+/* (context, M, n_heads, whether it is for a launch) */
 static PyObject* py_context(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   (void)self;
   PyObject* names[] = {s_cache, s_prefix_blocks, s_prefix_len, s_block_table, s_lengths, s_q_start, s_scale,
@@ -413,13 +449,14 @@ static PyObject* py_context(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   PyObject* v[11] = {0};
   lr_context c;
   int64_t m, heads, max_q;
-  int ok = n_args("context", n, 3) == 0 && arg_i64(a[1], &m) == 0 && arg_i64(a[2], &heads) == 0 &&
+  int ok = n_args("context", n, 4) == 0 && arg_i64(a[1], &m) == 0 && arg_i64(a[2], &heads) == 0 &&
            attr_i64(a[0], s_max_q, &max_q) == 0;
   memset(&c, 0, sizeof(c));
   for (int i = 0; ok && i < 11; ++i) ok = (v[i] = PyObject_GetAttr(a[0], names[i])) != NULL;
   ok = ok && attn_desc(heads, v[0], v[1], v[2], v[3], v[4], v[5], max_q, v[6], &c.attn) == 0 &&
        head_map(v[7], &c.heads) == 0 && vector_i32(v[8], "pos", m, &c.pos) == 0 &&
-       vector_i32(v[9], "rows", m, &c.rows) == 0 && vector_i32(v[10], "n_active", -1, &c.n_active) == 0;
+       vector_i32(v[9], "rows", m, &c.rows) == 0 && word_i32(v[10], "n_active", &c.n_active) == 0 &&
+       (a[3] != Py_True || on_gpu(m) == 0);
   for (int i = 0; i < 11; ++i) Py_XDECREF(v[i]);
   return ok ? PyBytes_FromStringAndSize((const char*)&c, sizeof(c)) : NULL;
 }
@@ -465,7 +502,7 @@ PyMODINIT_FUNC PyInit__calls(void) {
                {&s_n_kv_heads, "n_kv_heads"}, {&s_block_rows, "block_rows"}, {&s_cache, "cache"}, {&s_heads, "heads"},
                {&s_pos, "pos"}, {&s_rows, "rows"}, {&s_prefix_blocks, "prefix_blocks"}, {&s_prefix_len, "prefix_len"},
                {&s_block_table, "block_table"}, {&s_lengths, "lengths"}, {&s_q_start, "q_start"}, {&s_max_q, "max_q"},
-               {&s_scale, "scale"}, {&s_n_active, "n_active"}};
+               {&s_scale, "scale"}, {&s_n_active, "n_active"}, {&s_is_cuda, "is_cuda"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
     if ((*names[i].at = PyUnicode_InternFromString(names[i].name)) == NULL) return NULL;
   return PyModule_Create(&module);
