@@ -149,7 +149,10 @@ def _load():
 
 
 lib = _load()
-from . import _calls  # noqa: E402  (built beside liblr.so)
+try:
+    from . import _calls  # noqa: E402  (built beside liblr.so, for this Python)
+except ImportError:
+    from . import _marshal as _calls  # noqa: E402  (the same through ctypes)
 
 
 def status_string(st: int) -> str:
@@ -445,7 +448,8 @@ def kv_reconstruct_paged(latent_pool, blocks, n_blocks, Bt, out, status, stream=
 
 # ------------------------------------------------- attention over a context
 # These calls sit in a decode step whose kernels take a few microseconds: their
-# arguments are checked and put together in C (csrc/lr_calls.c).
+# arguments are checked and put together in C (csrc/lr_calls.c), or by ctypes where
+# that extension could not be built for this Python (_marshal.py).
 _ready = False
 
 

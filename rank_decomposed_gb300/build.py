@@ -1,5 +1,5 @@
-"""Build liblr.so (the CUDA path), _calls.so (argument marshalling of small
-calls) and libsynth.so (the GPU input generator).
+"""Build liblr.so (the CUDA path), the extension _calls (argument marshalling of
+small calls, for this Python alone) and libsynth.so (the GPU input generator).
 
 All are compiled in-tree, the CUDA code for sm_103a only, with nvcc, one
 translation unit per process so a build takes well under a minute.
@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblr.so")
 CALLS_SRC = os.path.join(CSRC, "lr_calls.c")
-CALLS_LIB = os.path.join(PKG, "_calls.so")
+CALLS_LIB = os.path.join(PKG, "_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SYNTH_SRC = os.path.join(ROOT, "synth", "synth_gen.cu")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 SYNTH_HOST_SRC = os.path.join(ROOT, "synth", "synth_host.c")
@@ -48,6 +48,15 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def calls_command():
+    """The command that builds the extension, or None where this Python has no C headers: the package runs without it."""
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    return [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-I", include, "-I",
+            os.path.join(ROOT, "include"), CALLS_SRC, "-o", CALLS_LIB]
+
+
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     exe = nvcc()
@@ -60,14 +69,17 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
                  SYNTH_SRC, "-o", SYNTH_LIB]
     host_cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c99", "-fopenmp", "-fPIC", "-shared",
                 SYNTH_HOST_SRC, "-o", SYNTH_HOST_LIB]
-    calls_cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-fPIC", "-shared", "-I",
-                 sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"), CALLS_SRC, "-o", CALLS_LIB]
+    calls_cmd = calls_command()
+    untagged = os.path.join(PKG, "_calls.so")  # what any Python would load
+    if untagged != CALLS_LIB and os.path.exists(untagged):
+        os.remove(untagged)
     logs = []
     with cf.ThreadPoolExecutor(max_workers=min(8, len(jobs) + 1)) as ex:
         futs = [ex.submit(_run, cmd) for cmd, _ in jobs]
         futs.append(ex.submit(_run, synth_cmd))
         futs.append(ex.submit(_run, host_cmd))
-        futs.append(ex.submit(_run, calls_cmd))
+        if calls_cmd is not None:
+            futs.append(ex.submit(_run, calls_cmd))
         for f in futs:
             logs.append(f.result())
     _run([exe, *ARCH, "-shared", "-o", LIB, *[o for _, o in jobs], "-lcudart_static"])
