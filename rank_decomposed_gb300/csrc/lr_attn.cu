@@ -536,6 +536,15 @@ bool by_rows(int64_t M, int64_t mq, int G, const lr_attn_desc* d, int64_t cap_pr
   return 3.7 * wide * (shared + own) / (2.0 * num_sms()) + keys / 16e3 <= 12.0;
 }
 
+// CTAs of a planned call, by rows or on tiles (key ranges of tiles are another
+// dimension of their grid).
+int64_t plan_ctas(int64_t M, const lr_attn_desc* d, const AttnPlan& a) {
+  const int64_t G = d->n_heads / d->cache.n_kv_heads, mq = most_q(M, d), pair = 2 * attn_tile_rows(static_cast<int>(G));
+  if (a.tiles) return (a.whole ? d->n_seq * static_cast<int64_t>(cdiv(mq, pair)) : cdiv(M, pair)) * d->cache.n_kv_heads;
+  return (static_cast<int64_t>(cdiv(M * G, kRowsTile)) * a.prefix_slots +
+          d->n_seq * static_cast<int64_t>(cdiv(mq * G, kRowsTile)) * a.own_slots) * d->cache.n_kv_heads;
+}
+
 size_t result_bytes(int64_t rows, int64_t each) { return static_cast<size_t>(rows * each + 255) / 256 * 256; }
 
 AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
@@ -645,7 +654,6 @@ lr_status launch_attn_rows(const AttnParams& p, int head_dim, cudaStream_t s) {
   rl.tiles[1] = cdiv(static_cast<int64_t>(p.max_q) * p.group, kRowsTile);
   const int64_t ctas0 = static_cast<int64_t>(rl.tiles[0]) * p.n_kv * p.prefix_slots;
   const int64_t ctas = ctas0 + static_cast<int64_t>(rl.tiles[1]) * p.n_seq * p.n_kv * p.own_slots;
-  if (ctas > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "prefix_attention: too many rows for one launch");
   if (ctas == 0) return LR_OK;
   rl.ctas0 = static_cast<int32_t>(ctas0);
   const dim3 grid(static_cast<unsigned>(ctas));
@@ -688,6 +696,7 @@ lr_status check_attention(const void* q, int64_t ldq, const void* out, int64_t l
     return bad(LR_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned with leading dimensions >= %lld, multiples of 8", who,
                static_cast<long long>(width));
   const AttnPlan plan = attn_plan(M, d);
+  if (plan_ctas(M, d, plan) > 0x7FFFFFFF) return bad(LR_ERR_UNSUPPORTED, "%s: too many rows for one launch", who);
   if (plan.bytes > 0 && (workspace == nullptr || !aligned(workspace, 256)))
     return bad(LR_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", who);
   if (ws_bytes < plan.bytes)

@@ -1120,10 +1120,6 @@ lr_status launch_attn_tiles(const AttnParams& p, int head_dim, const AttnPart& p
   a.two = part.two;
   a.stall = test_stall_producer();
   const int64_t ctas = static_cast<int64_t>(a.pairs) * (part.whole ? p.n_seq : 1) * p.n_kv;
-  if (ctas > 0x7FFFFFFF) {
-    set_error("prefix_attention: too many rows for one launch");
-    return LR_ERR_UNSUPPORTED;
-  }
   const dim3 grid(static_cast<unsigned>(ctas), 1, part.slots);
   if (head_dim == 64) return part.whole ? launch_tiles<64, true>(a, grid, s) : launch_tiles<64, false>(a, grid, s);
   return part.whole ? launch_tiles<128, true>(a, grid, s) : launch_tiles<128, false>(a, grid, s);

@@ -72,3 +72,15 @@ def test_one_workspace_for_a_decode_batch_of_any_size():
     """512 prefix pages and 32 own pages of 16 rows, 64 heads over 8: the call needs 18 MB at 64 rows, none at 512."""
     sizes = [_rule(M, (64, 8, 128), 16, 512, M, 32, 1, False) for M in (1, 64, 256, 512, 4096)]
     assert sizes == sorted(sizes) and sizes[1] >= 18 << 20 and sizes[-1] < 48 << 20
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("nh,nkv,n_seq,mq", [(32, 8, 1 << 29, 5), (8, 8, 1 << 30, 1)])
+def test_too_many_sequences_for_a_launch_are_refused_before_anything_is_enqueued(kernel, nh, nkv, n_seq, mq):
+    d, w = _desc((nh, nkv, 128), 16, 3, n_seq, 4, mq, True), nh * 128
+    lr.lib.lr_test_attention_kernel(kernel)
+    try:
+        st = lr.lib.lr_prefix_attention(0x10000, w, 0x20000, w, 0, 9, ctypes.byref(d), 0x30000, 1 << 40, None, None)
+    finally:
+        lr.lib.lr_test_attention_kernel(0)
+    assert st == lr.LR_ERR_UNSUPPORTED and "one launch" in lr.last_error()
