@@ -388,7 +388,7 @@ def block_forward_cached(h, factors, n_heads: int, n_kv: int, head_dim: int, k_p
     """block_forward with attention over a paged context.
 
     k_pool, v_pool (fp64 arrays) get the new tokens' rows; batch(q) is the attention of the prepared queries
-    over the pools.  gains: (q gain, k gain) or None for no norm.
+    over the pools.  gains: (q gain, k gain) or None for no norm.  A gate of None: the ReLU MLP of block_forward.
     """
     h = np.asarray(h, dtype=np.float64)
     n1 = rmsnorm(h, eps)
@@ -399,7 +399,8 @@ def block_forward_cached(h, factors, n_heads: int, n_kv: int, head_dim: int, k_p
     attn = batch(map_heads(q, head_dim, gq, head_eps, cos, sin, style))
     h1 = h + lowrank_linear(attn, *factors["o"])[1]
     n2 = rmsnorm(h1, eps)
-    a = silu(lowrank_linear(n2, *factors["gate"])[1]) * lowrank_linear(n2, *factors["up"])[1]
+    u = lowrank_linear(n2, *factors["up"])[1]
+    a = relu(u) if factors["gate"] is None else silu(lowrank_linear(n2, *factors["gate"])[1]) * u
     return h1 + lowrank_linear(a, *factors["down"])[1]
 
 
