@@ -106,9 +106,10 @@ def _status(t, host):
     if t is None:
         return None
     _typed(t, "status", _i32)
-    if t.nbytes < 4:
+    p = _address(t, "status", host)
+    if p is None:
         raise ValueError("status is empty")
-    return _address(t, "status", host)
+    return p
 
 
 def _head_map(o, host):

@@ -200,12 +200,10 @@ static int word_i32(PyObject* t, const char* name, const int32_t** p) {
 
 /* The status word: any int32 tensor with an element; None is NULL. */
 static int status_word(PyObject* t, void** p) {
-  int64_t bytes;
   *p = NULL;
   if (t == Py_None) return 0;
-  if (has_dtype(t, "status", t_i32) < 0 || attr_i64(t, s_nbytes, &bytes) < 0) return -1;
-  if (bytes < 4) return fail(PyExc_ValueError, "%s is empty", "status");
-  return address(t, "status", p);
+  if (has_dtype(t, "status", t_i32) < 0 || address(t, "status", p) < 0) return -1;
+  return *p != NULL ? 0 : fail(PyExc_ValueError, "%s is empty", "status"); /* an empty tensor's address */
 }
 
 static int attr_table(PyObject* o, PyObject* attr, PyObject* type, int dims, int64_t n, void** p, int64_t* shape) {
