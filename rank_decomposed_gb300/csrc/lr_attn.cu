@@ -324,7 +324,10 @@ __device__ __forceinline__ void attn_rows_cta(const AttnParams& p, const RowsLau
     const int r = row0 + rr;
     const int64_t at = base + static_cast<int64_t>(q0 + r / G) * p.n_heads + kvh * G + r % G;
     *reinterpret_cast<float4*>(p.po + at * HD + c * 4) = acc;
-    if (c == 0) p.pml[at] = make_float2(m, l);
+    if (c == 0) {
+      const int sees = prefix ? len : len - n + r / G + 1;
+      p.pml[at] = make_float2(m, l == 0.f && sees > c_lo * kRowsChunk ? -0.f : l);
+    }
   }
 }
 
@@ -346,25 +349,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32)
 // 59, 68; 100 of 56 heads behind 300 (2 slots) 40, 44.
 constexpr int kMaxSlots = 64;  // of each part
 
-// Whether row m, of some sequence, sees a token: asked where all weights are zero.
-// Then none was summed, or all scores are minus infinity, whose softmax is 0 / 0.
-__device__ __noinline__ bool row_sees(const AttnParams& p, int m) {
-  if (prefix_view(p, false) > 0) return true;
-  int b = m;
-  if (p.q_start != nullptr) {  // the last sequence that starts at or before m
-    int end = p.n_seq;
-    for (b = 0; end - b > 1;) {
-      const int mid = b + (end - b) / 2;
-      if (p.q_start[mid] <= m)
-        b = mid;
-      else
-        end = mid;
-    }
-  }
-  const SeqView v = seq_view(p, b, false);
-  return v.len - v.n + (m - v.q0) + 1 > 0;
-}
-
 template <int HD, int W>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p) {
   constexpr int kE = HD / 32;  // elements per lane
@@ -382,10 +366,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     to = p.n_seq > 0 ? p.q_start[p.n_seq] : from;
   }
   // A part without pages has no CTA of the rows kernel: what it holds is looked at here.
-  if (p.cap_own == 0)
-    for (int64_t b = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; b < p.n_seq; b += static_cast<int64_t>(gridDim.x) * 256)
-      seq_view(p, static_cast<int>(b), true);
-  if (p.cap_prefix == 0 && p.prefix_len != nullptr && blockIdx.x == 0 && threadIdx.x == 0) prefix_rows(p, *p.prefix_len, true);
+  if (blockIdx.x == 0 && (p.cap_own == 0 || p.cap_prefix == 0)) {
+    for (int b = threadIdx.x; p.cap_own == 0 && b < p.n_seq; b += 256) seq_view(p, b, true);
+    if (p.cap_prefix == 0 && p.prefix_len != nullptr && threadIdx.x == 0) prefix_rows(p, *p.prefix_len, true);
+  }
   float acc[kE], inv = 0.f;
 #pragma unroll
   for (int j = 0; j < kE; ++j) acc[j] = 0.f;
@@ -421,7 +405,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    inv = l != 0.f ? 1.f / l : (row_sees(p, m) ? NAN : 0.f);  // no visible key: zeros
+    if (l != 0.f) {
+      inv = 1.f / l;
+    } else {  // no visible key: zeros; only keys of score minus infinity: 0 / 0
+      bool none = false;
+      for (int i = lane; i < slots; i += 32) none |= signbit(p.pml[i * rows + r].y);
+      inv = __any_sync(0xffffffffu, none) ? NAN : 0.f;
+    }
   }
   if (W > 1) {
 #pragma unroll

@@ -28,8 +28,8 @@ struct AttnParams {
   int32_t cap_own;            // rows
   // Partial results.  Slot i of row r = m * n_heads + head: numerators
   // po[(i * M * n_heads + r) * head_dim ..], and pml[i * M * n_heads + r] =
-  // (running maximum, sum), sum = 0 where the slot saw no key.  The prefix's
-  // slots come first.
+  // (running maximum, sum), sum = 0 where the slot saw no key, -0 where the keys
+  // that the row sees all scored minus infinity.  The prefix's slots come first.
   float* po;
   float2* pml;
   int32_t prefix_slots, own_slots;

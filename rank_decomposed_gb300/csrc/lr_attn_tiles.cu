@@ -814,6 +814,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool busy = (warp & 3) * 32 < live_rows;  // a warp without rows only keeps the rings moving
       bool ok = true;
+      // a ring without keys waits for nothing else: its Q tile, where the rows are turned
+      // below, may still be on its way here
+      if (my_n == 0) ok = mbar_wait(&bars.q_full, 0, &abort_sh);
       for (int i = 0; i < my_n && ok; ++i) {
         ok = mbar_wait(&bars.s_full[t], i & 1, &abort_sh);
         ok = __all_sync(0xffffffffu, ok);
@@ -947,10 +950,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the ring is the other one's too: its products end before it is written below
         if (ok && joins && t == 1) ok = mbar_wait(&bars.o_done[0], 0, &abort_sh);
         tc_fence_after();
-      } else if (ok) {
-        // a ring without keys waited for nothing: its Q tile, where the rows are turned
-        // below, may still be on its way here
-        ok = mbar_wait(&bars.q_full, 0, &abort_sh);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) {
@@ -1007,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f0 *= inv;
           f1 *= inv;
         } else if (live) {
-          p.pml[at] = make_float2(m, l);
+          p.pml[at] = make_float2(m, l == 0.f && sees ? -0.f : l);
           if (a.two && !dual) p.pml[at + slot_rows] = make_float2(-INFINITY, 0.f);
         }
         const float* other = reinterpret_cast<const float*>(ring) + trow * (HD + 4);
