@@ -32,9 +32,9 @@ namespace {
 // the four join through shared memory.  With 16 rows a tile the products are far
 // from any bound (16 rows use 1/8 of a tcgen05 tile's lanes, hence mma.sync from
 // registers, which needs no TMEM and no second pipeline to start).
-// Measured, cold: one row of 64 heads over 8 behind 16000, 60000, 128000 tokens
-// 26, 52, 93 us with the join (2.5, 4.7, 5.6 TB/s); of 32 over 32 behind 60000
-// 156 us (6.3 TB/s); three short sequences 13 us, all of it latency.
+// Measured with the join, caches cold: one row of 64 heads over 8 behind 16000,
+// 60000, 128000 tokens 26, 52, 95 us (2.5, 4.7, 5.5 TB/s); of 32 over 32 behind 60000
+// 160 us (6.1 TB/s); three short sequences 12 us, 10 with warm caches, all of it latency.
 constexpr int kRowsWarps = 4;
 constexpr int kRowsTile = 16;
 constexpr int kRowsChunk = 16;
@@ -509,11 +509,14 @@ constexpr int kMostHeads = 64;  // query heads a key head: a tile has two query 
 // The rows kernel takes 3.7 us for each wave of CTAs (two an SM with heads of 128,
 // four with 64) and reads the keys once for every 16 rows, 512 bytes for a key of
 // 128 elements, from L2 at 8 TB/s (16e3 keys a us).  It is taken when that comes
-// to 12 us at most, and always when all rows fit one tile of it.  Measured
-// (rows, tiles), all of 64 heads over 8: 4 rows behind 200 tokens 13, 22 us; 8
-// behind 2000 23, 25; 15 behind 1300 22, 25; 8 behind 16000 45, 32; 94 behind 119
-// 28, 26; 1 behind 128000 93, 102.  100 calls of other shapes agree within 2 us but
-// for one (96 rows in 3 sequences of 32 heads: tiles 30, rows 26).
+// to 12 us at most, and always when all rows fit one tile of it.  Measured on the
+// device, caches cold (rows, tiles), of 64 heads over 8: 4 rows behind 200 tokens 13,
+// 22 us; 8 behind 2000 24, 26; 15 behind 1300 24, 26; 8 behind 16000 40, 33; 94 behind
+// 119 32, 29; 1 behind 128000 95, 95.  Of 8 heads over 2 of 64, on both sides of the
+// choice: 256 rows behind 1500 23, 25, 320 rows 28, 27; 256 behind 2000 26, 26, 320
+// rows 32, 28; 192 behind 3000 26, 26, 256 rows 31, 27.  Calls of other shapes agree
+// within 2 us but for a few that go on tiles and would be quicker by rows: 96 rows in 3
+// sequences of 32 heads 30 for 26, 400 rows of 8 heads of 64 behind 500 28 for 22.
 bool by_rows(int64_t M, int64_t mq, int G, const lr_attn_desc* d, int64_t cap_prefix, int64_t cap_own) {
   const int forced = test_attention_kernel();
   if (forced != 0) return forced == 1;
@@ -726,7 +729,6 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
   p.v = static_cast<const uint16_t*>(c.v);
   p.ld = c.ld;
   p.pool_blocks = c.pool_blocks;
-  p.pool_rows = c.pool_blocks * c.block_rows;
   p.block_rows = c.block_rows;
   p.block_shift = -1;
   for (int i = 4; i < 31; ++i)

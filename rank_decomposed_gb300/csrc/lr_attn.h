@@ -12,7 +12,7 @@ struct AttnParams {
   const uint16_t* k;
   const uint16_t* v;
   int64_t ld;                 // row stride of both pools, elements
-  int64_t pool_rows, pool_blocks;
+  int64_t pool_blocks;
   int32_t block_rows;
   int32_t block_shift;        // log2(block_rows), or -1
   int32_t n_heads, n_kv, group;
