@@ -569,7 +569,9 @@ AttnPlan attn_plan(int64_t M, const lr_attn_desc* d) {
     // with 1, 2, 4 CTAs an SM, one of 32 over 32 behind 60000 167, 156, 155.
     const int64_t want = num_sms() * 2;
     a.prefix_slots = slots_for(static_cast<int64_t>(cdiv(M * G, kRowsTile)) * kv, cap_prefix, want, 128);
-    a.own_slots = d->n_seq == 0 ? 0 : slots_for(larger(d->n_seq * cdiv(mq * G, kRowsTile), cdiv(M * G, kRowsTile)) * kv, cap_own, want, 128);
+    // (rows of no sequence count as if they had one: the workspace's bound goes by rows)
+    const int64_t own_tiles = larger(d->n_seq * cdiv(mq * G, kRowsTile), cdiv(M * G, kRowsTile));
+    a.own_slots = d->n_seq == 0 ? 0 : slots_for(own_tiles * kv, cap_own, want, 128);
   }
   const int64_t rows = M * d->n_heads * (a.prefix_slots + a.own_slots);
   a.ml_off = result_bytes(rows, d->cache.head_dim * 4);
@@ -598,7 +600,8 @@ size_t attn_workspace(int64_t M, const lr_attn_desc* d) {
   const int64_t by_rows = smaller((cap_prefix + 127) / 128, kMaxSlots) + smaller((cap_own + 127) / 128, kMaxSlots);
   const int64_t steps = (cap_prefix + 127) / 128 + (smaller(d->n_seq, pair / 2) * cap_own + 127) / 128;
   const int64_t on_tiles = smaller((steps + kMinSteps - 1) / kMinSteps, kMaxSlots / 2);
-  int64_t most = larger(512 * static_cast<int64_t>(num_sms()), 2 * smaller(R, static_cast<int64_t>(kRowsTile) * d->cache.n_kv_heads));
+  const int64_t one_tile = smaller(R, static_cast<int64_t>(kRowsTile) * d->cache.n_kv_heads);
+  int64_t most = larger(512 * static_cast<int64_t>(num_sms()), 2 * one_tile);
   if (test_attention_kernel() == 1) most = larger(most, 2 * R);
   const int64_t rows = smaller(R * larger(by_rows, on_tiles > 1 ? 2 * on_tiles : 0), most);
   return result_bytes(rows, d->cache.head_dim * 4) + result_bytes(rows, 8);
