@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
       const float* ang = p.cos_sin + static_cast<uint64_t>(static_cast<uint32_t>(at < 0 ? 0 : at)) * static_cast<uint32_t>(p.rot_dim) + sub * 4;
       c = *reinterpret_cast<const float4*>(ang), s = *reinterpret_cast<const float4*>(ang + half);
     };
-    // Normed (but for the row's factor, which is returned) and rotated.
+    // Normed and rotated.  The row's factor goes to the elements before their scale does: a head of zeros
+    // has the factor eps^-1/2 and the scale 2^-120, whose quotient may be infinite.
     auto map = [&](float (&x)[8], const float4& c, const float4& s) {
       if (!F32) {
 #pragma unroll
@@ -566,13 +567,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
           x[j] = w * cv[k] + u * sv[k];
         }
       }
-      return inv;
+      if (NORM && maps) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= inv;
+      }
     };
-    auto largest = [&](const float (&x)[8], float inv) {
+    auto largest = [&](const float (&x)[8]) {
       float m = fmaxf(fabsf(x[0]), fabsf(x[1]));  // (passes a NaN over)
 #pragma unroll
       for (int j = 2; j < 8; j += 2) m = max3(m, fabsf(x[j]), fabsf(x[j + 1]));
-      return NORM && maps ? m * inv : m;
+      return m;
     };
     uint8_t* codes = static_cast<uint8_t*>(p.dst[kind]) + static_cast<int64_t>(head0) * p.head_dim;
     auto keep = [&](uint8_t* d, const float (&x)[8], float unit) {
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
     for (int head = 0; head < kEach && (kEach == 1 || head0 + head < heads); ++head, ++scale, src += p.head_dim * kSize, codes += p.head_dim) {
       old = held_rows > 0 ? *scale : 0.f;
       float top = 0.f, all = 0.f;
-      float x[kRounds][8], inv[kRounds];
+      float x[kRounds][8];
       const bool held = !LONG || total <= a.hold;
       if (held) {
         const uint8_t* from = src + grp * step + o1 * kSize;
@@ -623,8 +627,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
             next_at = __shfl_sync(0xffffffffu, at, ((f + 1 << log_groups) + grp) & 31);
             turn_by(next_at, next_c, next_s);
           }
-          inv[f] = map(x[f], c, s);
-          float m = largest(x[f], inv[f]);
+          map(x[f], c, s);
+          float m = largest(x[f]);
           if (where < 0) m = 0.f;
           if (one) {
             all = fmaxf(all, m);
@@ -693,13 +697,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
           ask(t + (kTogether << log_groups));
 #pragma unroll
           for (int k = 0; k < kTogether; ++k) {
-            const float f = map(y[k], c[k], s[k]);
+            map(y[k], c[k], s[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               if (fabsf(y[k][j]) == INFINITY) y[k][j] = NAN;
-            if (where[k] >= 0) m = fmaxf(m, largest(y[k], f));
+            if (where[k] >= 0) m = fmaxf(m, largest(y[k]));
             if (storing && where[k] >= 0 && lives)
-              keep(codes + static_cast<int64_t>(first_row + t - t0 + (k << log_groups) + grp) * p.ldo[kind], y[k], unit * f);
+              keep(codes + static_cast<int64_t>(first_row + t - t0 + (k << log_groups) + grp) * p.ldo[kind], y[k], unit);
           }
         }
 #pragma unroll
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
 #pragma unroll
         for (int f = 0; f < kRounds; ++f, d += p.ldo[kind] << log_groups) {
           if (f << log_groups >= total) break;
-          if (row0 >= 0 && (counts >> ((f << log_groups) + grp) & 1u) && lives) keep(d, x[f], NORM && maps ? unit * inv[f] : unit);
+          if (row0 >= 0 && (counts >> ((f << log_groups) + grp) & 1u) && lives) keep(d, x[f], unit);
         }
       } else {
         const int live_row = at < 0 ? -1 : row;
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
           const int t = (f << log_groups) + grp;
           const int to = __shfl_sync(0xffffffffu, live_row, t & 31);
           const float unit = power_of(-__shfl_sync(0xffffffffu, e, t & 31));
-          if (t < total && to >= 0 && lives) keep(codes + static_cast<int64_t>(to) * p.ldo[kind], x[f], NORM && maps ? unit * inv[f] : unit);
+          if (t < total && to >= 0 && lives) keep(codes + static_cast<int64_t>(to) * p.ldo[kind], x[f], unit);
         }
       }
     }
