@@ -573,9 +573,9 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
       }
     };
     auto largest = [&](const float (&x)[8]) {
-      float m = fmaxf(fabsf(x[0]), fabsf(x[1]));  // (passes a NaN over)
+      float m = 0.f;  // (passes a NaN over: of NaN alone, zero)
 #pragma unroll
-      for (int j = 2; j < 8; j += 2) m = max3(m, fabsf(x[j]), fabsf(x[j + 1]));
+      for (int j = 0; j < 8; j += 2) m = max3(m, fabsf(x[j]), fabsf(x[j + 1]));
       return m;
     };
     uint8_t* codes = static_cast<uint8_t*>(p.dst[kind]) + static_cast<int64_t>(head0) * p.head_dim;

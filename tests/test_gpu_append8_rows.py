@@ -84,3 +84,19 @@ def test_heads_of_zeros_with_a_norm(hd, br, nkv, least, style, dtype, eps):
     c.check()
 
 
+@pytest.mark.parametrize("hd,br,nkv,least", SIZES)
+@pytest.mark.parametrize("norm,style,dtype", [(True, "half", torch.bfloat16), (False, "pair", torch.float32), (False, "half", torch.bfloat16)])
+def test_rows_of_nan(hd, br, nkv, least, norm, style, dtype):
+    """A row without a finite element counts for nothing in its page's scale: alone, as all of a run, and among others.
+    With a norm one NaN makes a head's row of them."""
+    c = Call(hd, br, nkv, least, norm, style, dtype)
+    run, place = torch.from_numpy(c.run).cuda(), torch.from_numpy(c.place).cuda()
+    k, v = c.heads(c.k), c.heads(c.v)
+    for rows in (run % 3 == 1, place % 7 == 3):     # whole runs; some rows of the others
+        k[rows, 0, 3 if norm else slice(None)] = float("nan")
+        v[rows, 0] = float("nan")
+        k[rows, -1] = float("nan")
+    v[run % 5 == 2] = float("nan")
+    c.check()
+
+
