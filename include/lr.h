@@ -457,7 +457,9 @@ typedef struct {
  * order without gaps, as remap_build lists them; rows that do not (one page met
  * twice, a row twice) leave that page's codes and scales unspecified.
  * A row outside the pool or a position outside [0, max_pos) is skipped and
- * reported as in lr_kv_append; the arguments and checks are otherwise its own. */
+ * reported as in lr_kv_append, and is none of the new rows above: a page without
+ * another one keeps its codes and scales.  The arguments and checks are otherwise
+ * lr_kv_append's. */
 lr_status lr_kv_append8(const void* k, int64_t ldk, const void* v, int64_t ldv, const void* q, int64_t ldq,
                         int32_t n_heads, lr_dtype in_dtype, int64_t M, const int32_t* pos,
                         const int32_t* rows, const int32_t* n_active, const lr_head_map* hm,

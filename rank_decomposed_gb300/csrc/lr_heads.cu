@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
     Mask left = joint ? together : starts;
     // The next runs that fit, or one: tokens m0 .. m0 + total, bit k of `opens` where one starts.
     const int i0 = first_of(left);
-    int m0 = base + i0, total = 0, run_row = -1;
+    int m0 = base + i0, total = 0, run_row = -1, run_rows = 0;
     uint32_t opens = 0;
     while (left != 0) {
       const int i = first_of(left);
@@ -483,7 +483,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
       opens |= 1u << (i - i0);
       total += run;
       left &= left - 1;
-      if (joint) break;
+      if (joint) {
+        run_rows = run;
+        break;
+      }
     }
     if (joint)
       together = left;
@@ -498,12 +501,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
     // Lane k: token m0 + k, its row and the scale of its page.
     const bool one = joint || (opens & (opens - 1)) == 0;
     int row = lane < total ? p.rows[m0 + lane] : -1;
+    int joint_at = 0;  // position of the run's first row
+    if (joint && ROT != ROT_NONE) joint_at = i0 < 32 ? __shfl_sync(0xffffffffu, near, i0) : p.pos[base + i0];
     const bool row_ok = row >= 0 && row < p.pool_rows;
     if (lane < total && !row_ok) report_status(p.status, LR_ERR_REMAP_RANGE);
     if (!row_ok) row = -1;
     const int opener = joint ? 0 : 31 - __clz(opens & (0xffffffffu >> (31 - lane)));  // lane of the run's first token
     const int row0 = joint ? (run_row >= 0 && run_row < p.pool_rows ? run_row : -1) : __shfl_sync(0xffffffffu, row, opener);
-    const int page = row0 < 0 ? 0 : page_of(row0), held_rows = row0 < 0 ? 0 : row0 - page * br;
+    const int page = row0 < 0 ? 0 : page_of(row0);
     float* scale = a.scale[kind - 1] + static_cast<int64_t>(page) * heads + head0;
     float old = 0.f;
 
@@ -601,6 +606,33 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
         at = -1;
       }
     }
+    // Row of the run's first token that counts, -1 if none does: rows before it are the page's
+    // earlier ones, and a run that counts for nothing leaves its page alone.
+    int first_row = row0;
+    if (ROT != ROT_NONE) {
+      auto lead_of = [&](int from, int n) {  // of n tokens of one run: how many are before the first that counts
+        for (int t = 0; t < n; t += 32) {
+          const int x = t + lane < n ? p.pos[from + t + lane] : -1;
+          const uint32_t counts = __ballot_sync(0xffffffffu, x >= 0 && x < p.max_pos);
+          if (counts != 0) return t + __ffs(counts) - 1;
+        }
+        return -1;
+      };
+      const uint32_t counts = __ballot_sync(0xffffffffu, at >= 0 && row >= 0);
+      int lead = 0;
+      if (joint) {
+        if (joint_at < 0 || joint_at >= p.max_pos) lead = lead_of(base + i0, run_rows);
+      } else if (LONG && total > 32) {
+        if ((counts & 1u) == 0) lead = lead_of(m0, total);
+      } else if (counts != __ballot_sync(0xffffffffu, row >= 0)) {
+        const uint32_t later = opens & ~((2u << opener) - 1);  // (of lane 31 none)
+        const int end = later != 0 ? __ffs(later) - 1 : total;
+        const uint32_t mine = counts >> opener << opener & (end < 32 ? (1u << end) - 1 : ~0u);
+        lead = mine != 0 ? __ffs(mine) - 1 - opener : -1;
+      }
+      if (lead != 0) first_row = lead < 0 || row0 < 0 ? -1 : row0 + lead;
+    }
+    const int held_rows = first_row < 0 ? 0 : first_row - page * br;
     // (what the lanes know of the rows serves several heads)
 #pragma unroll 1
     for (int head = 0; head < kEach && (kEach == 1 || head0 + head < heads); ++head, ++scale, src += p.head_dim * kSize, codes += p.head_dim) {
@@ -650,10 +682,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 4) append8_kernel(const __g
         }
         e = e < kLeast8 ? kLeast8 : (e > 120 ? 120 : e);  // (a scale that was none)
         // the codes of the rows before a run, anew
-        const bool opens_run = joint ? lane == 0 && row0 >= 0 : lane == opener && lane < total && row_ok;
+        const bool opens_run = first_row >= 0 && (joint ? lane == 0 : lane == opener && lane < total);
         for (uint32_t left = __ballot_sync(0xffffffffu, grows && opens_run); left != 0; left &= left - 1) {
           const int who = __ffs(left) - 1;
-          const int first = joint ? row0 : __shfl_sync(0xffffffffu, row, who), rows = first - page_of(first) * br;
+          const int first = joint ? first_row : __shfl_sync(0xffffffffu, first_row, who), rows = first - page_of(first) * br;
           const int less = (static_cast<int>(__float_as_uint(__shfl_sync(0xffffffffu, old, who)) >> 23 & 0xFFu) - 127) - __shfl_sync(0xffffffffu, e, who);
           const float f = power_of(less < -126 ? -126 : less);
           for (int t = grp + (joint ? part << log_groups : 0); t < rows && lives; t += joint ? kAppendWarps << log_groups : groups) {

@@ -100,3 +100,14 @@ def test_rows_of_nan(hd, br, nkv, least, norm, style, dtype):
     c.check()
 
 
+@pytest.mark.parametrize("hd,br,nkv,least", SIZES)
+@pytest.mark.parametrize("norm,style,dtype", [(True, "half", torch.bfloat16), (False, "pair", torch.float32), (False, "half", torch.bfloat16)])
+def test_skipped_rows_are_none_of_a_page_s_new_rows(hd, br, nkv, least, norm, style, dtype):
+    """Positions out of range: the first row of a run, its first ones, all of them.  A page without a new row keeps its
+    scales, and in one whose first rows are skipped those before the first new one keep what they stand for."""
+    c = Call(hd, br, nkv, least, norm, style, dtype)
+    for i, (page, at, n) in enumerate(c.runs):
+        rows = np.flatnonzero(c.run == i)
+        bad = {0: rows, 1: rows[:1], 2: rows[:3], 3: rows[:0], 4: rows[:-1], 5: rows[1::2], 6: rows[:40]}[i * 5 % 7]
+        c.pos[bad] = 5000 if i % 2 else -1
+    c.check(lr.LR_ERR_INDEX_RANGE)
