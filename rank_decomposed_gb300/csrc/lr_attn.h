@@ -121,8 +121,11 @@ __device__ __forceinline__ int prefix_rows(const AttnParams& p, int len, bool te
   if (tell && n != len && p.status != nullptr) atomicCAS(p.status, 0, LR_ERR_INDEX_RANGE);
   return n;
 }
+// (a length that is given without pages has the capacity 0)
 __device__ __forceinline__ int prefix_view(const AttnParams& p, bool tell) {
-  return p.cap_prefix > 0 ? prefix_rows(p, *p.prefix_len, tell) : 0;
+  if (p.cap_prefix > 0) return prefix_rows(p, *p.prefix_len, tell);
+  if (tell && p.prefix_len != nullptr) prefix_rows(p, *p.prefix_len, true);
+  return 0;
 }
 
 // Rows of no sequence come out zero: CTA `item` of `items` takes every items-th row of q.

@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     q0 = v.q0, nq = v.nq, n = v.n, len = v.len;
     own_pages += static_cast<int64_t>(b) * p.blocks_per_seq;
     row0 = (tile - b * rl.tiles[1]) * kTile;
-    if (WIN) P = prefix_view(p, tell);
+    if (WIN)
+      P = prefix_view(p, tell);
+    else if (p.direct)
+      prefix_view(p, tell);  // (no pages of it; no join looks at a length that is given all the same)
   }
   if (p.direct && kvh == 0 && split == 0) zero_rows(p, tile, p.n_seq * rl.tiles[1], HD, kWarps * 32);
   n_rows = nq * G - row0;
