@@ -569,9 +569,9 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
  *   lr_prefix_attention_workspace_bytes.
  *   What is not said here is as there, but for the arithmetic over 8 bits.  An
  *   element of a query counts to 2^-39 of its row's largest (those above 2^-28 of
- *   it, exactly); probabilities round to f16, whose small ones, under 2^-14 of the
+ *   it, exactly); probabilities round to f16, whose small ones, under 2^-21 of the
  *   largest product of a probability and a page's scale of V, keep a multiple of
- *   2^-24 of it; values of a page whose scale of V is under 2^-60 keep a multiple of
+ *   2^-31 of it; values of a page whose scale of V is under 2^-60 keep a multiple of
  *   2^-84.  The V scales of one head are to lie within 2^100 of each other, any under
  *   2^-60 counting as that (keys of a smaller one may be lost from the sum).
  *   Without a window and scales it is lr_prefix_attention. */

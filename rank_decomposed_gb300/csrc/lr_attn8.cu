@@ -7,10 +7,11 @@
 //     to 2^14: exact but for elements under 2^-28 of it.  Back with the page's
 //     scale: s = scale log2(e) 2^x ks (code . q).
 //   O = P V:  the page's scale of V, 2^ev, goes into the powers, which keep a
-//     reference mo of their own: P' = 2^(s + ev - mo) <= 2^8 for the product,
-//     O = sum P' code, and P = 2^(s - m) for the sum l = sum P.  out = 2^(mo - m)
-//     O / l.  (With the scale left in V, a page of large values that no row attends
-//     to would push the others' powers under what f16 holds.)
+//     reference mo of their own, 7 below the largest s + ev: P' = 2^(s + ev - mo) <= 2^15
+//     for the product, O = sum P' code, and P = 2^(s - m) for the sum l = sum P.
+//     out = 2^(mo - m) O / l.  (With the scale left in V, a page of large values that no
+//     row attends to would push the others' powers under what f16 holds; with the largest
+//     power at 1, the tail of a long context beside a few keys that take the most.)
 //
 // Bound by the bytes of K and V.  A CTA takes 8 NT rows (query rows times the heads
 // of one key head) and a range of keys; each of its four warps walks chunks of 16
@@ -22,7 +23,7 @@
 // elements in the reduction is free, Q has the same), and 16 neighbouring codes of
 // four keys for O.
 // Roundings: Q to f16 (above), powers to f16, whose error of 2^-11 is an eighth of
-// bf16's; scores, maxima, sums and O are fp32.
+// bf16's (below 2^-21 of the largest, 2^-32 of that); scores, maxima, sums and O are fp32.
 //
 // Measured with the join, heads of 128, 64 over 8: one sequence of 131000 tokens 57 us
 // (268 MB: 4.7 TB/s, 0.70 of the copy rate), 64 of 300 to 6000 84 us (415 MB, 4.9 TB/s,
@@ -48,6 +49,7 @@ constexpr int kWarps = 4;
 constexpr int kChunk = 16;
 constexpr int kStages = 3;
 constexpr float kSlack = 8.f;  // how far powers may pass their reference before it moves
+constexpr float kLift = 7.f;   // powers for the product are 2^kLift times as large: 2^15 at most
 
 template <int HD, int NT>
 constexpr int smem8() {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float limit = kSlack + fminf(m[t][r], mo[t][r] - ev);
+        const float limit = kSlack + fminf(m[t][r], mo[t][r] + (kLift - ev));
         move |= s[t][r] > limit || s[t][r + 2] > limit;
       }
     if (__any_sync(0xffffffffu, move)) {
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
           float top = fmaxf(s[t][r], s[t][r + 2]);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          const float now = fmaxf(m[t][r], top), now_o = fmaxf(mo[t][r], top + ev);
+          const float now = fmaxf(m[t][r], top), now_o = fmaxf(mo[t][r], top + (ev - kLift));
           const float f = now == -INFINITY ? 1.f : ex2(m[t][r] - now);
           const float fo = now_o == -INFINITY ? 1.f : ex2(mo[t][r] - now_o);
           m[t][r] = now, mo[t][r] = now_o;
@@ -502,8 +504,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       sum += ex2(st.x - ref) * st.y;
       any |= st.w != 0.f;
       if (st.z == -INFINITY) continue;  // nothing was summed
-      const float f = exp2f(st.z - ref);
-      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm) + (w * kTile + rr) * (HD + 4) + d * 4);
+      // (the lift apart: with it 2^(mo - m) of the smallest scale would be subnormal)
+      const float f = exp2f(st.z + kLift - ref);
+      float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm) + (w * kTile + rr) * (HD + 4) + d * 4);
+      constexpr float kLower = 1.f / (1 << static_cast<int>(kLift));
+      v.x *= kLower, v.y *= kLower, v.z *= kLower, v.w *= kLower;
       acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
     }
     const int r = row0 + rr;

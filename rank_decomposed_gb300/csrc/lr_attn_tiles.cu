@@ -81,9 +81,10 @@
 // through the loading warps: the copies bring a tile to a place of each thread's own, three
 // tiles ahead, and it is stored from there.  Q becomes f16 with one power of two a row,
 // whose inverse and the page's scale of K go to the scores; P is f16 with the page's power of
-// two of V in it: P = 2^(s + ev - m), O = sum P Vc, l = sum P 2^-ev.  The roundings beside
-// bf16's: Q's elements under 2^-28 of the row's largest, by 2^-39 of it; P to f16 (2^-11;
-// below 2^-14 of the largest product of a power and a scale, 2^-25 of it).
+// two of V in it, and 7 more, for the tail of a long context: P = 2^(s + ev - m + 7),
+// O = sum P Vc, l = sum P 2^-ev.  The roundings beside bf16's: Q's elements under 2^-28 of
+// the row's largest, by 2^-39 of it; P to f16 (2^-11; below 2^-21 of the largest product of
+// a power and a scale, 2^-32 of it).
 // Measured: the 12 ragged turns 314 us (bf16 247), 64 sequences behind 8192 55 (44): the
 // conversions stand in the loading warps' way (some 590 cycles of a step's 4000 are waits for K)
 // and in the softmax's (their instructions and the powers share the schedulers).  K as it lies in
@@ -131,6 +132,7 @@ constexpr int kKeys = 128;           // keys per tile
 constexpr int kPage = 16;            // rows of a page, at least
 constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 each), O0, O1 (head_dim each)
 constexpr float kSlack = 8.f;
+constexpr float kLift = 7.f;         // over codes powers are 2^kLift times as large: 2^15 at most
 
 template <int HD, bool Q8>
 struct Shape {
@@ -1219,8 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if ((use >> g & 1u) == 0) tops[g] = -INFINITY;
           }
           // What a score of each group counts, and the exponent that its powers have beside it:
-          // over codes P = 2^(s + ev - m) is of V's codes, and the sum l = sum 2^(s - m), by
-          // the same m, is of 2^-ev times as much.
+          // over codes P = 2^(s + ev - m + kLift) is of V's codes, and the sum l = sum 2^(s - m + kLift),
+          // by the same m, is of 2^-ev times as much.
           float unit[8], ev[8];
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
@@ -1254,7 +1256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float neg = mref == -INFINITY ? 0.f : -mref;
+          const float neg = mref == -INFINITY ? 0.f : (Q8 ? kLift - mref : -mref);
           const uint64_t scale2 = pack2(back, back), neg2 = pack2(neg, neg);
           uint64_t part[8];  // of each group
 #pragma unroll

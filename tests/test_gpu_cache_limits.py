@@ -34,3 +34,35 @@ def test_a_prefix_length_is_reported_where_there_are_no_prefix_pages(kernel, len
         assert int(b.status.item()) == lr.LR_ERR_INDEX_RANGE, bad
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("qs", [None, [40, 33, 70]])
+@pytest.mark.parametrize("prefix", [0, 160])
+def test_small_weights_beside_a_large_one(kernel, prefix, qs, hd):
+    """In every 16 keys one of weight 1 and value 0 and 15 of weight e^-18 and value 1.  Such a weight is 2^-25.97, and an
+    f16 of it times 2^7 is a multiple of 2^-24, off by 2^-25 at most: the sum of 15 by 15 / 16 of 2^-32 of the weights of 1.
+    (A reference that lags behind the maximum only leaves more bits.)"""
+    b = Cached(51, 8, 2, hd, prefix, [64, 160, 320], qs=qs)
+    b.q.fill_(0)
+    b.q.view(b.m, 8, hd)[:, :, 0] = 1.0
+    for codes, scale in ((b.k8, b.ks), (b.v8, b.vs)):
+        scale.fill_(1.0)
+        codes.view(torch.uint8).zero_()
+    k, v = (x.view(torch.uint8).view(b.pages, 16, 2, hd) for x in (b.k8, b.v8))
+    code = lambda x: int(torch.tensor(x).to(F8).view(torch.uint8))  # noqa: E731
+    k[:, 3, :, 0] = code(18.0)
+    v[:] = code(1.0)
+    v[:, 3] = 0
+    out = torch.empty(b.m, 8 * hd, device="cuda")
+    b.run(out=out, scale=1.0)
+    assert int(b.status.item()) == 0
+    want, mag = b.want(scale=1.0)
+    if qs is None:   # (rows of turns end inside a group)
+        w = np.exp(-18.0)
+        assert np.allclose(want, 15 * w / (1 + 15 * w), rtol=1e-12)
+    large = np.exp(-18.0) * np.ones_like(want)
+    sees = want > 0.5                                 # a row that sees no key of weight 1 is exactly 1
+    off = np.abs(_f64(out) - want)
+    assert np.all(off[~sees] <= (18 * 2.0 ** -32 + 2.0 ** -10 * (mag + large))[~sees]), float(off[~sees].max())
+    assert np.all(off[sees] <= 2.0 ** -10)
+
+
