@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     int e = top > 0.f ? 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23) : 0;
-    e = e > 126 ? 126 : e;
+    e = e > 126 ? 126 : e;  // (bf16 is a multiple of 2^-133, so that nothing rounds where this holds)
     const float f = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 #pragma unroll
     for (int j = 0; j < kPieces; ++j)

@@ -1093,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t top = (top2 & 0xFFFFu) > top2 >> 16 ? top2 << 16 : top2 & 0xFFFF0000u;
         int e = static_cast<int>(top >> 23) - 127 - 14;
-        e = e < -120 ? -120 : e;
+        e = e < -120 ? -120 : e;  // (bf16 is a multiple of 2^-133, so that nothing rounds where this holds)
         const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
         // an infinite or NaN element leaves no score of the row a number, nor its softmax

@@ -66,3 +66,16 @@ def test_small_weights_beside_a_large_one(kernel, prefix, qs, hd):
     assert np.all(off[sees] <= 2.0 ** -10)
 
 
+@pytest.mark.parametrize("kexp,vexp", [(124, 0), (124, -112), (-112, 100)])
+@pytest.mark.parametrize("qs", [None, [60, 33, 3]])
+def test_queries_and_scales_at_the_ends_of_the_range(kernel, qs, kexp, vexp):
+    """Scales of K of some 2^118 under queries of 2^-124, bf16's subnormal numbers among them, and the reverse."""
+    b = Cached(52, 8, 2, 128, 64, [90, 80, 200], qs=qs, sizes=0)
+    b.ks *= 2.0 ** kexp
+    b.vs *= 2.0 ** vexp
+    q = b.q.float() * torch.exp2(-12.0 * (torch.arange(b.q.shape[1], device="cuda") % 2))   # every second one 2^-12 of it
+    b.q = (q * 2.0 ** -kexp).bfloat16()
+    out = torch.empty(b.m, 1024, device="cuda")
+    b.run(out=out)
+    assert int(b.status.item()) == 0
+    close(out, *b.want(), f32=True)
