@@ -1347,7 +1347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = trow < live_rows;
       if (busy) {
         const uint32_t o_at = tmem + 256 + t * HD + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const bool both = joins && n1 > 0;
+        // (a packed row of no sequence is not joined: its numerators may be NaN)
+        const bool both = joins && n1 > 0 && (WHOLE || my_seq >= 0);
         float f0 = 1.f, f1 = 0.f, m = mref, l = sum;
         if (both) {
           const float2 o = hand_ml[trow];

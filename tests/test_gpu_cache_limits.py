@@ -79,3 +79,18 @@ def test_queries_and_scales_at_the_ends_of_the_range(kernel, qs, kexp, vexp):
     b.run(out=out)
     assert int(b.status.item()) == 0
     close(out, *b.want(), f32=True)
+
+
+@pytest.mark.parametrize("eight,window", [(True, 0), (False, 0), (True, 300)])
+@pytest.mark.parametrize("prefix", [129, 272, 700])
+@pytest.mark.parametrize("hd,nh,nkv,lens,qs", [(128, 3, 3, [20], None), (64, 40, 5, [0, 7], None), (128, 8, 1, [80, 1], [0, 1]),
+                                               (64, 8, 2, [60, 30, 5], [50, 30, 5])])
+def test_padding_rows_behind_a_prefix_of_several_tiles(kernel, hd, nh, nkv, lens, qs, prefix, eight, window):
+    """Queries of NaN in rows of no sequence, whose results are joined from several parts of the prefix: zeros."""
+    b = Cached(53, nh, nkv, hd, prefix, lens, qs=qs, eight=eight, window=window)
+    pad = torch.full((3, nh * hd), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((b.m + 3, nh * hd), 7.0, device="cuda")
+    b.run(out=out, q=torch.cat([b.q, pad]))
+    assert int(b.status.item()) == 0
+    assert not out[b.m:].any()
+    close(out[:b.m], *b.want(), f32=True, eight=eight)
