@@ -774,6 +774,18 @@ struct CachePlan {
 // to 6000 tokens 85, 83, 87 us, 32 of 1000 to 4000 with 32 key heads 113, 115, 127.
 constexpr int kRangeKeys = 1536;
 
+// Costs in us of a call by rows (as it is, of a key for tiles of 8, 16, 32 rows, of a row tile's start at
+// two an SM) and on tiles (as it is, a CTA, a step of packed rows over shared and over own
+// tokens, a step of whole turns, the part of a step that does not go by the size of a head), and
+// of a join (its launch, a megabyte of results).
+struct CacheCosts {
+  double rows, key[3], start[3], rows_join, rows_results;
+  double tiles, cta, shared_step, own_step, whole_step, narrow, tiles_join, tiles_results;
+};
+constexpr CacheCosts kCosts8 = {6.0, {1 / 31e3, 1 / 20e3, 1 / 12.5e3}, {1.0, 2.8, 8.5}, 4.0, 1.5, -1.5, 10.5, 2.0, 2.2, 2.3, 0.6, 3.4, 0.7};
+// (bf16 with a window: row tiles of 16, whole turns)
+constexpr CacheCosts kCosts16 = {4.7, {0.0, 1 / 15.7e3, 0.0}, {0.0, 2.35, 0.0}, 3.0, 1.25, -0.5, 8.0, 0.0, 0.0, 2.35, 0.4, 2.7, 0.45};
+
 // Partial results of a call are no more than this many rows, so that a workspace of
 // them serves every call.
 int64_t most_rows() { return 512 * static_cast<int64_t>(num_sms()); }
@@ -821,34 +833,44 @@ CachePlan cache_plan(int64_t M, const lr_cache_attn_desc* x) {
   const int by_rows1 = cut(own_ctas, listed(mq), larger(1, room - by_rows0));
   const bool direct = by_rows0 == 0 && by_rows1 == 1;
   // Rows or tiles, by two costs in us.  By rows a key of 128 elements is read once for
-  // a row tile, over 8 bits by 1, 2 or 4 groups of eight rows at an equal price each, and
-  // every row tile costs its start.  A step of a tile pair takes 2 us of an SM.  Fitted to 188
-  // calls without a window (1 to 256 sequences of 1 to 300 rows, contexts of 200 to 32000
-  // tokens, three head layouts; 0.6 % over the faster kernel of each on average, 40 % at
-  // most) and, with the join's launch and the start of a CTA on tiles counted, to 168 with
-  // windows of 100 and 1024 (1.6 %, 35 % at most; each kind of cache by itself).
+  // a row tile, at a price that goes by the tile's rows, and every row tile costs its start.
+  // On tiles a CTA has its start and its results, and steps, which hardly get shorter with
+  // smaller heads.  A join costs its launch and the results that it reads.  Fitted to 2400
+  // calls (1 to 256 sequences of 1 to 100 rows, contexts of 5 to 16000 tokens, prefixes up to
+  // 8192, six head layouts, windows of 100 to 1024 and none).  Of 1800 others the kernel taken
+  // is over the faster one by 1.3 % on average and 84 % at most (21 us for 12) over 8 bits, with
+  // a window by 2.0 and 46 %, over bf16 with a window by 0.4 and 17 %.  (A price of 2 us for
+  // every step, whatever it holds, and none for a CTA: 256 sequences of 700 tokens in 8 bits 168
+  // us on tiles, so 71 by rows; 256 of 200, 32 heads, a window of 100 over bf16 471, so 139.)
+  const CacheCosts& k = c.eight ? kCosts8 : kCosts16;
   const double wide = d->cache.head_dim / 128.0, sms = num_sms();
+  const int kind = tile == 8 ? 0 : (tile == 16 ? 1 : 2);
+  auto join_cost = [&](double launch, double each, int64_t slots) {
+    return launch + each * 1e-6 * static_cast<double>(R * slots * d->cache.head_dim * 4);
+  };
   const double shared_tiles = static_cast<double>(cdiv(M * G, tile)) * kv, own_tiles = static_cast<double>(own_ctas);
   const double read = (shared_tiles * static_cast<double>(shared) + own_tiles * static_cast<double>(listed(mq))) * wide;
   const double started = (shared > 0 ? shared_tiles : 0.0) + own_tiles;
-  double rows_cost = c.eight ? read * (tile / 8.0) / 20e3 + 3.0 * started / (2 * sms) : read / 20e3 + 2.0 * started / (2 * sms);
-  const double pairs = static_cast<double>(a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv;
-  double tiles_cost;
-  if (win) {
-    const double waves = pairs / sms < 1.0 ? 1.0 : pairs / sms, walk = static_cast<double>(steps) * wide;
-    rows_cost = 0.8 * rows_cost + (direct ? 0.0 : 6.0);
-    tiles_cost = c.eight ? 1.4 * waves * (walk + 6.0) - 4.0 : 1.4 * waves * walk + 8.0;
-  } else {
-    const double busy = pairs * static_cast<double>(steps) * wide / sms;
-    tiles_cost = (c.eight ? 4.0 : 14.0) + 2.0 * (busy < 1.0 ? 1.0 : busy);
-  }
+  const double rows_cost = k.rows + k.key[kind] * read + k.start[kind] * started / (2 * sms) +
+                           (direct ? 0.0 : join_cost(k.rows_join, k.rows_results, by_rows0 + by_rows1));
+  AttnPlan on_tiles = a;
+  cut_tiles(on_tiles, M, d, steps);
+  const int64_t slots = on_tiles.tile_slots;
+  const double ctas = static_cast<double>((a.whole ? d->n_seq * cdiv(mq, pair) : cdiv(M, pair)) * kv * slots);
+  const double waves = ctas < sms ? 1.0 : ctas / sms;
+  const int64_t own_steps = cdiv(smaller(d->n_seq, cdiv(pair / 2, mq)) * cap_own, 128);  // of packed rows, a ring's
+  const double walk = a.whole ? k.whole_step * static_cast<double>(steps)
+                              : k.shared_step * cdiv(cap_prefix, 128) + k.own_step * static_cast<double>(own_steps);
+  const double tiles_cost = k.tiles + waves * (k.cta + (k.narrow + (1.0 - k.narrow) * wide) * walk / static_cast<double>(slots)) +
+                            (slots > 1 ? join_cost(k.tiles_join, k.tiles_results, slots) : 0.0);
   const int forced = test_attention_kernel();
-  a.tiles = forced ? forced == 2 : M * G > 16 && rows_cost > tiles_cost;
+  bool tiles = forced ? forced == 2 : M * G > 16 && rows_cost > tiles_cost;
   // two parts, each with one result a row, are more than the workspace holds
-  if (forced == 0 && shared > 0 && 2 * R > most_rows()) a.tiles = true;
-  if (win && d->n_seq == 0) a.tiles = false;  // no sequence, no tile
-  if (a.tiles) {
-    cut_tiles(a, M, d, steps);
+  if (forced == 0 && shared > 0 && 2 * R > most_rows()) tiles = true;
+  if (win && d->n_seq == 0) tiles = false;  // no sequence, no tile
+  if (tiles) {
+    a = on_tiles;
+    a.tiles = true;
   } else {
     a.whole = false;
     a.prefix_slots = by_rows0;
