@@ -25,15 +25,18 @@
 // Roundings: Q to f16 (above), powers to f16, whose error of 2^-11 is an eighth of
 // bf16's (below 2^-21 of the largest, 2^-32 of that); scores, maxima, sums and O are fp32.
 //
-// Measured with the join, heads of 128, 64 over 8: one sequence of 131000 tokens 57 us
-// (268 MB: 4.7 TB/s, 0.70 of the copy rate), 64 of 300 to 6000 84 us (415 MB, 4.9 TB/s,
-// 0.74), 256 of 100 to 1500 79 us.  A copy of the kernel that only loads takes 126 of 144 us
+// Measured with the join, heads of 128, 64 over 8: one sequence of 131000 tokens 59 us
+// (268 MB: 4.5 TB/s, 0.68 of the copy rate), 64 of 300 to 6000 86 us (415 MB, 4.8 TB/s,
+// 0.72), 256 of 100 to 1500 78 us.  A copy of the kernel that only loads takes 126 of 144 us
 // for 64 sequences of 6000: ranges start with three trips to memory one after another
 // (lengths, pages, keys), and four CTAs an SM hide part of them.  Two stages a warp
 // and five CTAs, four stages and three: even.  Products by m16n8k32 on the codes as they
 // are, with Q as two e4m3 parts: even (what the conversions save, the second part costs).
 // Several rows a key head in the other operand's eight columns: 16 and 32 rows a CTA cost
-// two and four times the products, and are chosen where that many rows share the keys.
+// two and four times the products, and are chosen where that many rows share the keys (32
+// rows of heads of 128 take 255 registers and spill 180 to 330 bytes).  One width serves both
+// parts of a launch: behind a short prefix that many sequences share, the own tokens' CTAs
+// have the prefix's width, too.
 #include <cuda_fp16.h>
 
 #include <cmath>

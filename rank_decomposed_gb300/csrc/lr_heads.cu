@@ -297,12 +297,18 @@ __global__ void __launch_bounds__(kHeadWarps * 32, kHeadCtas) heads_kernel(const
 // remain.
 //
 // Bound by memory in bytes (4099 rows of 32 + 32 heads: 101 MB and the angles, 15 us), but a
-// head takes 1190 instructions a warp of 16 rows, behind several trips to memory one after
-// another (rows, positions, elements and angles, the page's scale), and 126 registers leave
-// room for 16 warps an SM: 37 us, 2.7 TB/s (with one head a warp 41, 38 % of the issue slots).
-// 64 rows of a decode step with their queries 5 us.  In pages of 64 rows the 4099 take 59 us
-// (walked twice, 93), 777 fp32 rows of 2 heads of 64 8 (19), 300 of 8 + 8 heads 8 (38), the
-// decode step 5 (5).  Others measured for the 4099 rows in pages of 16: a warp a run
+// head takes 1200 instructions a warp of 16 rows, behind several trips to memory one after
+// another (rows, positions, elements and angles, the page's scale), and 128 registers leave
+// room for 16 warps an SM: 37.5 us, 2.7 TB/s, 36 % of the issue slots (with one head a warp
+// 41); with norms 45.  64 rows of a decode step with their queries 5 us.  In pages of 64 rows
+// the 4099 take 52 us (walked twice, 93), with norms 59, in pages of 256, which are walked, 128
+// and 175; 777 fp32 rows of 2 heads of 64 in pages of 64 8 (walked, 19), 300 of 8 + 8 heads
+// 8.5 (38), the decode step 5 (5).  These are calls in turn over pages whose scales have grown
+// before; where every page's scale grows, so that the codes before the new rows are made anew,
+// and caches are flushed the 4099 take 48 us (43 without), the decode step 14 (10).  With norms
+// the rotated variants spill (a warp's runs 8 to 124 bytes, teams 110 to 220, walked pages 670 to
+// 1360), without them the walked ones (270 to 640) alone.
+// Others measured for the 4099 rows in pages of 16: a warp a run
 // without windows 56; eight warps a page with a barrier a head 84; the elements in shared
 // memory and two walks 48 to 57; elements held as they were loaded and mapped twice 42 to 48.
 struct AppendParams {
@@ -939,7 +945,7 @@ lr_status launch_append8(AppendParams& a, const lr_head_map* hm, lr_dtype in_dty
   const int64_t windows = (static_cast<int64_t>(p.M) + a.window - 1) / a.window;
   // Two heads a warp share what it finds out about its rows, where enough warps remain: 4099 rows
   // of 32 + 32 heads 41 us, so 37.5.  Not with norms, whose gains and sums take the registers
-  // (16000 rows 171, so 174).
+  // (16000 rows of 32 + 32 heads 171, so 174).
   if (how == kByWarp && !hm->norm && windows * 2 * ((kv + 1) / 2) >= want) how = kByWarpTwo;
   const int64_t blocks = (windows * 2 * (how == kByWarpTwo ? (kv + 1) / 2 : kv) + each - 1) / each;
   if (q_blocks + blocks > 0x7FFFFFFF / kAppendWarps) return bad(LR_ERR_UNSUPPORTED, "heads: too many rows and heads for one launch");
