@@ -573,9 +573,9 @@ lr_status lr_prefix_attention(const void* q, int64_t ldq, void* out, int64_t ldo
  *   largest product of a probability and a page's scale of V, keep a multiple of
  *   2^-31 of it; values of a page whose scale of V is under 2^-60 keep a multiple of
  *   2^-84.  The V scales of one head are to lie within 2^100 of each other, any under
- *   2^-60 counting as that (keys of a smaller one may be lost from the sum); a row's
- *   largest finite query element times a scale of K times `scale` is to lie under
- *   2^128 (its scores may be NaN beyond).
+ *   2^-60 counting as that (keys of a smaller one may be lost from the sum).  Scores,
+ *   scale q . k, are to lie under 2^22, and a row's largest finite query element times
+ *   a scale of K times `scale` under 2^128 (beyond, weights may be wrong or NaN).
  *   Without a window and scales it is lr_prefix_attention. */
 typedef struct {
   lr_attn_desc base;

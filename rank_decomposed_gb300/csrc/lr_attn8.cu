@@ -7,11 +7,12 @@
 //     to 2^14: exact but for elements under 2^-28 of it.  Back with the page's
 //     scale: s = scale log2(e) 2^x ks (code . q).
 //   O = P V:  the page's scale of V, 2^ev, goes into the powers, which keep a
-//     reference mo of their own, 7 below the largest s + ev: P' = 2^(s + ev - mo) <= 2^15
-//     for the product, O = sum P' code, and P = 2^(s - m) for the sum l = sum P.
-//     out = 2^(mo - m) O / l.  (With the scale left in V, a page of large values that no
-//     row attends to would push the others' powers under what f16 holds; with the largest
-//     power at 1, the tail of a long context beside a few keys that take the most.)
+//     reference of their own, m + dv, 7 below the largest s + ev: P' = 2^((s - m) + (ev - dv))
+//     <= 2^15 for the product, O = sum P' code, and P = 2^(s - m) for the sum l = sum P.
+//     out = 2^dv O / l.  (With the scale left in V, a page of large values that no row
+//     attends to would push the others' powers under what f16 holds; with the largest power
+//     at 1, the tail of a long context beside a few keys that take the most.  Scores enter by
+//     their differences alone: a reference s + ev loses the scale beside scores of 2^24.)
 //
 // Bound by the bytes of K and V.  A CTA takes 8 NT rows (query rows times the heads
 // of one key head) and a range of keys; each of its four warps walks chunks of 16
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   constexpr int kSteps = HD / 16;          // of the reduction over the head; tiles of 16 of its elements
   constexpr uint32_t kBytes = kChunk * HD; // of a chunk's K or V
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ float4 stats[kWarps][kTile];           // m, l, mo, whether a key was seen
+  __shared__ float4 stats[kWarps][kTile];           // m, l, dv, whether a key was seen
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -257,13 +258,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
   }
 
   float o[NT][kSteps][4];  // elements 16 g + 2 i, + 1 (in steps of two) of rows 2c, 2c + 1
-  float m[NT][2], mo[NT][2], l[NT][2];
+  float m[NT][2], dv[NT][2], l[NT][2];
   uint32_t saw = 0;  // bit 2 t + i: a key of that row
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-    m[t][0] = m[t][1] = mo[t][0] = mo[t][1] = -INFINITY;
+    m[t][0] = m[t][1] = dv[t][0] = dv[t][1] = -INFINITY;  // (no key yet)
     l[t][0] = l[t][1] = 0.f;
   }
 
@@ -401,8 +402,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float limit = kSlack + fminf(m[t][r], mo[t][r] + (kLift - ev));
-        move |= s[t][r] > limit || s[t][r + 2] > limit;
+        const float base = m[t][r] == -INFINITY ? 0.f : m[t][r];
+        const float limit = kSlack + fminf(0.f, dv[t][r] + (kLift - ev));
+        move |= s[t][r] - base > limit || s[t][r + 2] - base > limit;
       }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -412,10 +414,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
           float top = fmaxf(s[t][r], s[t][r + 2]);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          const float now = fmaxf(m[t][r], top), now_o = fmaxf(mo[t][r], top + (ev - kLift));
-          const float f = now == -INFINITY ? 1.f : ex2(m[t][r] - now);
-          const float fo = now_o == -INFINITY ? 1.f : ex2(mo[t][r] - now_o);
-          m[t][r] = now, mo[t][r] = now_o;
+          const float now = fmaxf(m[t][r], top);
+          const bool none = now == -INFINITY;
+          const float less = none ? 0.f : m[t][r] - now, as_was = dv[t][r] + less;
+          const float next = none ? -INFINITY : fmaxf(as_was, top - now + (ev - kLift));
+          const float f = ex2(less), fo = none ? 1.f : ex2(as_was - next);
+          m[t][r] = now, dv[t][r] = next;
           l[t][r] *= f;
 #pragma unroll
           for (int i2 = 0; i2 < kSteps; ++i2) o[t][i2][r] *= fo, o[t][i2][r + 2] *= fo;
@@ -429,8 +433,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       for (int j = 0; j < 4; ++j) {
         const int r = j & 1;
         // (no key yet: every power is 2^-inf = 0)
-        l[t][r] += ex2(s[t][j] - (m[t][r] == -INFINITY ? 0.f : m[t][r]));
-        x[j] = ex2(s[t][j] + (mo[t][r] == -INFINITY ? 0.f : ev - mo[t][r]));
+        const bool none = m[t][r] == -INFINITY;
+        const float u = s[t][j] - (none ? 0.f : m[t][r]);
+        l[t][r] += ex2(u);
+        x[j] = ex2(u + (none ? 0.f : ev - dv[t][r]));
       }
       // the product takes f16: its powers round here, those of the sum do not
       pb[t][0] = transposed(pack_f16(x[0], x[1]));
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int rr = t * 8 + 2 * c + r;
-      if (g == 0) stats[warp][rr] = make_float4(m[t][r], l[t][r], mo[t][r], saw >> (2 * t + r) & 1u ? 1.f : 0.f);
+      if (g == 0) stats[warp][rr] = make_float4(m[t][r], l[t][r], dv[t][r], saw >> (2 * t + r) & 1u ? 1.f : 0.f);
       float* dst = jo + rr * (HD + 4) + g * (HD / 8);
 #pragma unroll
       for (int i = 0; i < kSteps; i += 2)
@@ -507,8 +513,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
       sum += ex2(st.x - ref) * st.y;
       any |= st.w != 0.f;
       if (st.z == -INFINITY) continue;  // nothing was summed
-      // (the lift apart: with it 2^(mo - m) of the smallest scale would be subnormal)
-      const float f = exp2f(st.z + kLift - ref);
+      // (the lift apart: with it 2^dv of the smallest scale would be subnormal)
+      const float f = exp2f(st.x - ref + (st.z + kLift));
       float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm) + (w * kTile + rr) * (HD + 4) + d * 4);
       constexpr float kLower = 1.f / (1 << static_cast<int>(kLift));
       v.x *= kLower, v.y *= kLower, v.z *= kLower, v.w *= kLower;

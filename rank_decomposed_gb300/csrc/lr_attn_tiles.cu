@@ -1270,9 +1270,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               x = ex2(x);
               y = ex2(y);
               part[g] = at % kPage == 0 ? pack2(x, y) : add2(part[g], pack2(x, y));
-              // the product takes 16-bit floats: the powers round here, their sum does not
+              // The product takes 16-bit floats: the powers round here, their sum does not.  (Of
+              // scores over 2^23, whose rounding is a half and more, some would pass f16's largest.)
               if (Q8)
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
+                asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
               else
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y), "f"(x));
             }

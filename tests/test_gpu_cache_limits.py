@@ -94,3 +94,61 @@ def test_padding_rows_behind_a_prefix_of_several_tiles(kernel, hd, nh, nkv, lens
     assert int(b.status.item()) == 0
     assert not out[b.m:].any()
     close(out[:b.m], *b.want(), f32=True, eight=eight)
+
+
+LARGE = [16, 19, 21]      # scores under 2^22 on every kernel; by rows of all sizes
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("qs", [None, [40, 1, 70]])
+@pytest.mark.parametrize("size", LARGE + [24, 28, 40])
+def test_one_key_takes_all_among_large_scores(kernel, size, qs, hd):
+    """Scores of some 2^size, in natural units, and a key whose score is far above the others': its values, whatever the
+    scales of its page and of others are.  (A power of two times a code, and once f16's half step.)"""
+    if size not in LARGE and kernel != 1:
+        pytest.skip("by rows only")
+    b = Cached(55, 8, 2, hd, 90, [64, 160, 320], qs=qs)
+    g = torch.Generator().manual_seed(size)
+    codes = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g).float().to(F8).view(torch.uint8).cuda()  # noqa: E731
+    b.q.fill_(0)
+    q, k, v = b.q.view(b.m, 8, hd), *(x.view(torch.uint8).view(b.pages, 16, 2, hd) for x in (b.k8, b.v8))
+    q[:, :, 0] = 2.0 ** (size - 8)
+    k.zero_()
+    k[..., 0] = codes(1, 200, b.pages, 16, 2)
+    v.copy_(codes(-400, 400, *v.shape))
+    first = int(b.prefix_blocks[2])                       # a token of the prefix, which every row sees
+    k[first, 7, :, 0] = int(torch.tensor(256.0).to(F8).view(torch.uint8))
+    b.ks.fill_(1.0)
+    b.vs.copy_(torch.exp2(torch.randint(-6, 6, (b.pages, 2), generator=g).float()).cuda())
+    b.vs[first] = torch.tensor([2.0 ** -6, 2.0 ** 5], device="cuda")
+    out = torch.empty(b.m, 8 * hd, device="cuda")
+    b.run(out=out, scale=0.9)
+    assert int(b.status.item()) == 0
+    want = (b.v8.view(b.pages, 16, 2, hd)[first, 7].float() * b.vs[first][:, None]).double().repeat_interleave(4, 0).view(1, -1)
+    assert torch.all((out.double() - want).abs() <= 2.0 ** -10 * want.abs())
+
+
+@pytest.mark.parametrize("qs", [None, [40, 1, 70]])
+@pytest.mark.parametrize("size", LARGE + [24, 28, 40])
+def test_scores_that_differ_by_little_beside_their_size(kernel, size, qs):
+    """Maxima lag behind by what the reference allows.  Results are averages of the values all the same."""
+    if size not in LARGE and kernel != 1:
+        pytest.skip("by rows only")
+    b = Cached(54, 8, 2, 128, 90, [64, 160, 320], qs=qs)
+    g = torch.Generator().manual_seed(size)
+    rand = lambda n, *shape: torch.randint(0, n, shape, generator=g).cuda()  # noqa: E731
+    code = lambda x: int(torch.tensor(x).to(F8).view(torch.uint8))  # noqa: E731
+    b.q.fill_(0)
+    q, k, v = b.q.view(b.m, 8, 128), *(x.view(torch.uint8).view(b.pages, 16, 2, 128) for x in (b.k8, b.v8))
+    q[:, :, 0], q[:, :, 1] = 2.0 ** (size - 8), 1.0
+    k.zero_()
+    k[..., 0] = code(256.0)
+    k[..., 1] = torch.arange(0.0, 24.0).to(F8).view(torch.uint8).cuda()[rand(24, b.pages, 16, 2)]
+    v[:] = code(448.0)
+    b.ks.fill_(1.0)
+    b.vs.copy_(torch.exp2(rand(3, b.pages, 2).float()))
+    out = torch.empty(b.m, 1024, device="cuda")
+    b.run(out=out, scale=0.9)
+    assert int(b.status.item()) == 0
+    got = _f64(out)
+    assert np.all(got >= 448 * (1 - 2.0 ** -10)) and np.all(got <= 448 * 4 * (1 + 2.0 ** -10))
